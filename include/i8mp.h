@@ -185,6 +185,7 @@ i8mp_status i8mp_int8_mm_dequant(const int32_t* c, int64_t ldc, const float* row
  */
 #define I8MP_DTYPE_F16 0
 #define I8MP_DTYPE_F32 1
+#define I8MP_DTYPE_BF16 2 /* the 4-bit key/value cache only */
 i8mp_status i8mp_int8_vectorwise_dequant(const int8_t* q, int64_t ldq, int64_t m, int64_t k,
                                          const float* absmax, int32_t out_dtype, void* out, int64_t ldout,
                                          hipStream_t stream);
@@ -406,6 +407,115 @@ i8mp_status i8mp_fp4_dequantize(const uint8_t* codes, int64_t ldc, int64_t n, in
 i8mp_status i8mp_fp4_linear(const void* x, int64_t m, int64_t k, int64_t ldx, const uint8_t* codes, int64_t ldc,
                             const float* absmax, const uint8_t* c8, const float* s2, int64_t n, const void* bias,
                             void* out, int64_t ldout, hipStream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* A 4-bit key/value cache and the attention that reads it.  Keys and values
+ * are held in the 4-bit weights' number format: E2M1 codes in blocks of 64 along
+ * the head dimension, 4.25 bits an element.  A block's absmax A is one of the
+ * 16-bit numbers it was taken from, so the cache keeps it in that type, unrounded.
+ *  - code = sign bit of x | magnitude code of the E2M1 value nearest to
+ *    fl32(|x| * fl32(6 * fl32(1 / A))), ties to the even mantissa bit, saturating
+ *    at 6 (two roundings make the factor here, one in i8mp_fp4_quantize: a value
+ *    at a tie can fall the other way);
+ *  - x' = fl32(E2M1 value * fl32(A / 6));
+ *  - a NaN counts as a zero when a block is quantized; a block with an infinity
+ *    reads back as NaN.
+ *
+ * The cache is paged: data is uint8 [pages][kv_heads][slab], one slab holding
+ * page_size tokens of one head in four parts (D = head_dim = 64 NB):
+ *   K codes   32 NB bytes a token: [4 groups g][NB blocks b][8 bytes], the bytes
+ *             holding dims 64 b + 16 g + 0..15
+ *   V codes   128 NB bytes per 4 tokens: [16 groups m][NB blocks b][tokens 0, 2,
+ *             1, 3][2 bytes], the bytes holding dims 64 b + 4 m + 0..3
+ *   K scales  [page_size][NB] absmax in the cache's type, then V scales likewise
+ * with the even element in a byte's low nibble: 68 NB bytes a token.  A slot is
+ * page * page_size + the token's place in the page.
+ */
+typedef struct i8mp_fp4_cache {
+    void* data;         /* device, 16-byte aligned, i8mp_fp4_cache_bytes() bytes   */
+    int64_t pages;      /* >= 1, < 2^31                                           */
+    int32_t kv_heads;   /* >= 1, <= 65535                                         */
+    int32_t page_size;  /* tokens of a page: 16, 32, 64, 128 or 256                */
+    int32_t head_dim;   /* 64, 128 or 256                                         */
+    int32_t dtype;      /* I8MP_DTYPE_F16 or I8MP_DTYPE_BF16: the type of the keys,
+                           values, queries and outputs beside the cache           */
+} i8mp_fp4_cache;
+
+/* Host.  Bytes of the cache's data; 0 if a field other than data is out of range. */
+size_t i8mp_fp4_cache_bytes(const i8mp_fp4_cache* cache /* host */);
+
+/* Quantizes and writes one token's keys and values per slot.
+ *   k, v    [tokens x kv_heads x head_dim] in the cache's type: ldk, ldv elements
+ *           from token to token, hsk, hsv from head to head, unit stride within
+ *           a head; 16-byte aligned with strides that are multiples of 8
+ *   slots   int64 [tokens] (device).  A slot outside [0, pages * page_size) is
+ *           skipped (-1 marks padding).  The slots of a call are distinct: where
+ *           two tokens name one slot, it is undefined which parts of it are whose.
+ * tokens >= 0.  Nothing but the named slots is read or written. */
+i8mp_status i8mp_fp4_cache_write(const i8mp_fp4_cache* cache /* host */, const void* k, int64_t ldk, int64_t hsk,
+                                 const void* v, int64_t ldv, int64_t hsv, const int64_t* slots, int64_t tokens,
+                                 hipStream_t stream);
+
+/* Reads slots back: k, v [tokens x kv_heads x head_dim] outputs in out_dtype
+ * (I8MP_DTYPE_F16, _F32 or _BF16, rounded once from the fp32 x'), strides and
+ * alignment as for the write (for fp32 strides that are multiples of 4).  A slot
+ * outside the cache reads as zeros. */
+i8mp_status i8mp_fp4_cache_read(const i8mp_fp4_cache* cache /* host */, const int64_t* slots, int64_t tokens,
+                                int32_t out_dtype, void* k, int64_t ldk, int64_t hsk, void* v, int64_t ldv,
+                                int64_t hsv, hipStream_t stream);
+
+/* Attention of query rows over the cached tokens of their sequences.  Sequence b
+ * has length L = lengths[b] tokens in the cache, the last of which are its queries'
+ * own: query i of its n is at position p = L - n + i.  Its token j is at place
+ * j % page_size of page table[b][j / page_size].  For every query head h, with
+ * kv head h / (q_heads / kv_heads):
+ *   s_j   = scale * sum_d q[d] k'[j, d]
+ *   s_j   = softcap * tanh(s_j / softcap)              if softcap > 0
+ *   s_j   = s_j - alibi[h] * |p - j|                   if alibi is given
+ *   lse   = log sum_j e^s_j,  out[d] = sum_j e^(s_j - lse) v'[j, d]
+ * over the visible tokens: j < L and (j < prefix[b], or j <= p and, where
+ * window > 0, p - j < window).  prefix names tokens at a sequence's start that
+ * every query sees: a prompt without causal order, or the first tokens kept in
+ * sight beside a window.  A row that sees nothing (L = 0, or a query before the
+ * first token) gets zeros and lse = -inf.  Sums, maxima and the softmax are fp32;
+ * the weights e^s, times a block's A, are rounded once to the 16-bit type for the
+ * product with the E2M1 values.
+ *
+ * What is read on the device is bounded there: lengths are taken into [0, max_len],
+ * query offsets into [0, tokens], a sequence's queries past max_q are left out, and
+ * tokens on a page outside [0, pages) are not visible.  Tokens past a sequence's
+ * length may hold anything. */
+typedef struct i8mp_fp4_attention {
+    const void* q;            /* [tokens x q_heads x head_dim], strides ldq, hsq     */
+    int64_t ldq, hsq;
+    void* out;                /* the same shape, strides ldo, hso                    */
+    int64_t ldo, hso;         /* all four multiples of 8, q and out 16-byte aligned  */
+    float* lse;               /* optional fp32 [tokens x q_heads]                    */
+    const int32_t* table;     /* [batch x ldt] page ids, table_cols of them a row    */
+    int64_t ldt;
+    int32_t table_cols;
+    const int32_t* lengths;   /* [batch]                                            */
+    const int32_t* q_offsets; /* optional [batch + 1], ascending: sequence b has q rows
+                                 [q_offsets[b], q_offsets[b + 1]); NULL: max_q each  */
+    const float* alibi;       /* optional fp32 [q_heads]                             */
+    const int32_t* prefix;    /* optional [batch]                                    */
+    int64_t tokens;           /* rows of q                                          */
+    int32_t batch;
+    int32_t q_heads;          /* a multiple of kv_heads                              */
+    int32_t max_q;            /* most queries of a sequence, >= 1                    */
+    int32_t max_len;          /* bound on the lengths, <= table_cols * page_size     */
+    int32_t window;           /* 0: none                                            */
+    float scale;
+    float softcap;            /* 0: none                                            */
+} i8mp_fp4_attention;
+
+/* Host.  Workspace of a call with these sizes (its pointers are not looked at): 0
+ * if none is needed or a size is out of range. */
+size_t i8mp_fp4_attention_workspace_bytes(const i8mp_fp4_cache* cache /* host */,
+                                          const i8mp_fp4_attention* call /* host */);
+
+i8mp_status i8mp_fp4_cache_attention(const i8mp_fp4_cache* cache /* host */, const i8mp_fp4_attention* call /* host */,
+                                     void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,8 @@ import torch
 from ._lib import (  # noqa: F401
     EXPORTS,
     BackwardWorkspaceLayout,
+    Fp4AttentionStruct,
+    Fp4CacheStruct,
     I8MP_MAX_K,
     I8MP_NOALLOC_SCRATCH_BYTES,
     I8mpError,
@@ -51,6 +53,10 @@ __all__ = [
     "fp4_double_quant",
     "fp4_dequantize",
     "fp4_linear",
+    "Fp4Cache",
+    "fp4_cache_write",
+    "fp4_cache_read",
+    "fp4_cache_attention",
     "I8mpError",
 ]
 
@@ -602,3 +608,163 @@ def fp4_linear(x: torch.Tensor, fw: Fp4Weight, bias: Optional[torch.Tensor] = No
               "i8mp_fp4_linear")
     return out
 
+
+_DTYPE_CODE = {torch.float16: 0, torch.float32: 1, torch.bfloat16: 2}
+
+
+@dataclass
+class Fp4Cache:
+    """A paged 4-bit key/value cache: ``data`` uint8 [pages, kv_heads, slab] in the
+    layout of include/i8mp.h (``create`` allocates it), pages of ``page_size``
+    tokens, beside keys, values and queries of ``dtype`` (fp16 or bfloat16).
+    Slot ``page * page_size + i`` is place i of a page."""
+
+    data: torch.Tensor
+    page_size: int
+    head_dim: int
+    dtype: torch.dtype = torch.float16
+
+    @classmethod
+    def create(cls, pages: int, kv_heads: int, head_dim: int, page_size: int = 64,
+               dtype: torch.dtype = torch.float16, device="cuda") -> "Fp4Cache":
+        nbytes = page_size * (head_dim + 4 * (head_dim // 64))
+        cache = cls(torch.zeros((pages, kv_heads, nbytes), dtype=torch.uint8, device=device), page_size, head_dim, dtype)
+        cache.struct()
+        return cache
+
+    @property
+    def pages(self) -> int:
+        return self.data.shape[0]
+
+    @property
+    def kv_heads(self) -> int:
+        return self.data.shape[1]
+
+    def struct(self) -> Fp4CacheStruct:
+        """The C form, after checking the fields."""
+        if self.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError(f"a cache's dtype is torch.float16 or torch.bfloat16, got {self.dtype}")
+        d = self.data
+        if d.dtype != torch.uint8 or d.dim() != 3 or not d.is_contiguous():
+            raise ValueError("data must be a contiguous uint8 [pages, kv_heads, slab] tensor")
+        c = Fp4CacheStruct(d.data_ptr(), d.shape[0], d.shape[1], self.page_size, self.head_dim, _DTYPE_CODE[self.dtype])
+        if d.shape[2] != self.page_size * (self.head_dim + 4 * (self.head_dim // 64)) or \
+                lib().i8mp_fp4_cache_bytes(ctypes.byref(c)) != d.numel():
+            raise ValueError("data, page_size (16 to 256, a power of two) and head_dim (64, 128 or 256) do not go together")
+        return c
+
+
+def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, heads: Optional[int], head_dim: int) -> Tuple[int, int]:
+    """Token and head strides of a [tokens, heads, head_dim] tensor with unit stride within a head."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != head_dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, {head_dim}]")
+    ld, hs, unit = t.stride()
+    if unit != 1:
+        raise ValueError(f"{name} must have unit stride within a head")
+    # the stride of an axis of one element is never taken: any that the library accepts will do
+    return (ld if shape[0] > 1 else max(ld, shape[1] * head_dim)), (hs if shape[1] > 1 else head_dim)
+
+
+def fp4_cache_write(cache: Fp4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
+    """Quantizes k and v [tokens, kv_heads, head_dim] into the cache's slots (int64 [tokens], distinct).
+
+    A slot outside the cache (-1) is skipped."""
+    dev = _device_of(cache.data, k, v, slots)
+    c = cache.struct()
+    ldk, hsk = _heads(k, "k", cache.dtype, c.kv_heads, c.head_dim)
+    ldv, hsv = _heads(v, "v", cache.dtype, c.kv_heads, c.head_dim)
+    n = k.shape[0]
+    if v.shape[0] != n:
+        raise ValueError("k and v differ in tokens")
+    _vec(slots, "slots", torch.int64, n)
+    with torch.cuda.device(dev):
+        check(lib().i8mp_fp4_cache_write(ctypes.byref(c), k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv,
+                                         slots.data_ptr(), n, _stream(dev)),
+              "i8mp_fp4_cache_write")
+
+
+def fp4_cache_read(cache: Fp4Cache, slots: torch.Tensor, dtype: Optional[torch.dtype] = None
+                   ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(k, v) [tokens, kv_heads, head_dim] held at the slots, as the cache's type or ``dtype``
+    (fp16, bfloat16 or fp32).  A slot outside the cache reads as zeros."""
+    dtype = cache.dtype if dtype is None else dtype
+    if dtype not in _DTYPE_CODE:
+        raise ValueError("dtype must be torch.float16, torch.bfloat16 or torch.float32")
+    dev = _device_of(cache.data, slots)
+    c = cache.struct()
+    n = slots.shape[0]
+    _vec(slots, "slots", torch.int64, n)
+    k = torch.empty((n, c.kv_heads, c.head_dim), dtype=dtype, device=dev)
+    v = torch.empty_like(k)
+    ld, hs = c.kv_heads * c.head_dim, c.head_dim
+    with torch.cuda.device(dev):
+        check(lib().i8mp_fp4_cache_read(ctypes.byref(c), slots.data_ptr(), n, _DTYPE_CODE[dtype], k.data_ptr(), ld, hs,
+                                        v.data_ptr(), ld, hs, _stream(dev)),
+              "i8mp_fp4_cache_read")
+    return k, v
+
+
+def fp4_cache_attention(q: torch.Tensor, cache: Fp4Cache, table: torch.Tensor, lengths: torch.Tensor,
+                        q_offsets: Optional[torch.Tensor] = None, max_q: Optional[int] = None,
+                        max_len: Optional[int] = None, scale: Optional[float] = None, window: int = 0,
+                        softcap: float = 0.0, alibi: Optional[torch.Tensor] = None,
+                        prefix: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                        return_lse: bool = False, workspace: Optional[torch.Tensor] = None):
+    """Attention of q [tokens, q_heads, head_dim] over the 4-bit cache: out, or (out, lse fp32 [tokens, q_heads]).
+
+    ``lengths`` int32 [batch] counts each sequence's cached tokens, its queries' own
+    included (write them first); ``table`` int32 [batch, n] names its pages.  The rows
+    of q are ``max_q`` queries a sequence (default: tokens / batch), or, with
+    ``q_offsets`` int32 [batch + 1], rows q_offsets[b] .. q_offsets[b + 1] (``max_q``
+    then bounds them; default: tokens).  Query i of n is at position lengths - n + i
+    and sees tokens up to it, within ``window`` (0: all), and the first ``prefix``
+    (int32 [batch]) tokens.  ``softcap`` > 0 caps scores by a tanh; ``alibi`` (fp32
+    [q_heads]) subtracts alibi * distance.  ``scale`` defaults to head_dim ** -0.5,
+    ``max_len`` (a bound on the lengths) to the table's width.  A row that sees
+    nothing is zeros, its lse -inf.  ``workspace``: uint8, reused by the caller
+    (default: allocated here)."""
+    dev = _device_of(q, cache.data, table, lengths, q_offsets, alibi, prefix, out, workspace)
+    c = cache.struct()
+    ldq, hsq = _heads(q, "q", cache.dtype, None, c.head_dim)
+    tokens, q_heads = q.shape[:2]
+    batch = lengths.shape[0]
+    _vec(lengths, "lengths", torch.int32, batch)
+    ldt = _rowmajor(table, "table", torch.int32)
+    cols = table.shape[1]
+    if table.shape[0] != batch:
+        raise ValueError("table and lengths differ in sequences")
+    if q_offsets is not None:
+        _vec(q_offsets, "q_offsets", torch.int32, batch + 1)
+    if alibi is not None:
+        _vec(alibi, "alibi", torch.float32, q_heads)
+    if prefix is not None:
+        _vec(prefix, "prefix", torch.int32, batch)
+    if max_q is None:
+        max_q = tokens if q_offsets is not None else tokens // max(batch, 1)
+    if q_offsets is None and max_q * batch != tokens:
+        raise ValueError("without q_offsets every sequence has max_q queries: tokens must be batch * max_q")
+    if out is None:
+        out = torch.empty((tokens, q_heads, c.head_dim), dtype=cache.dtype, device=dev)
+    ldo, hso = _heads(out, "out", cache.dtype, q_heads, c.head_dim)
+    if out.shape[0] != tokens:
+        raise ValueError("out has the wrong shape")
+    lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=dev) if return_lse else None
+    call = Fp4AttentionStruct(
+        q.data_ptr(), ldq, hsq, out.data_ptr(), ldo, hso, None if lse is None else lse.data_ptr(), table.data_ptr(), ldt,
+        cols, lengths.data_ptr(), None if q_offsets is None else q_offsets.data_ptr(),
+        None if alibi is None else alibi.data_ptr(), None if prefix is None else prefix.data_ptr(), tokens, batch,
+        q_heads, max(max_q, 1), cols * cache.page_size if max_len is None else max_len, window,
+        c.head_dim ** -0.5 if scale is None else scale, softcap)
+    L = lib()
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = L.i8mp_fp4_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(call))
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        check(L.i8mp_fp4_cache_attention(ctypes.byref(c), ctypes.byref(call),
+                                         None if workspace is None else workspace.data_ptr(),
+                                         0 if workspace is None else workspace.numel(), _stream(dev)),
+              "i8mp_fp4_cache_attention")
+    return out if lse is None else (out, lse)

@@ -42,6 +42,11 @@ EXPORTS = (
     "i8mp_fp4_double_quant",
     "i8mp_fp4_dequantize",
     "i8mp_fp4_linear",
+    "i8mp_fp4_cache_bytes",
+    "i8mp_fp4_cache_write",
+    "i8mp_fp4_cache_read",
+    "i8mp_fp4_attention_workspace_bytes",
+    "i8mp_fp4_cache_attention",
 )
 
 
@@ -77,6 +82,44 @@ class BackwardWorkspaceLayout(Structure):
         ("xts_offset", c_size_t),
         ("scratch_offset", c_size_t),
         ("scratch_bytes", c_size_t),
+    ]
+
+
+class Fp4CacheStruct(Structure):
+    _fields_ = [
+        ("data", c_void_p),
+        ("pages", c_int64),
+        ("kv_heads", c_int32),
+        ("page_size", c_int32),
+        ("head_dim", c_int32),
+        ("dtype", c_int32),
+    ]
+
+
+class Fp4AttentionStruct(Structure):
+    _fields_ = [
+        ("q", c_void_p),
+        ("ldq", c_int64),
+        ("hsq", c_int64),
+        ("out", c_void_p),
+        ("ldo", c_int64),
+        ("hso", c_int64),
+        ("lse", c_void_p),
+        ("table", c_void_p),
+        ("ldt", c_int64),
+        ("table_cols", c_int32),
+        ("lengths", c_void_p),
+        ("q_offsets", c_void_p),
+        ("alibi", c_void_p),
+        ("prefix", c_void_p),
+        ("tokens", c_int64),
+        ("batch", c_int32),
+        ("q_heads", c_int32),
+        ("max_q", c_int32),
+        ("max_len", c_int32),
+        ("window", c_int32),
+        ("scale", c_float),
+        ("softcap", c_float),
     ]
 
 
@@ -151,6 +194,19 @@ def _declare(lib):
     lib.i8mp_fp4_linear.argtypes = [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_void_p,
                                     c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p]
     lib.i8mp_fp4_linear.restype = c_int32
+    cache = POINTER(Fp4CacheStruct)
+    lib.i8mp_fp4_cache_bytes.argtypes = [cache]
+    lib.i8mp_fp4_cache_bytes.restype = c_size_t
+    lib.i8mp_fp4_cache_write.argtypes = [cache, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_void_p,
+                                         c_int64, c_void_p]
+    lib.i8mp_fp4_cache_write.restype = c_int32
+    lib.i8mp_fp4_cache_read.argtypes = [cache, c_void_p, c_int64, c_int32, c_void_p, c_int64, c_int64, c_void_p,
+                                        c_int64, c_int64, c_void_p]
+    lib.i8mp_fp4_cache_read.restype = c_int32
+    lib.i8mp_fp4_attention_workspace_bytes.argtypes = [cache, POINTER(Fp4AttentionStruct)]
+    lib.i8mp_fp4_attention_workspace_bytes.restype = c_size_t
+    lib.i8mp_fp4_cache_attention.argtypes = [cache, POINTER(Fp4AttentionStruct), c_void_p, c_size_t, c_void_p]
+    lib.i8mp_fp4_cache_attention.restype = c_int32
 
 
 def lib():

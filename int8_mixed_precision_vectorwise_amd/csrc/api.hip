@@ -2,12 +2,14 @@
 // layout, launch sequencing.  Nothing here allocates, synchronizes or reads
 // device memory; every launch goes to the caller's stream.
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
 #include "common.h"
 #include "backward.h"
 #include "fp4.h"
+#include "kvcache.h"
 
 using namespace i8mp;
 
@@ -109,7 +111,7 @@ const char* i8mp_status_string(i8mp_status s) {
     }
 }
 
-int32_t i8mp_abi_version(void) { return (3 << 16) | 0; }
+int32_t i8mp_abi_version(void) { return (3 << 16) | 1; }
 
 size_t i8mp_quant_workspace_bytes(int64_t m, int64_t k) {
     if (m <= 0 || k < 1 || k > I8MP_MAX_K) return 0;
@@ -713,6 +715,137 @@ i8mp_status i8mp_fp4_linear(const void* x, int64_t m, int64_t k, int64_t ldx, co
     a.n = n;
     a.k = k;
     return launched(launch_fp4_linear(a, stream));
+}
+
+namespace {
+bool half_type(int32_t dtype) { return dtype == I8MP_DTYPE_F16 || dtype == I8MP_DTYPE_BF16; }
+
+// the internal form of a cache, if its fields are in range (data is not looked at)
+bool kv_cache(const i8mp_fp4_cache* c, KvCache* k) {
+    if (!c || c->pages < 1 || c->pages > INT32_MAX || c->kv_heads < 1 || c->kv_heads > 65535) return false;
+    int shift = 4;
+    while (shift <= 8 && (1 << shift) != c->page_size) ++shift;
+    if (shift > 8) return false;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return false;
+    if (!half_type(c->dtype)) return false;
+    k->data = static_cast<uint8_t*>(c->data);
+    k->pages = c->pages;
+    k->heads = c->kv_heads;
+    k->page_size = c->page_size;
+    k->page_shift = shift;
+    k->blocks = c->head_dim / 64;
+    k->bf16 = c->dtype == I8MP_DTYPE_BF16;
+    return true;
+}
+
+// strides of [tokens x heads x head_dim] in elements, multiples of `unit`
+bool kv_strides(int64_t ld, int64_t hs, const i8mp_fp4_cache* c, int unit) {
+    return ld >= c->head_dim && hs >= c->head_dim && ld % unit == 0 && hs % unit == 0;
+}
+
+// the internal form of an attention call, if its sizes are in range
+bool kv_call(const i8mp_fp4_cache* cache, const i8mp_fp4_attention* p, KvAttnArgs* a) {
+    if (!kv_cache(cache, &a->c) || !p) return false;
+    if (p->tokens < 0 || p->tokens > INT32_MAX || p->batch < 0 || p->max_q < 1 || p->window < 0 || p->max_len < 0)
+        return false;
+    if (p->q_heads < 1 || p->q_heads > 65535 || p->q_heads % cache->kv_heads) return false;
+    if (p->max_len > (1 << 30) || p->max_q > (1 << 30) || p->table_cols < 0 || p->ldt < p->table_cols) return false;
+    if (p->max_len > (int64_t)p->table_cols * cache->page_size) return false;
+    if (!std::isfinite(p->scale) || !(p->softcap >= 0.0f) || !std::isfinite(p->softcap)) return false;
+    if (!p->q_offsets && p->tokens != (int64_t)p->batch * p->max_q) return false;
+    if (!kv_strides(p->ldq, p->hsq, cache, 8) || !kv_strides(p->ldo, p->hso, cache, 8)) return false;
+    a->q = static_cast<const half_bits*>(p->q);
+    a->ldq = p->ldq;
+    a->hsq = p->hsq;
+    a->out = static_cast<half_bits*>(p->out);
+    a->ldo = p->ldo;
+    a->hso = p->hso;
+    a->lse = p->lse;
+    a->table = p->table;
+    a->ldt = p->ldt;
+    a->table_cols = p->table_cols;
+    a->lengths = p->lengths;
+    a->q_offsets = p->q_offsets;
+    a->alibi = p->alibi;
+    a->prefix = p->prefix;
+    a->batch = p->batch;
+    a->q_heads = p->q_heads;
+    a->group = p->q_heads / cache->kv_heads;
+    a->max_q = p->max_q;
+    a->window = p->window;
+    a->tokens = p->tokens;
+    a->scale = p->scale;
+    a->softcap = p->softcap;
+    a->max_len = p->max_len;
+    return true;
+}
+}  // namespace
+
+size_t i8mp_fp4_cache_bytes(const i8mp_fp4_cache* cache) {
+    KvCache c{};
+    if (!kv_cache(cache, &c)) return 0;
+    return (size_t)c.pages * c.heads * c.slab();
+}
+
+i8mp_status i8mp_fp4_cache_write(const i8mp_fp4_cache* cache, const void* k, int64_t ldk, int64_t hsk, const void* v,
+                                 int64_t ldv, int64_t hsv, const int64_t* slots, int64_t tokens, hipStream_t stream) {
+    KvMoveArgs a{};
+    if (!kv_cache(cache, &a.c) || tokens < 0) return I8MP_EINVAL;
+    if (!kv_strides(ldk, hsk, cache, 8) || !kv_strides(ldv, hsv, cache, 8)) return I8MP_EINVAL;
+    if (tokens == 0) return I8MP_OK;
+    if (!a.c.data || !k || !v || !slots || !aligned16(a.c.data) || !aligned16(k) || !aligned16(v)) return I8MP_EINVAL;
+    if (i8mp_status s = check_device(); s != I8MP_OK) return s;
+    a.slots = slots;
+    a.tokens = tokens;
+    a.k = const_cast<void*>(k);
+    a.ldk = ldk;
+    a.hsk = hsk;
+    a.v = const_cast<void*>(v);
+    a.ldv = ldv;
+    a.hsv = hsv;
+    return launched(launch_kv_write(a, stream));
+}
+
+i8mp_status i8mp_fp4_cache_read(const i8mp_fp4_cache* cache, const int64_t* slots, int64_t tokens, int32_t out_dtype,
+                                void* k, int64_t ldk, int64_t hsk, void* v, int64_t ldv, int64_t hsv,
+                                hipStream_t stream) {
+    KvMoveArgs a{};
+    if (!kv_cache(cache, &a.c) || tokens < 0) return I8MP_EINVAL;
+    if (!half_type(out_dtype) && out_dtype != I8MP_DTYPE_F32) return I8MP_EINVAL;
+    const int unit = out_dtype == I8MP_DTYPE_F32 ? 4 : 8;
+    if (!kv_strides(ldk, hsk, cache, unit) || !kv_strides(ldv, hsv, cache, unit)) return I8MP_EINVAL;
+    if (tokens == 0) return I8MP_OK;
+    if (!a.c.data || !k || !v || !slots || !aligned16(a.c.data) || !aligned16(k) || !aligned16(v)) return I8MP_EINVAL;
+    if (i8mp_status s = check_device(); s != I8MP_OK) return s;
+    a.slots = slots;
+    a.tokens = tokens;
+    a.out_dtype = out_dtype;
+    a.k = k;
+    a.ldk = ldk;
+    a.hsk = hsk;
+    a.v = v;
+    a.ldv = ldv;
+    a.hsv = hsv;
+    return launched(launch_kv_read(a, stream));
+}
+
+size_t i8mp_fp4_attention_workspace_bytes(const i8mp_fp4_cache* cache, const i8mp_fp4_attention* call) {
+    KvAttnArgs a{};
+    if (!kv_call(cache, call, &a) || a.batch == 0 || a.tokens == 0) return 0;
+    return kv_attention_workspace(a);
+}
+
+i8mp_status i8mp_fp4_cache_attention(const i8mp_fp4_cache* cache, const i8mp_fp4_attention* call, void* workspace,
+                                     size_t workspace_bytes, hipStream_t stream) {
+    KvAttnArgs a{};
+    if (!kv_call(cache, call, &a)) return I8MP_EINVAL;
+    if (a.batch == 0 || a.tokens == 0) return I8MP_OK;
+    if (!a.c.data || !a.q || !a.out || !a.lengths || (a.table_cols > 0 && !a.table)) return I8MP_EINVAL;
+    if (!aligned16(a.c.data) || !aligned16(a.q) || !aligned16(a.out)) return I8MP_EINVAL;
+    const size_t need = kv_attention_workspace(a);
+    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return I8MP_EWORKSPACE;
+    if (i8mp_status s = check_device(); s != I8MP_OK) return s;
+    return launched(launch_kv_attention(a, workspace, stream));
 }
 
 }  // extern "C"
