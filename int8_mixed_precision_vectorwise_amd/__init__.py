@@ -610,6 +610,9 @@ def fp4_linear(x: torch.Tensor, fw: Fp4Weight, bias: Optional[torch.Tensor] = No
 
 
 _DTYPE_CODE = {torch.float16: 0, torch.float32: 1, torch.bfloat16: 2}
+_CACHE_CODE = {torch.float16: 0, torch.bfloat16: 2}
+# the handle of a device's current stream, without a Stream object around it (2 us a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 @dataclass
@@ -629,7 +632,8 @@ class Fp4Cache:
                dtype: torch.dtype = torch.float16, device="cuda") -> "Fp4Cache":
         nbytes = page_size * (head_dim + 4 * (head_dim // 64))
         cache = cls(torch.zeros((pages, kv_heads, nbytes), dtype=torch.uint8, device=device), page_size, head_dim, dtype)
-        cache.struct()
+        if lib().i8mp_fp4_cache_bytes(ctypes.byref(cache.struct())) == 0:
+            raise ValueError("a cache has page_size 16, 32, 64, 128 or 256 and head_dim 64, 128 or 256")
         return cache
 
     @property
@@ -641,17 +645,27 @@ class Fp4Cache:
         return self.data.shape[1]
 
     def struct(self) -> Fp4CacheStruct:
-        """The C form, after checking the fields."""
-        if self.dtype not in (torch.float16, torch.bfloat16):
-            raise TypeError(f"a cache's dtype is torch.float16 or torch.bfloat16, got {self.dtype}")
+        """The C form, after checking that the fields go together (the library checks their ranges)."""
         d = self.data
+        dtype = _CACHE_CODE.get(self.dtype)
+        if dtype is None:
+            raise TypeError(f"a cache's dtype is torch.float16 or torch.bfloat16, got {self.dtype}")
         if d.dtype != torch.uint8 or d.dim() != 3 or not d.is_contiguous():
             raise ValueError("data must be a contiguous uint8 [pages, kv_heads, slab] tensor")
-        c = Fp4CacheStruct(d.data_ptr(), d.shape[0], d.shape[1], self.page_size, self.head_dim, _DTYPE_CODE[self.dtype])
-        if d.shape[2] != self.page_size * (self.head_dim + 4 * (self.head_dim // 64)) or \
-                lib().i8mp_fp4_cache_bytes(ctypes.byref(c)) != d.numel():
-            raise ValueError("data, page_size (16 to 256, a power of two) and head_dim (64, 128 or 256) do not go together")
-        return c
+        pages, heads, slab = d.shape
+        if slab != self.page_size * (self.head_dim + 4 * (self.head_dim // 64)):
+            raise ValueError("data's last axis must be page_size * (head_dim + head_dim / 16) bytes")
+        return Fp4CacheStruct(d.data_ptr(), pages, heads, self.page_size, self.head_dim, dtype)
+
+
+def _run(dev: torch.device, what: str, *args) -> None:
+    """Calls a library entry point on dev with its current stream as the last argument."""
+    f = getattr(lib(), what)
+    if dev.index == torch.cuda.current_device():
+        check(f(*args, _raw_stream(dev.index)), what)
+    else:
+        with torch.cuda.device(dev):
+            check(f(*args, _raw_stream(dev.index)), what)
 
 
 def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, heads: Optional[int], head_dim: int) -> Tuple[int, int]:
@@ -680,10 +694,8 @@ def fp4_cache_write(cache: Fp4Cache, k: torch.Tensor, v: torch.Tensor, slots: to
     if v.shape[0] != n:
         raise ValueError("k and v differ in tokens")
     _vec(slots, "slots", torch.int64, n)
-    with torch.cuda.device(dev):
-        check(lib().i8mp_fp4_cache_write(ctypes.byref(c), k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv,
-                                         slots.data_ptr(), n, _stream(dev)),
-              "i8mp_fp4_cache_write")
+    _run(dev, "i8mp_fp4_cache_write", ctypes.byref(c), k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv,
+         slots.data_ptr(), n)
 
 
 def fp4_cache_read(cache: Fp4Cache, slots: torch.Tensor, dtype: Optional[torch.dtype] = None
@@ -700,10 +712,8 @@ def fp4_cache_read(cache: Fp4Cache, slots: torch.Tensor, dtype: Optional[torch.d
     k = torch.empty((n, c.kv_heads, c.head_dim), dtype=dtype, device=dev)
     v = torch.empty_like(k)
     ld, hs = c.kv_heads * c.head_dim, c.head_dim
-    with torch.cuda.device(dev):
-        check(lib().i8mp_fp4_cache_read(ctypes.byref(c), slots.data_ptr(), n, _DTYPE_CODE[dtype], k.data_ptr(), ld, hs,
-                                        v.data_ptr(), ld, hs, _stream(dev)),
-              "i8mp_fp4_cache_read")
+    _run(dev, "i8mp_fp4_cache_read", ctypes.byref(c), slots.data_ptr(), n, _DTYPE_CODE[dtype], k.data_ptr(), ld, hs,
+         v.data_ptr(), ld, hs)
     return k, v
 
 
@@ -758,13 +768,9 @@ def fp4_cache_attention(q: torch.Tensor, cache: Fp4Cache, table: torch.Tensor, l
         None if alibi is None else alibi.data_ptr(), None if prefix is None else prefix.data_ptr(), tokens, batch,
         q_heads, max(max_q, 1), cols * cache.page_size if max_len is None else max_len, window,
         c.head_dim ** -0.5 if scale is None else scale, softcap)
-    L = lib()
-    with torch.cuda.device(dev):
-        if workspace is None:
-            need = L.i8mp_fp4_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(call))
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        check(L.i8mp_fp4_cache_attention(ctypes.byref(c), ctypes.byref(call),
-                                         None if workspace is None else workspace.data_ptr(),
-                                         0 if workspace is None else workspace.numel(), _stream(dev)),
-              "i8mp_fp4_cache_attention")
+    if workspace is None:
+        need = lib().i8mp_fp4_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(call))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _run(dev, "i8mp_fp4_cache_attention", ctypes.byref(c), ctypes.byref(call),
+         None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
     return out if lse is None else (out, lse)

@@ -87,11 +87,12 @@ __device__ inline Seq sequence(const KvAttnArgs& a, int b) {
     q1 = q1 < q0 ? q0 : (q1 > a.tokens ? a.tokens : q1);
     s.row0 = q0;
     s.q_len = (int)(q1 - q0 > a.max_q ? a.max_q : q1 - q0);
+    const int n = (int)(q1 - q0);
     const int64_t most = a.max_len;
     int64_t len = a.lengths[b];
     len = len < 0 ? 0 : (len > most ? most : len);
     s.length = (int)len;
-    s.past = s.length - s.q_len;
+    s.past = s.length - n;
     const int pre = a.prefix ? a.prefix[b] : 0;
     s.prefix = pre < 0 ? 0 : (pre > s.length ? s.length : pre);
     return s;
@@ -119,162 +120,387 @@ __device__ inline Span span_of(const Seq& s, int i0, int i1, int window) {
     return r;
 }
 
-// A tile's share of one lane (row r = lane % 16, group g = lane / 16), as loaded.
-template <int NB>
-struct KeyTile {
-    uint32_t k[2][NB * 2];   // keys 16 u + r: group g's dims, 8 bytes a block
-    uint32_t v[2][NB * 2];   // values of keys 16 u + 4 g .. + 3: dims 64 b + 4 r .. + 3
-    uint32_t ks[2][NB * 2];  // scales of keys 16 u + 4 g .. + 3
-    uint32_t vs[2][NB * 2];
-    bool live[2];            // the page id was in range
+// A segment, one kv head of one row tile with n key tiles, is cut into this many
+// parts, nearly equal, each for one workgroup (at least one part: rows that see
+// nothing still get their zeros).
+__device__ inline int parts_of(const KvAttnArgs& a, int n) {
+    const int p = (n + a.chunk_tiles - 1) / a.chunk_tiles;
+    return p < 1 ? 1 : p;
+}
+
+// First token of tile n of a span.
+__device__ inline int tile_token(const Span& span, int n) { return (n < span.head ? n : n - span.head + span.low) * kTile; }
+
+// Where the two halves (16 keys each) of a tile lie.  kOne: pages hold at least a
+// tile, so both are on one page, the second right behind the first.
+template <bool kOne>
+struct Place {
+    const uint8_t* codes[kOne ? 1 : 2];   // slab + the keys' K codes
+    const uint8_t* scales[kOne ? 1 : 2];  // slab + the keys' place among the scales
+    bool live[kOne ? 1 : 2];              // the page id was in range
 };
 
-template <int N>
-__device__ inline void load_words(uint32_t (&d)[N], const uint8_t* p) {
-    if constexpr (N % 4 == 0) {
+// The pages of up to 64 of a wave's tiles, n, n + kWaves, ...: lane i loads those of
+// the i-th, so that a tile's address later takes a lane read and no load.
+template <bool kOne>
+struct Pages {
+    int32_t id[kOne ? 1 : 2];
+};
+
+template <bool kOne>
+__device__ inline Pages<kOne> load_pages(const KvAttnArgs& a, const int32_t* table, const Span& span, int n, int n1,
+                                         int length, int lane) {
+    Pages<kOne> p;
+    const int nn = n + lane * kWaves;
+    const int t0 = tile_token(span, nn < n1 ? nn : n);
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const uint4 x = reinterpret_cast<const uint4*>(p)[i];
-            d[4 * i] = x.x;
-            d[4 * i + 1] = x.y;
-            d[4 * i + 2] = x.z;
-            d[4 * i + 3] = x.w;
+    for (int u = 0; u < (kOne ? 1 : 2); ++u) {
+        const int t = t0 + 16 * u;
+        p.id[u] = table[(t < length ? t : length - 1) >> a.c.page_shift];  // past the end: the last page, masked
+        // waited for here: else the compiler, which sees a load on one path only, waits for
+        // every DMA before each lane read
+        asm volatile("" : "+v"(p.id[u]));
+    }
+    return p;
+}
+
+template <int NB, bool kOne>
+__device__ inline Place<kOne> place_of(const KvAttnArgs& a, const Pages<kOne>& pages, int slot, int h, int t0) {
+    Place<kOne> w;
+    const uint32_t slab = (uint32_t)a.c.page_size * (68 * NB);
+#pragma unroll
+    for (int u = 0; u < (kOne ? 1 : 2); ++u) {
+        const int32_t id = __builtin_amdgcn_readlane(pages.id[u], slot);
+        w.live[u] = (uint32_t)id < (uint32_t)a.c.pages;
+        const uint8_t* base = a.c.data + (uint64_t)((w.live[u] ? (uint32_t)id : 0u) * (uint64_t)a.c.heads + (uint32_t)h) * slab;
+        const uint32_t at = (uint32_t)(t0 + 16 * u) & (uint32_t)(a.c.page_size - 1);
+        w.codes[u] = base + at * 32 * NB;
+        w.scales[u] = base + at * 2 * NB;
+    }
+    return w;
+}
+
+// A tile in LDS: K codes (1024 NB bytes, 32 NB a key), V codes (the same), then for
+// each half the scales of K and of V (32 NB bytes each).  A DMA instruction moves 16
+// bytes a lane (codes) or 4 (scales, and the codes of a half that has only 512 bytes).
+template <int NB, bool kOne>
+struct Stage {
+    static constexpr int kScales = 2048 * NB;
+    static constexpr int kBytes = kScales + (NB == 4 ? 512 : 256);
+    static constexpr int kIns = (kOne || NB > 1 ? 2 * NB : 8) + (kOne ? (NB == 4 ? 2 : 1) : 2);
+};
+
+__device__ inline __amdgpu_buffer_rsrc_t slab_rsrc(const uint8_t* base) {  // every access is inside the slab
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), (short)0, 0x7fffffff, 0x00020000);
+}
+__device__ inline void dma16(__amdgpu_buffer_rsrc_t src, uint8_t* lds, uint32_t offset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)lds, 16, (int)offset, 0, 0, 0);
+}
+__device__ inline void dma4(__amdgpu_buffer_rsrc_t src, uint8_t* lds, uint32_t offset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)lds, 4, (int)offset, 0, 0, 0);
+}
+
+// Requests a tile; lane i's bytes land at i times their size from the place given.  `v`
+// is where the V codes are behind the K codes, `s` the lane's scale bytes behind theirs.
+template <int NB, bool kOne>
+__device__ inline void request(const Place<kOne>& w, uint8_t* lds, int lane, uint32_t v, const uint32_t (&s)[2]) {
+#pragma unroll
+    for (int u = 0; u < (kOne ? 1 : 2); ++u) {
+        const __amdgpu_buffer_rsrc_t codes = slab_rsrc(w.codes[u]), scales = slab_rsrc(w.scales[u]);
+        constexpr int kHalf = kOne ? 1024 * NB : 512 * NB;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {  // K, V
+            uint8_t* to = lds + x * 1024 * NB + u * kHalf;
+            const uint32_t from = x ? v : 0;
+            if constexpr (kHalf >= 1024) {
+#pragma unroll
+                for (int o = 0; o < kHalf; o += 1024) dma16(codes, to + o, from + o + lane * 16);
+            } else {
+#pragma unroll
+                for (int o = 0; o < kHalf; o += 256) dma4(codes, to + o, from + o + lane * 4);
+            }
         }
-    } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(p);
-        d[0] = x.x;
-        d[1] = x.y;
+        if (kOne) {
+            dma4(scales, lds + Stage<NB, kOne>::kScales, s[0]);
+            if (NB == 4) dma4(scales, lds + Stage<NB, kOne>::kScales + 256, s[1]);
+        } else if (lane < 16 * NB) {
+            dma4(scales, lds + Stage<NB, kOne>::kScales + u * 64 * NB, s[0]);
+        }
     }
 }
 
-template <int NB>
-__device__ inline void load_tile(const KvAttnArgs& a, const int32_t* table, int h, int t0, int length, int lane,
-                                 KeyTile<NB>& kt) {
-    const int r = lane & 15, g = lane >> 4;
-    const int P = a.c.page_size;
+template <int n>
+__device__ inline void wait_loads() {  // all but the n newest
+    asm volatile("s_waitcnt vmcnt(%0)" ::"i"(n) : "memory");
+}
+
+// A tile's share of one lane, codes and scales of its two halves, out of LDS: K codes
+// at k, V codes at v, K scales at s and V scales 32 NB bytes behind, the second halves
+// 512 NB (codes) and 64 NB bytes behind the first.  Instructions of their own, with
+// their wait: for an LDS read of its own the compiler waits for every DMA under way.
+typedef unsigned v2u __attribute__((ext_vector_type(2)));
+
+__device__ inline void read_share(uint32_t (&kc)[2][2], uint32_t (&vc)[2][2], uint32_t (&ks)[2][2], uint32_t (&vs)[2][2],
+                                  uint32_t k, uint32_t v, uint32_t s) {
+    v2u r[8];
+    asm volatile(
+        "ds_read_b64 %0, %8\n ds_read_b64 %1, %8 offset:512\n"
+        "ds_read_b64 %2, %9\n ds_read_b64 %3, %9 offset:512\n"
+        "ds_read_b64 %4, %10\n ds_read_b64 %5, %10 offset:64\n"
+        "ds_read_b64 %6, %10 offset:32\n ds_read_b64 %7, %10 offset:96\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]), "=&v"(r[6]), "=&v"(r[7])
+        : "v"(k), "v"(v), "v"(s)
+        : "memory");
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        int t = t0 + 16 * u;
-        t = t < length ? t : (length - 1) & ~15;        // past the end: the last page again, masked
-        const int64_t id = table[t >> a.c.page_shift];
-        kt.live[u] = id >= 0 && id < a.c.pages;
-        const uint8_t* slab = a.c.data + ((kt.live[u] ? id : 0) * a.c.heads + h) * a.c.slab();
-        const int at = t & (P - 1);
-        load_words(kt.k[u], slab + (at + r) * 32 * NB + g * 8 * NB);
-        load_words(kt.v[u], slab + P * 32 * NB + ((at >> 2) + g) * 128 * NB + r * 8 * NB);
-        load_words(kt.ks[u], slab + P * 64 * NB + (at + 4 * g) * 2 * NB);
-        load_words(kt.vs[u], slab + P * 66 * NB + (at + 4 * g) * 2 * NB);
-    }
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            kc[u][i] = r[u][i];
+            vc[u][i] = r[2 + u][i];
+            ks[u][i] = r[4 + u][i];
+            vs[u][i] = r[6 + u][i];
+        }
 }
 
-// 16-bit scale of block b of the i-th of a lane's four tokens
+__device__ inline void read_share(uint32_t (&kc)[2][4], uint32_t (&vc)[2][4], uint32_t (&ks)[2][4], uint32_t (&vs)[2][4],
+                                  uint32_t k, uint32_t v, uint32_t s) {
+    v4u r[8];
+    asm volatile(
+        "ds_read_b128 %0, %8\n ds_read_b128 %1, %8 offset:1024\n"
+        "ds_read_b128 %2, %9\n ds_read_b128 %3, %9 offset:1024\n"
+        "ds_read_b128 %4, %10\n ds_read_b128 %5, %10 offset:128\n"
+        "ds_read_b128 %6, %10 offset:64\n ds_read_b128 %7, %10 offset:192\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]), "=&v"(r[6]), "=&v"(r[7])
+        : "v"(k), "v"(v), "v"(s)
+        : "memory");
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            kc[u][i] = r[u][i];
+            vc[u][i] = r[2 + u][i];
+            ks[u][i] = r[4 + u][i];
+            vs[u][i] = r[6 + u][i];
+        }
+}
+
+__device__ inline void read_share(uint32_t (&kc)[2][8], uint32_t (&vc)[2][8], uint32_t (&ks)[2][8], uint32_t (&vs)[2][8],
+                                  uint32_t k, uint32_t v, uint32_t s) {
+    v4u r[16];
+    asm volatile(
+        "ds_read_b128 %0, %16\n ds_read_b128 %1, %16 offset:16\n"
+        "ds_read_b128 %2, %16 offset:2048\n ds_read_b128 %3, %16 offset:2064\n"
+        "ds_read_b128 %4, %17\n ds_read_b128 %5, %17 offset:16\n"
+        "ds_read_b128 %6, %17 offset:2048\n ds_read_b128 %7, %17 offset:2064\n"
+        "ds_read_b128 %8, %18\n ds_read_b128 %9, %18 offset:16\n"
+        "ds_read_b128 %10, %18 offset:256\n ds_read_b128 %11, %18 offset:272\n"
+        "ds_read_b128 %12, %18 offset:128\n ds_read_b128 %13, %18 offset:144\n"
+        "ds_read_b128 %14, %18 offset:384\n ds_read_b128 %15, %18 offset:400\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(r[0]), "=&v"(r[1]), "=&v"(r[2]), "=&v"(r[3]), "=&v"(r[4]), "=&v"(r[5]), "=&v"(r[6]), "=&v"(r[7]),
+          "=&v"(r[8]), "=&v"(r[9]), "=&v"(r[10]), "=&v"(r[11]), "=&v"(r[12]), "=&v"(r[13]), "=&v"(r[14]), "=&v"(r[15])
+        : "v"(k), "v"(v), "v"(s)
+        : "memory");
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            kc[u][i] = r[2 * u + i / 4][i % 4];
+            vc[u][i] = r[4 + 2 * u + i / 4][i % 4];
+            ks[u][i] = r[8 + 2 * u + i / 4][i % 4];
+            vs[u][i] = r[12 + 2 * u + i / 4][i % 4];
+        }
+}
+
+// The scale of block b of the i-th of a lane's four keys
 template <bool kBf16, int NB>
 __device__ inline float scale_at(const uint32_t (&w)[NB * 2], int i, int b) {
     const int j = i * NB + b;
-    return Half<kBf16>::wide((w[j >> 1] >> (16 * (j & 1))) & 0xffffu);
+    if (kBf16) return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+    return Half<false>::wide((w[j >> 1] >> (16 * (j & 1))) & 0xffffu);
 }
 
 // One workgroup: one sequence, kv head, row tile of 16 query rows (token-major,
-// then the heads of the group) and a run of key tiles.  S^T = K Q^T leaves a
-// lane with 4 keys x 2 of one query column, which is the layout that P^T needs
-// as the second operand of O^T = V^T P^T, so P never moves between lanes.
-template <bool kBf16, int NB>
-__global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs a) {
+// then the heads of the group) and a run of key tiles.  S^T = K Q^T leaves a lane
+// with 4 keys of each half tile and one query column, which is the layout that P^T
+// needs as the second operand of O^T = V^T P^T, so P never moves between lanes.
+// Tiles come through a ring of kRing stages of LDS for each wave, filled by DMA: a
+// tile is read into registers whole and its stage requested anew before the products.
+// kScored: scores get a cap, a distance term or a factor of 0 (else a factor alone,
+// which then rides on the exponential's argument).
+template <int NB>
+constexpr int kWorkgroups() { return NB == 4 ? 2 : 4; }  // of a CU
+template <int NB>
+constexpr int kRing() { return NB == 1 ? 4 : 2; }
+
+template <bool kBf16, int NB, bool kOne, bool kScored>
+__global__ __launch_bounds__(64 * kWaves, kWorkgroups<NB>()) void kv_attention_kernel(KvAttnArgs a) {
     typedef Half<kBf16> H;
     typedef typename H::v8 v8;
+    typedef Stage<NB, kOne> St;
+    constexpr int R = kRing<NB>();
+    // one LDS array: the waves' rings, later their sums [wave][row][64 NB + 4] and maxima
+    // (a second object would make the compiler wait for every DMA before an LDS read)
+    constexpr int kPart = kWaves * kRows * (64 * NB + 4) * 4, kRings = kWaves * R * St::kBytes;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[(kPart > kRings ? kPart : kRings) + kWaves * kRows * 8];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
-    int64_t id = blockIdx.x;
-    const int chunk = (int)(id % a.chunks);
-    id /= a.chunks;
-    const int h = (int)(id % a.c.heads);
-    id /= a.c.heads;
-    const int rt = (int)(id % a.row_tiles);
-    const int b = (int)(id / a.row_tiles);
+    // part-major: the later parts, which shorter sequences lack, come last
+    uint32_t id = blockIdx.x;
+    const uint32_t segments = (uint32_t)a.batch * (uint32_t)a.row_tiles * (uint32_t)a.c.heads;
+    const int chunk = (int)(id / segments);
+    id -= chunk * segments;
+    const uint32_t segment = id;
+    const int h = (int)(id % (uint32_t)a.c.heads);
+    id /= (uint32_t)a.c.heads;
+    const int rt = (int)(id % (uint32_t)a.row_tiles);
+    const int b = (int)(id / (uint32_t)a.row_tiles);
     const Seq s = sequence(a, b);
     const int rows = s.q_len * a.group;
     const int r0 = rt * kRows;
     if (r0 >= rows) return;
     const int r1 = r0 + kRows < rows ? r0 + kRows : rows;
-    const Span span = span_of(s, r0 / a.group, (r1 - 1) / a.group, a.window);
-    const int n0 = chunk * a.chunk_tiles;
-    if (chunk > 0 && n0 >= span.n) return;
-    const int n1 = n0 + a.chunk_tiles < span.n ? n0 + a.chunk_tiles : span.n;
+    const int i0 = r0 / a.group, i1 = (r1 - 1) / a.group;
+    const Span span = span_of(s, i0, i1, a.window);
+    const int parts = parts_of(a, span.n);
+    if (chunk >= parts) return;
+    const int n0 = (int)((int64_t)span.n * chunk / parts), n1 = (int)((int64_t)span.n * (chunk + 1) / parts);
 
     const int row = r0 + c;
     const bool live_row = row < rows;
     const int qi = live_row ? row / a.group : 0;
-    const int head = h * a.group + (live_row ? row % a.group : 0);
+    const int head = h * a.group + (live_row ? row - qi * a.group : 0);
     const int pos = s.past + qi;
     // this row sees keys [0, see_pre) and [see_lo, pos]
     const int see_pre = pos >= 0 ? s.prefix : 0;
     const int see_lo = a.window > 0 ? pos - a.window + 1 : 0;
-    const int pos0 = s.past + r0 / a.group, pos1 = s.past + (r1 - 1) / a.group;
-    const float slope = a.alibi ? a.alibi[head] * kLog2e : 0.0f;
+    const int pos0 = s.past + i0, pos1 = s.past + i1;
+
+    const int32_t* table = a.table + (int64_t)b * a.ldt;
+    const uint32_t P = (uint32_t)a.c.page_size;
+    const uint32_t at_v = P * 32 * NB;                        // V codes behind the K codes
+    uint32_t at_s[2];                                         // the lane's scale bytes behind their place
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t o = (lane + 64 * i) * 4 & (128 * NB - 1), half = o / (64 * NB), kv = o / (32 * NB) & 1;
+        at_s[i] = P * 64 * NB + kv * P * 2 * NB + half * 32 * NB + (o & (32 * NB - 1));
+    }
+    uint8_t* ring = smem + wave * R * St::kBytes;
+    const uint32_t ring_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)ring;
+    Pages<kOne> pages;
+    uint32_t live = 0;                                        // bits 2 i, 2 i + 1: the halves of the i-th next tile are live
+    int first = n0 + wave;
+    // requests tile n into a stage, `place` tiles ahead of the one in use
+    const auto ask = [&](int n, int stage, int place) {
+        int slot = (n - first) / kWaves;
+        const Place<kOne> w = place_of<NB, kOne>(a, pages, slot, h, tile_token(span, n));
+        live |= ((uint32_t)w.live[0] | (uint32_t)w.live[kOne ? 0 : 1] << 1) << (2 * place);
+        request<NB, kOne>(w, ring + stage * St::kBytes, lane, at_v, at_s);
+    };
+    const int last = n0 + wave + (n1 - 1 - n0 - wave) / kWaves * kWaves;  // the wave's last tile, if it has any
+    if (first < n1) {
+        pages = load_pages<kOne>(a, table, span, first, n1, s.length, lane);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (first + i * kWaves <= last) ask(first + i * kWaves, i, i);
+    }
+
     const half_bits* qrow = a.q + (s.row0 + qi) * a.ldq + head * a.hsq;
+    // a factor below 0 is taken into q's sign
+    const uint32_t flip = !kScored && a.scale < 0.0f ? 0x80008000u : 0u;
     v8 q[NB][2];
 #pragma unroll
     for (int bb = 0; bb < NB; ++bb)
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
-            const uint4 x = live_row ? *reinterpret_cast<const uint4*>(qrow + 64 * bb + 16 * g + 8 * st)
-                                     : make_uint4(0, 0, 0, 0);
+            uint4 x = live_row ? *reinterpret_cast<const uint4*>(qrow + 64 * bb + 16 * g + 8 * st) : make_uint4(0, 0, 0, 0);
+            x = make_uint4(x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip);
             q[bb][st] = __builtin_bit_cast(v8, x);
         }
+    const float slope = kScored && a.alibi ? a.alibi[head] * kLog2e : 0.0f;
 
-    // s in units of log2 e: without a cap the factor goes onto the block scales
-    const float pre = a.scale / 6.0f * (a.softcap > 0.0f ? 1.0f : kLog2e);
-    const int32_t* table = a.table + (int64_t)b * a.ldt;
-    float m = -INFINITY, l = 0.0f;
+    // a score is x * unit, in units of log2 e
+    const float unit = kScored ? 1.0f : fabsf(a.scale) / 6.0f * kLog2e;
+    float m = -INFINITY, l = 0.0f;   // largest x, and the sum of this lane's weights
     v4f acc[NB][4];
 #pragma unroll
     for (int bb = 0; bb < NB; ++bb)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[bb][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-    for (int n = n0 + wave; n < n1; n += kWaves) {
-        const int t0 = (n < span.head ? n : n - span.head + span.low) * kTile;
-        KeyTile<NB> kt;
-        load_tile<NB>(a, table, h, t0, s.length, lane, kt);
-        float sc[2][4];
-        // every key of the tile visible to every row: no masks
-        const bool whole = kt.live[0] & kt.live[1] & (pos0 >= 0) &
-                           ((t0 + kTile <= s.prefix) |
-                            ((t0 + kTile - 1 <= pos0) & ((a.window == 0) | (pos1 - t0 < a.window))));
+    int stage = 0;
+    for (int n = first; n < n1; n += kWaves) {
+        const int t0 = tile_token(span, n);
+        const bool live0 = live & 1, live1 = live & 2;
+        live >>= 2;
+        uint32_t kc[2][NB * 2];  // keys 16 u + c: group g's dims, 8 bytes a block
+        uint32_t ks[2][NB * 2];  // scales of keys 16 u + 4 g .. + 3
+        uint32_t vc[2][NB * 2];  // values of keys 16 u + 4 g .. + 3: dims 64 b + 4 c .. + 3
+        uint32_t vs[2][NB * 2];
+        if (n + (R - 1) * kWaves <= last)
+            wait_loads<(R - 1) * St::kIns>();  // the tiles requested after it stay in flight
+        else
+            wait_loads<0>();
+        {
+            const uint32_t st = ring_at + stage * St::kBytes;
+            read_share(kc, vc, ks, vs, st + (c * 32 + g * 8) * NB, st + 1024 * NB + (g * 128 + c * 8) * NB,
+                       st + St::kScales + g * 8 * NB);
+            const int nn = n + R * kWaves;
+            if (nn <= last) {
+                if ((nn - first) / kWaves >= 64) {
+                    first = nn;
+                    pages = load_pages<kOne>(a, table, span, first, n1, s.length, lane);
+                }
+                ask(nn, stage, R - 1);
+            }
+            stage = stage + 1 < R ? stage + 1 : 0;
+        }
+        float x[2][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             v4f p[NB];
 #pragma unroll
             for (int bb = 0; bb < NB; ++bb) {
-                p[bb] = H::mfma(codes8<kBf16>(kt.k[u][2 * bb]), q[bb][0], v4f{0.0f, 0.0f, 0.0f, 0.0f});
-                p[bb] = H::mfma(codes8<kBf16>(kt.k[u][2 * bb + 1]), q[bb][1], p[bb]);
+                p[bb] = H::mfma(codes8<kBf16>(kc[u][2 * bb]), q[bb][0], v4f{0.0f, 0.0f, 0.0f, 0.0f});
+                p[bb] = H::mfma(codes8<kBf16>(kc[u][2 * bb + 1]), q[bb][1], p[bb]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float x = p[0][i] * (scale_at<kBf16, NB>(kt.ks[u], i, 0) * pre);
+                x[u][i] = p[0][i] * scale_at<kBf16, NB>(ks[u], i, 0);
 #pragma unroll
-                for (int bb = 1; bb < NB; ++bb) x = fmaf(p[bb][i], scale_at<kBf16, NB>(kt.ks[u], i, bb) * pre, x);
-                sc[u][i] = x;
+                for (int bb = 1; bb < NB; ++bb) x[u][i] = fmaf(p[bb][i], scale_at<kBf16, NB>(ks[u], i, bb), x[u][i]);
             }
         }
-        if (a.softcap > 0.0f) {
-            const float inv = 2.0f * kLog2e / a.softcap, cap = a.softcap * kLog2e;
+        if (kScored) {
+            const float f = a.scale / 6.0f;
+            if (a.softcap > 0.0f) {
+                const float arg = 2.0f * kLog2e * f / a.softcap, cap = a.softcap * kLog2e;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // tanh y = 1 - 2 / (1 + e^2y)
+                        const float e = __builtin_amdgcn_exp2f(x[u][i] * arg);
+                        x[u][i] = fmaf(__builtin_amdgcn_rcpf(1.0f + e), -2.0f * cap, cap);
+                    }
+            } else {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[u][i] *= f * kLog2e;
+            }
+            const float away = (float)(pos - t0 - 4 * g);
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {  // tanh x = (1 - e^-2|x|) / (1 + e^-2|x|), with x's sign
-                    const float e = __builtin_amdgcn_exp2f(-fabsf(sc[u][i]) * inv);
-                    sc[u][i] = copysignf(cap * (1.0f - e) / (1.0f + e), sc[u][i]);
-                }
+                for (int i = 0; i < 4; ++i) x[u][i] = fmaf(-slope, fabsf(away - (float)(16 * u + i)), x[u][i]);
         }
-        if (a.alibi) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sc[u][i] = fmaf(-slope, fabsf((float)(pos - (t0 + 16 * u + 4 * g + i))), sc[u][i]);
-        }
+        // every key of the tile visible to every row: no masks
+        const bool whole = live0 & live1 & (pos0 >= 0) &
+                           ((t0 + kTile <= s.prefix) |
+                            ((t0 + kTile - 1 <= pos0) & ((a.window == 0) | (pos1 - t0 < a.window))));
         if (!whole) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
@@ -283,18 +509,26 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs
                     const int j = t0 + 16 * u + 4 * g + i;
                     // bitwise, so that this is compares and a select: short circuits became
                     // branches, and among them the compiler lost a copy of a score
-                    const bool see = ((j < see_pre) | ((j >= see_lo) & (j <= pos))) & kt.live[u];
-                    sc[u][i] = see ? sc[u][i] : -INFINITY;
+                    const bool see = ((j < see_pre) | ((j >= see_lo) & (j <= pos))) & (u ? live1 : live0);
+                    x[u][i] = see ? x[u][i] : -INFINITY;
+                    // a masked key's value may be no number, and so may what a page holds past
+                    // a sequence's end: its scales are taken as 0 in this lane, which has this
+                    // row alone
+#pragma unroll
+                    for (int bb = 0; bb < NB; ++bb) {
+                        const int w = i * NB + bb;
+                        vs[u][w >> 1] = see ? vs[u][w >> 1] : vs[u][w >> 1] & (w & 1 ? 0xffffu : 0xffff0000u);
+                    }
                 }
         }
         float top = m;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[u][i]);
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, x[u][i]);
         top = column_max(top);
         if (__ballot(top > m)) {
-            const float drop = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+            const float drop = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((m - top) * unit);
             l *= drop;
 #pragma unroll
             for (int bb = 0; bb < NB; ++bb)
@@ -302,27 +536,23 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs
                 for (int j = 0; j < 4; ++j) acc[bb][j] *= drop;
             m = top;
         }
-        const float base = m == -INFINITY ? 0.0f : m;  // nothing seen yet: e^-inf below stays 0
+        const float base = m == -INFINITY ? 0.0f : m * unit;  // nothing seen yet: 2^-inf below stays 0
         float w[2][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                w[u][i] = __builtin_amdgcn_exp2f(sc[u][i] - base);
+                w[u][i] = __builtin_amdgcn_exp2f(kScored ? x[u][i] - base : fmaf(x[u][i], unit, -base));
                 l += w[u][i];
             }
-        // P A, rounded to the 16-bit type: like the output, one rounding of it.  A
-        // masked key's scale may be anything, so its product is replaced.
+        // P A, rounded to the 16-bit type: like the output, one rounding of it
         v8 pa[NB];
 #pragma unroll
         for (int bb = 0; bb < NB; ++bb)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float y = w[u][i] * scale_at<kBf16, NB>(kt.vs[u], i, bb);
-                    pa[bb][4 * u + i] = (typename H::T)(whole || sc[u][i] != -INFINITY ? y : 0.0f);
-                }
+                for (int i = 0; i < 4; ++i) pa[bb][4 * u + i] = (typename H::T)(w[u][i] * scale_at<kBf16, NB>(vs[u], i, bb));
         // V^T: a word holds two tokens' dims 0 .. 3; pairing the words' nibbles makes
         // bytes (token 0, token 1) and (token 2, token 3) of one dim
 #pragma unroll
@@ -330,7 +560,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs
             uint32_t ev[2], od[2];  // dims 0 and 2, dims 1 and 3
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const uint32_t wa = kt.v[u][2 * bb], wb = kt.v[u][2 * bb + 1];
+                const uint32_t wa = vc[u][2 * bb], wb = vc[u][2 * bb + 1];
                 ev[u] = (wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u);
                 od[u] = ((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u);
             }
@@ -347,131 +577,211 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_attention_kernel(KvAttnArgs
             }
         }
     }
+    m = m == -INFINITY ? m : m * unit;
 
     // join the waves: O^T row 4 g + i of acc[bb][j] is dim 64 bb + 4 (4 g + i) + j
-    __shared__ float part[kWaves][kRows][64 * NB + 4];
-    __shared__ float ml[kWaves][kRows][2];
     l = column_sum(l);
+    wait_loads<0>();
+    __syncthreads();  // every wave's DMA has landed: the rings are free
+    float (*part)[kRows][64 * NB + 4] = reinterpret_cast<float (*)[kRows][64 * NB + 4]>(smem);
+    float2 (*ml)[kRows] = reinterpret_cast<float2 (*)[kRows]>(smem + sizeof(smem) - kWaves * kRows * 8);
 #pragma unroll
     for (int bb = 0; bb < NB; ++bb)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) part[wave][c][64 * bb + 4 * (4 * g + i) + j] = acc[bb][j][i];
-    if (g == 0) {
-        ml[wave][c][0] = m;
-        ml[wave][c][1] = l;
-    }
+            *reinterpret_cast<v4f*>(&part[wave][c][64 * bb + 4 * (4 * g + i)]) =
+                v4f{acc[bb][0][i], acc[bb][1][i], acc[bb][2][i], acc[bb][3][i]};
+    if (g == 0) ml[wave][c] = make_float2(m, l);
     __syncthreads();
     const int cr = tid >> 4, d0 = tid & 15;  // 16 lanes a row, 4 dims a step
     const int orow = r0 + cr;
     if (orow >= r1) return;
     float mm = -INFINITY, ll = 0.0f, f[kWaves];
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, ml[w][cr][0]);
+    for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, ml[w][cr].x);
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-        f[w] = ml[w][cr][0] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[w][cr][0] - mm);
-        ll = fmaf(ml[w][cr][1], f[w], ll);
+        f[w] = ml[w][cr].x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[w][cr].x - mm);
+        ll = fmaf(ml[w][cr].y, f[w], ll);
     }
-    const int64_t tok = s.row0 + orow / a.group;
-    const int oh = h * a.group + orow % a.group;
-    const int64_t flat = tok * a.q_heads + oh;
-    const bool last = a.chunks == 1;
-    const float norm = last ? (ll > 0.0f ? 1.0f / (6.0f * ll) : 0.0f) : 1.0f;
+    const int oi = orow / a.group;
+    const int64_t tok = s.row0 + oi;
+    const int oh = h * a.group + orow - oi * a.group;
+    const int64_t slot = ((int64_t)segment * a.chunks + chunk) * a.slot_rows + cr;
+    const float norm = parts > 1 ? 1.0f : ll > 0.0f ? 1.0f / (6.0f * ll) : 0.0f;
 #pragma unroll
     for (int bb = 0; bb < NB; ++bb) {
-        float o[4];
+        v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float x = 0.0f;
+        for (int w = 0; w < kWaves; ++w) {
+            const v4f x = *reinterpret_cast<const v4f*>(&part[w][cr][64 * bb + 4 * d0]);
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) x = fmaf(part[w][cr][64 * bb + 4 * d0 + j], f[w], x);
-            o[j] = x * norm;
+            for (int j = 0; j < 4; ++j) o[j] = fmaf(x[j], f[w], o[j]);
         }
-        if (last) {
-            typename H::T* dst = reinterpret_cast<typename H::T*>(a.out) + tok * a.ldo + oh * a.hso + 64 * bb + 4 * d0;
-            typedef typename H::T t4 __attribute__((ext_vector_type(4)));
-            *reinterpret_cast<t4*>(dst) = t4{(typename H::T)o[0], (typename H::T)o[1], (typename H::T)o[2], (typename H::T)o[3]};
+        if (parts > 1) {
+            *reinterpret_cast<v4f*>(a.part + slot * 64 * NB + 64 * bb + 4 * d0) = o;
         } else {
-            *reinterpret_cast<float4*>(a.part + (flat * a.chunks + chunk) * 64 * NB + 64 * bb + 4 * d0) =
-                make_float4(o[0], o[1], o[2], o[3]);
+            typedef typename H::T t4 __attribute__((ext_vector_type(4)));
+            typename H::T* dst = reinterpret_cast<typename H::T*>(a.out) + tok * a.ldo + oh * a.hso + 64 * bb + 4 * d0;
+            *reinterpret_cast<t4*>(dst) = t4{(typename H::T)(o[0] * norm), (typename H::T)(o[1] * norm),
+                                             (typename H::T)(o[2] * norm), (typename H::T)(o[3] * norm)};
         }
     }
     if (d0 == 0) {
-        if (!last) {
-            float* dst = a.part_ml + (flat * a.chunks + chunk) * 2;
-            dst[0] = mm;
-            dst[1] = ll;
-        } else if (a.lse) {
-            a.lse[flat] = ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+        if (parts > 1)
+            reinterpret_cast<float2*>(a.part_ml)[slot] = make_float2(mm, ll);
+        else if (a.lse)
+            a.lse[tok * a.q_heads + oh] = ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+    }
+}
+
+// Joins the parts of a segment's rows, in the order of its keys.  A workgroup takes
+// a.join_rows rows (1 to 16) of one segment: 16 lanes a row, 4 NB dims each, times
+// 16 / join_rows sets of lanes that share the parts and meet in LDS.
+template <bool kBf16, int NB>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs a) {
+    typedef Half<kBf16> H;
+    __shared__ float red[16][64 * NB + 4], red_l[16];
+    const int tid = threadIdx.x;
+    const uint32_t segment = blockIdx.x / (uint32_t)a.join_groups;
+    const int e = (int)(segment / (uint32_t)a.c.heads), h = (int)(segment % (uint32_t)a.c.heads);
+    const int b = e / a.row_tiles;
+    const Seq s = sequence(a, b);
+    const int rows = s.q_len * a.group;
+    const int t0 = (e - b * a.row_tiles) * kRows;
+    if (t0 >= rows) return;
+    const int t1 = t0 + kRows < rows ? t0 + kRows : rows;
+    const int parts = parts_of(a, span_of(s, t0 / a.group, (t1 - 1) / a.group, a.window).n);
+    if (parts < 2) return;  // written already
+    const int set = tid >> 4, d0 = tid & 15;
+    const int rr = set % a.join_rows, cl = set / a.join_rows, step = 16 / a.join_rows;
+    const int cr = (int)(blockIdx.x % (uint32_t)a.join_groups) * a.join_rows + rr, row = t0 + cr;
+    // rows past the last read the last row's parts
+    const int64_t base0 = (int64_t)segment * a.chunks * a.slot_rows + (row < t1 ? cr : t1 - 1 - t0);
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+    float m = -INFINITY, l = 0.0f;
+    v4f o[NB];
+#pragma unroll
+    for (int bb = 0; bb < NB; ++bb) o[bb] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int kAhead = NB == 4 ? 2 : 4;  // parts in flight
+    for (int w = cl; w < parts; w += step * kAhead) {
+        float2 p[kAhead];
+        v4f x[kAhead][NB];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t at = base0 + (int64_t)(w + k * step < parts ? w + k * step : w) * a.slot_rows;
+            p[k] = ml[at];
+#pragma unroll
+            for (int bb = 0; bb < NB; ++bb)
+                x[k][bb] = *reinterpret_cast<const v4f*>(a.part + at * 64 * NB + 64 * bb + 4 * d0);
+        }
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            p[k] = w + k * step < parts ? p[k] : make_float2(-INFINITY, 0.0f);
+            top = fmaxf(top, p[k].x);
+        }
+        const float base = top == -INFINITY ? 0.0f : top;
+        const float keep = __builtin_amdgcn_exp2f(m - base);
+        m = top;
+        l *= keep;
+#pragma unroll
+        for (int bb = 0; bb < NB; ++bb) o[bb] *= keep;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float f = __builtin_amdgcn_exp2f(p[k].x - base);
+            l = fmaf(p[k].y, f, l);
+#pragma unroll
+            for (int bb = 0; bb < NB; ++bb)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[bb][j] = fmaf(x[k][bb][j], f, o[bb][j]);
         }
     }
-}
-
-// Joins the chunks of a row in ascending order, one wave a row: so the result does
-// not depend on which workgroup ended first.
-template <bool kBf16, int NB>
-__global__ __launch_bounds__(64) void kv_join_kernel(KvAttnArgs a) {
-    typedef Half<kBf16> H;
-    const int lane = threadIdx.x;
-    const int64_t id = blockIdx.x;
-    const int head = (int)(id % a.q_heads);
-    const int64_t bi = id / a.q_heads;
-    const int qi = (int)(bi % a.max_q);
-    const Seq s = sequence(a, (int)(bi / a.max_q));
-    if (qi >= s.q_len) return;
-    const int row = qi * a.group + head % a.group;
-    const int r0 = row / kRows * kRows, rows = s.q_len * a.group;
-    const int r1 = r0 + kRows < rows ? r0 + kRows : rows;
-    const Span span = span_of(s, r0 / a.group, (r1 - 1) / a.group, a.window);
-    int n = (span.n + a.chunk_tiles - 1) / a.chunk_tiles;
-    n = n < 1 ? 1 : n;
-    const int64_t tok = s.row0 + qi;
-    const int64_t flat = tok * a.q_heads + head;
-    const float* ml = a.part_ml + flat * a.chunks * 2;
-    const float* part = a.part + flat * a.chunks * 64 * NB;
-    float m = -INFINITY;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, ml[2 * i]);
-    float l = 0.0f, o[NB];
+    float top = m;
+    if (step > 1) {  // the sets of a row meet: rr, rr + join_rows, ...
+        if (d0 == 0) red_l[set] = m;
+        __syncthreads();
+        for (int k = 0; k < step; ++k) top = fmaxf(top, red_l[rr + k * a.join_rows]);
+        __syncthreads();
+        const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
 #pragma unroll
-    for (int bb = 0; bb < NB; ++bb) o[bb] = 0.0f;
-    for (int i = 0; i < n; ++i) {
-        const float f = ml[2 * i] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[2 * i] - m);
-        l = fmaf(ml[2 * i + 1], f, l);
+        for (int bb = 0; bb < NB; ++bb) *reinterpret_cast<v4f*>(&red[set][64 * bb + 4 * d0]) = o[bb] * f;
+        if (d0 == 0) red_l[set] = l * f;
+        __syncthreads();
+        if (cl > 0) return;
+        l = 0.0f;
+        for (int k = 0; k < step; ++k) l += red_l[rr + k * a.join_rows];
 #pragma unroll
-        for (int bb = 0; bb < NB; ++bb) o[bb] = fmaf(part[(int64_t)i * 64 * NB + 64 * bb + lane], f, o[bb]);
+        for (int bb = 0; bb < NB; ++bb) {
+            o[bb] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int k = 0; k < step; ++k) o[bb] += *reinterpret_cast<const v4f*>(&red[rr + k * a.join_rows][64 * bb + 4 * d0]);
+        }
     }
+    if (row >= t1) return;
+    const int qi = row / a.group;
+    const int64_t tok = s.row0 + qi;
+    const int oh = h * a.group + row - qi * a.group;
     const float norm = l > 0.0f ? 1.0f / (6.0f * l) : 0.0f;
 #pragma unroll
-    for (int bb = 0; bb < NB; ++bb)
-        reinterpret_cast<typename H::T*>(a.out)[tok * a.ldo + head * a.hso + 64 * bb + lane] = (typename H::T)(o[bb] * norm);
-    if (lane == 0 && a.lse) a.lse[flat] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    for (int bb = 0; bb < NB; ++bb) {
+        typedef typename H::T t4 __attribute__((ext_vector_type(4)));
+        typename H::T* dst = reinterpret_cast<typename H::T*>(a.out) + tok * a.ldo + oh * a.hso + 64 * bb + 4 * d0;
+        *reinterpret_cast<t4*>(dst) = t4{(typename H::T)(o[bb][0] * norm), (typename H::T)(o[bb][1] * norm),
+                                         (typename H::T)(o[bb][2] * norm), (typename H::T)(o[bb][3] * norm)};
+    }
+    if (d0 == 0 && a.lse) a.lse[tok * a.q_heads + oh] = l > 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
 }
 
-// How the keys are cut: enough workgroups to fill the chip, each with at least two
-// tiles a wave.
+// How the keys are cut.  A part costs its workgroup a prologue and epilogue of about
+// 4 us and the join its sums, so there are no more parts than fill the chip once (one
+// sequence: all parts are alike) or twice (several, which may differ in length: 64
+// sequences of 2048 to 8192 tokens, 64 / 8 heads of 128, took 89 us at 0.75, 80 at 2
+// and 78 us at 4 times the chip's 1024 workgroups; equal ones 109, 113 and 116; one
+// sequence of 131072 tokens 29, 32 and 39).  Up to kWhole tiles are not cut: the
+// second launch costs more than a longer loop.
+constexpr int kWhole = 16;
+
 void plan(KvAttnArgs& a) {
     a.row_tiles = (int32_t)ceil_div((int64_t)a.max_q * a.group, kRows);
-    int64_t most = a.max_len;
-    if (a.window > 0 && !a.prefix && a.window + (int64_t)a.max_q + 2 * kTile < most) most = a.window + (int64_t)a.max_q + 2 * kTile;
-    const int64_t tiles = ceil_div(most, kTile);
-    const int64_t groups = (int64_t)a.batch * a.c.heads * a.row_tiles;
-    const int64_t want = 1024;
-    int64_t per = ceil_div(tiles * groups, want);
-    per = round_up(per < 2 * kWaves ? 2 * kWaves : per, kWaves);
+    const int64_t segments = (int64_t)a.batch * a.row_tiles * a.c.heads;
+    // keys that a row tile sees: beside a window, those of the prefix are not known here
+    int64_t near = a.max_len;
+    if (a.window > 0 && a.window + (int64_t)a.max_q + 2 * kTile < near) near = a.window + (int64_t)a.max_q + 2 * kTile;
+    const int64_t chip = 256 * (a.c.blocks == 1 ? kWorkgroups<1>() : a.c.blocks == 2 ? kWorkgroups<2>() : kWorkgroups<4>());
+    const int64_t tiles = ceil_div(near, kTile), most = ceil_div(a.prefix ? a.max_len : near, kTile);
+    int64_t per = ceil_div(tiles * segments, a.batch > 1 ? 2 * chip : chip);
+    per = per < kWaves ? kWaves : per;
+    if (most <= kWhole) per = kWhole;
     a.chunk_tiles = (int32_t)per;
-    a.chunks = (int32_t)ceil_div(tiles > 0 ? tiles : 1, per);
+    a.chunks = (int32_t)ceil_div(most > 0 ? most : 1, per);
+    const int64_t rows = (int64_t)a.max_q * a.group;
+    a.slot_rows = (int32_t)(rows < kRows ? rows : kRows);
+    a.join_rows = 1;
+    // few segments: their many parts are shared by a workgroup for each row; many: few
+    // parts each, and a workgroup takes all the rows there are
+    while (segments >= 256 && a.join_rows < a.slot_rows) a.join_rows *= 2;
+    a.join_groups = (int32_t)ceil_div(a.slot_rows, a.join_rows);
+}
+
+template <bool kBf16, int NB, bool kOne>
+void launch_main(const KvAttnArgs& a, hipStream_t stream) {
+    const dim3 grid((unsigned)((int64_t)a.batch * a.row_tiles * a.c.heads * a.chunks)), block(64 * kWaves);
+    if (a.softcap > 0.0f || a.alibi || fabsf(a.scale) < 1e-30f)
+        hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, kOne, true>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, kOne, false>), grid, block, 0, stream, a);
 }
 
 template <bool kBf16, int NB>
 hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
-    const int64_t blocks = (int64_t)a.batch * a.row_tiles * a.c.heads * a.chunks;
-    hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB>), dim3((unsigned)blocks), dim3(64 * kWaves), 0, stream, a);
+    if (a.c.page_size >= kTile)
+        launch_main<kBf16, NB, true>(a, stream);
+    else
+        launch_main<kBf16, NB, false>(a, stream);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (a.chunks > 1) {
-        const int64_t joins = (int64_t)a.batch * a.max_q * a.q_heads;
-        hipLaunchKernelGGL((kv_join_kernel<kBf16, NB>), dim3((unsigned)joins), dim3(64), 0, stream, a);
+        const int64_t joins = (int64_t)a.batch * a.row_tiles * a.c.heads * a.join_groups;
+        hipLaunchKernelGGL((kv_join_kernel<kBf16, NB>), dim3((unsigned)joins), dim3(256), 0, stream, a);
     }
     return hipGetLastError();
 }
@@ -481,15 +791,14 @@ hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
 size_t kv_attention_workspace(const KvAttnArgs& args) {
     KvAttnArgs a = args;
     plan(a);
-    if (a.chunks <= 1) return 0;
-    return (size_t)a.tokens * a.q_heads * a.chunks * (64 * a.c.blocks + 2) * 4;
+    return a.chunks == 1 ? 0 : (size_t)a.batch * a.row_tiles * a.c.heads * a.chunks * a.slot_rows * (64 * a.c.blocks + 2) * 4;
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& args, void* workspace, hipStream_t stream) {
     KvAttnArgs a = args;
     plan(a);
     a.part = static_cast<float*>(workspace);
-    a.part_ml = a.part + (a.chunks > 1 ? a.tokens * a.q_heads * a.chunks * 64 * a.c.blocks : 0);
+    a.part_ml = a.part + (a.chunks == 1 ? 0 : (int64_t)a.batch * a.row_tiles * a.c.heads * a.chunks * a.slot_rows * 64 * a.c.blocks);
     if (a.c.bf16)
         return a.c.blocks == 1 ? launch<true, 1>(a, stream) : a.c.blocks == 2 ? launch<true, 2>(a, stream) : launch<true, 4>(a, stream);
     return a.c.blocks == 1 ? launch<false, 1>(a, stream) : a.c.blocks == 2 ? launch<false, 2>(a, stream) : launch<false, 4>(a, stream);

@@ -57,10 +57,12 @@ struct KvAttnArgs {
     float scale, softcap;            // softcap 0: none
     int64_t max_len;                 // bound on the lengths
     // set by the launcher
-    int32_t chunk_tiles, chunks;     // tiles of keys per workgroup; most chunks of a row tile
     int32_t row_tiles;               // row tiles of the longest sequence
-    float* part;                     // [tokens x q_heads x chunks] partial sums, chunks > 1
-    float* part_ml;                  // [tokens x q_heads x chunks x 2]
+    int32_t chunk_tiles, chunks;     // most key tiles of a part, most parts of a segment (kv head of a row tile)
+    int32_t slot_rows;               // rows that a part leaves (up to 16)
+    int32_t join_rows, join_groups;  // rows of a workgroup of the join, its workgroups for a segment
+    float* part;                     // [segments][chunks][slot_rows][head_dim] partial sums
+    float* part_ml;                  // [segments][chunks][slot_rows][maximum, sum]
 };
 // workspace of one call (0: none needed)
 size_t kv_attention_workspace(const KvAttnArgs& a);
