@@ -57,9 +57,9 @@ struct KvAttnArgs {
     float scale, softcap;            // softcap 0: none
     int64_t max_len;                 // bound on the lengths
     // set by the launcher
-    int32_t row_tiles;               // row tiles of the longest sequence
+    int32_t tile_rows, row_tiles;    // rows of a row tile, row tiles of the longest sequence
     int32_t chunk_tiles, chunks;     // most key tiles of a part, most parts of a segment (kv head of a row tile)
-    int32_t slot_rows;               // rows that a part leaves (up to 16)
+    int32_t slot_rows;               // rows that a part leaves (up to tile_rows)
     int32_t join_rows, join_groups;  // rows of a workgroup of the join, its workgroups for a segment
     float* part;                     // [segments][chunks][slot_rows][head_dim] partial sums
     float* part_ml;                  // [segments][chunks][slot_rows][maximum, sum]
@@ -67,5 +67,6 @@ struct KvAttnArgs {
 // workspace of one call (0: none needed)
 size_t kv_attention_workspace(const KvAttnArgs& a);
 hipError_t launch_kv_attention(const KvAttnArgs& a, void* workspace, hipStream_t stream);
+hipError_t launch_kv_attention_bf16(const KvAttnArgs& a, hipStream_t stream);  // its bfloat16 part, with the cut made
 
 }  // namespace i8mp
