@@ -1,25 +1,29 @@
 // Writing 16-bit keys and values into the 4-bit cache, and reading them back.
-// The format is that of the 4-bit weights: blocks of 64, code = sign and the
-// E2M1 magnitude nearest to fl32(|x| * fl32(6 * fl32(1 / A))), A the block's absmax, and
-// x' = fl32(E2M1 value * fl32(A / 6)).  A is the absmax of 16-bit numbers and so
-// one of them: the cache keeps it in that type, 2 bytes a block, unrounded.
+// Blocks of 64 dims: code = sign and the E2M1 magnitude nearest to
+// fl32(|x| * fl32(6 * fl32(1 / A))), A the block's absmax, and x' = fl32(E2M1 value *
+// fl32(A / 6)).  A is the absmax of 16-bit numbers and so one of them: the cache keeps
+// it in that type, 2 bytes a block, unrounded.
+//
+// One lane has 8 dims of four neighbouring tokens, of K and of V: eight 16-byte loads
+// (or stores) under way, and where the four slots are one aligned group, as a prompt's
+// are, its V pieces are whole 8-byte words of the cache.  Both kernels are bound by HBM
+// where tokens are many.  The magnitudes' maximum is taken on the bits (8 lanes share a
+// block: three DPP steps), and the hardware's conversions round to codes and widen
+// them: comparing each value with the seven thresholds took 25 VALU instructions a
+// value against 5 and twice the time of the loads.
 #include "kvcache.h"
+#include "quant_util.h"
 
 namespace i8mp {
 
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kQuad = 4;   // tokens of a lane
 
-// fp32 of a 16-bit float's bits
 template <bool kBf16>
 __device__ inline float wide(uint32_t h) {
     return kBf16 ? __uint_as_float(h << 16) : h2f((half_bits)h);
-}
-
-template <bool kBf16>
-__device__ inline uint32_t narrow(float f) {  // round to nearest even
-    return kBf16 ? (uint32_t)__builtin_bit_cast(half_bits, (__bf16)f) : (uint32_t)f2h(f);
 }
 
 // E2M1 magnitude code of a non-negative fp32 value, ties to the even code; a NaN gives 0
@@ -28,137 +32,326 @@ __device__ inline uint32_t mag_code(float v) {
            (uint32_t)(v > 2.5f) + (uint32_t)(v >= 3.5f) + (uint32_t)(v > 5.0f);
 }
 
-__device__ inline float code_value(uint32_t c) {
-    const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-    const uint32_t mag = e ? (((e + 126u) << 23) | (m << 22)) : (m ? 0x3f000000u : 0u);
-    return __uint_as_float(mag | ((c & 8u) << 28));
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+
+// largest value of the 8 lanes that share a block
+__device__ inline uint32_t block_max(uint32_t v) {
+    const auto up = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+    v = up(v, (uint32_t)dpp_i32<kDppQuadSwap1>((int32_t)v));
+    v = up(v, (uint32_t)dpp_i32<kDppQuadSwap2>((int32_t)v));
+    return up(v, (uint32_t)dpp_i32<kDppHalfMirror>((int32_t)v));
 }
 
-// slab byte of the V codes of dims 4 m .. 4 m + 3 of block b, token t
-__device__ inline int v_byte(int t, int m, int b, int nb) {
-    return (t >> 2) * 128 * nb + m * 8 * nb + b * 8 + ((t & 1) * 2 + ((t >> 1) & 1)) * 2;
+// the chunk's largest magnitude, as the type's bits
+__device__ inline uint32_t chunk_top(const uint4& x) {
+    const uint32_t mag = 0x7fff7fffu;
+    us2 m = __builtin_elementwise_max(__builtin_bit_cast(us2, x.x & mag), __builtin_bit_cast(us2, x.y & mag));
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(us2, x.z & mag));
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(us2, x.w & mag));
+    return m.x > m.y ? m.x : m.y;
 }
 
-// One lane per 8 dims of one token, head and block, of K or of V: 8 lanes share
-// a block, so its absmax takes 3 shuffles.
+// The 8 codes of a lane's chunk and the bits of its block's A.  All lanes of a block call.
 template <bool kBf16>
-__global__ __launch_bounds__(kThreads) void kv_write_kernel(KvMoveArgs a) {
-    const int nb = a.c.blocks;
-    const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int part = (int)(t & 7);
-    const int64_t blk = t >> 3;
-    const int b = (int)(blk % nb);
-    const int64_t th = blk / nb;
-    const int h = (int)(th % a.c.heads);
-    const int64_t tok = th / a.c.heads;
-    if (tok >= a.tokens) return;  // 8 lanes of a block leave together
-    const int64_t slot = a.slots[tok];
-    if (slot < 0 || slot >= (a.c.pages << a.c.page_shift)) return;
-    const bool is_v = blockIdx.y != 0;
-    const half_bits* src = static_cast<const half_bits*>(is_v ? a.v : a.k) + tok * (is_v ? a.ldv : a.ldk) +
-                           h * (is_v ? a.hsv : a.hsk) + b * 64 + part * 8;
-    const uint4 x = *reinterpret_cast<const uint4*>(src);
+__device__ inline uint32_t quantize8(const uint4& x, uint32_t& a_bits) {
+    constexpr uint32_t kInf = kBf16 ? 0x7f80u : 0x7c00u;
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float f[8], mx = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        f[e] = fabsf(wide<kBf16>((w[e >> 1] >> (16 * (e & 1))) & 0xffffu));
-        mx = fmaxf(mx, f[e]);
-    }
-    mx = fmaxf(mx, __shfl_xor(mx, 1, 64));
-    mx = fmaxf(mx, __shfl_xor(mx, 2, 64));
-    mx = fmaxf(mx, __shfl_xor(mx, 4, 64));
-    const float inv = mx > 0.0f ? 6.0f * (1.0f / mx) : 0.0f;  // IEEE reciprocal
+    uint32_t top = block_max(chunk_top(x));
     uint32_t packed = 0;
+    if (top < kInf) {
+        const float mx = wide<kBf16>(top);
+        const float inv = mx > 0.0f ? 6.0f * (1.0f / mx) : 0.0f;  // IEEE reciprocal
+        // an element's magnitude is at most A, so products are within 6 and an ulp
+#define I8MP_PAIR(i)                                                                                            \
+    packed = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(packed, wide<kBf16>(w[i] & 0xffffu) * inv,                \
+                                                      wide<kBf16>(w[i] >> 16) * inv, 1.0f, i)
+        I8MP_PAIR(0);
+        I8MP_PAIR(1);
+        I8MP_PAIR(2);
+        I8MP_PAIR(3);
+#undef I8MP_PAIR
+    } else {  // an infinity or a NaN: NaNs are left out of A, and count as zeros
+        float f[8], mx = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t sign = (w[e >> 1] >> (16 * (e & 1) + 15)) & 1u;
-        packed |= (mag_code(f[e] * inv) | (sign << 3)) << (4 * e);
+        for (int e = 0; e < 8; ++e) {
+            f[e] = fabsf(wide<kBf16>((w[e >> 1] >> (16 * (e & 1))) & 0xffffu));
+            mx = fmaxf(mx, f[e]);
+        }
+        top = block_max(__float_as_uint(mx));
+        mx = __uint_as_float(top);
+        const float inv = mx > 0.0f ? 6.0f * (1.0f / mx) : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t sign = (w[e >> 1] >> (16 * (e & 1) + 15)) & 1u;
+            packed |= (mag_code(f[e] * inv) | (sign << 3)) << (4 * e);
+        }
+        top = kBf16 ? top >> 16 : (uint32_t)f2h(mx);
     }
-    const int at = (int)(slot & (a.c.page_size - 1));
-    const int P = a.c.page_size;
-    uint8_t* slab = a.c.data + ((slot >> a.c.page_shift) * a.c.heads + h) * a.c.slab();
-    if (is_v) {
-        uint8_t* codes = slab + P * 32 * nb;
-        *reinterpret_cast<uint16_t*>(codes + v_byte(at, part * 2, b, nb)) = (uint16_t)packed;
-        *reinterpret_cast<uint16_t*>(codes + v_byte(at, part * 2 + 1, b, nb)) = (uint16_t)(packed >> 16);
-    } else {
-        *reinterpret_cast<uint32_t*>(slab + at * 32 * nb + (part >> 1) * 8 * nb + b * 8 + (part & 1) * 4) = packed;
-    }
-    if (part == 0)
-        *reinterpret_cast<uint16_t*>(slab + P * (is_v ? 66 : 64) * nb + (at * nb + b) * 2) = (uint16_t)narrow<kBf16>(mx);
+    a_bits = top;
+    return packed;
 }
 
-// One lane per 8 dims, as above.
+// x' of 8 codes under A's bits
 template <bool kBf16>
-__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvMoveArgs a) {
-    const int nb = a.c.blocks;
-    const int64_t t = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int part = (int)(t & 7);
-    const int64_t blk = t >> 3;
-    const int b = (int)(blk % nb);
-    const int64_t th = blk / nb;
-    const int h = (int)(th % a.c.heads);
-    const int64_t tok = th / a.c.heads;
-    if (tok >= a.tokens) return;
-    const int64_t slot = a.slots[tok];
-    const bool is_v = blockIdx.y != 0;
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-    if (slot >= 0 && slot < (a.c.pages << a.c.page_shift)) {
-        const int at = (int)(slot & (a.c.page_size - 1));
-        const int P = a.c.page_size;
-        const uint8_t* slab = a.c.data + ((slot >> a.c.page_shift) * a.c.heads + h) * a.c.slab();
-        uint32_t packed;
-        if (is_v) {
-            const uint8_t* codes = slab + P * 32 * nb;
-            packed = *reinterpret_cast<const uint16_t*>(codes + v_byte(at, part * 2, b, nb)) |
-                     ((uint32_t)*reinterpret_cast<const uint16_t*>(codes + v_byte(at, part * 2 + 1, b, nb)) << 16);
-        } else {
-            packed = *reinterpret_cast<const uint32_t*>(slab + at * 32 * nb + (part >> 1) * 8 * nb + b * 8 + (part & 1) * 4);
-        }
-        const float d =
-            wide<kBf16>(*reinterpret_cast<const uint16_t*>(slab + P * (is_v ? 66 : 64) * nb + (at * nb + b) * 2)) / 6.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = code_value((packed >> (4 * e)) & 15u) * d;
+__device__ inline void values8(uint32_t codes, uint32_t a_bits, float (&x)[8]) {
+    const float d = wide<kBf16>(a_bits) / 6.0f;  // IEEE division
+#define I8MP_PAIR(i)                                                              \
+    do {                                                                          \
+        const f2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, i);    \
+        x[2 * i] = v.x * d;                                                       \
+        x[2 * i + 1] = v.y * d;                                                   \
+    } while (0)
+    I8MP_PAIR(0);
+    I8MP_PAIR(1);
+    I8MP_PAIR(2);
+    I8MP_PAIR(3);
+#undef I8MP_PAIR
+}
+
+// Which tokens and dims a lane has: 8 NB lanes a head, heads side by side, four tokens.
+template <int NB>
+struct Lane {
+    int64_t tok0;
+    int h, b, part;   // head, block, dims 8 part .. + 7 of it
+    bool live;
+};
+
+template <int NB>
+__device__ inline Lane<NB> lane_of(const KvMoveArgs& a) {
+    Lane<NB> l;
+    const uint32_t per = (uint32_t)a.c.heads * 8 * NB;  // lanes of a token
+    uint32_t i;
+    if (per >= kThreads) {  // several workgroups a quad of tokens
+        const uint32_t groups = (per + kThreads - 1) / kThreads;
+        const uint32_t quad = blockIdx.x / groups;
+        l.tok0 = (int64_t)quad * kQuad;
+        i = (blockIdx.x - quad * groups) * kThreads + threadIdx.x;
+        l.live = i < per;
+    } else {                // several quads a workgroup
+        const uint32_t quads = kThreads / per, q = threadIdx.x / per;
+        l.tok0 = ((int64_t)blockIdx.x * quads + q) * kQuad;
+        i = threadIdx.x - q * per;
+        l.live = q < quads;
     }
-    const int64_t o = tok * (is_v ? a.ldv : a.ldk) + h * (is_v ? a.hsv : a.hsk) + b * 64 + part * 8;
-    void* dst = is_v ? a.v : a.k;
-    if (a.out_dtype == I8MP_DTYPE_F32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(dst) + o);
+    l.live = l.live && l.tok0 < a.tokens;
+    l.part = (int)(i & 7);
+    l.b = (int)(i >> 3) & (NB - 1);
+    l.h = (int)(i / (8 * NB));
+    return l;
+}
+
+// A slot's place: first byte of its slab's row of K codes, of V codes, of K scales.
+struct Spot {
+    uint8_t* k;
+    uint8_t* v;
+    uint8_t* s;
+};
+
+template <int NB>
+__device__ inline Spot spot_of(const KvCache& c, int64_t slot, const Lane<NB>& l) {
+    const int P = c.page_size, t = (int)(slot & (P - 1));
+    uint8_t* slab = c.data + ((slot >> c.page_shift) * c.heads + l.h) * ((int64_t)P * 68 * NB);
+    Spot s;
+    s.k = slab + t * 32 * NB + (l.part >> 1) * 8 * NB + l.b * 8 + (l.part & 1) * 4;
+    // dims 8 part + 0..3 and + 4..7 are V groups m = 2 part and 2 part + 1
+    s.v = slab + P * 32 * NB + (t >> 2) * 128 * NB + l.part * 16 * NB + l.b * 8 + ((t & 1) * 2 + ((t >> 1) & 1)) * 2;
+    s.s = slab + P * 64 * NB + (t * NB + l.b) * 2;
+    return s;
+}
+
+__device__ inline bool in_cache(const KvCache& c, int64_t slot) { return slot >= 0 && slot < (c.pages << c.page_shift); }
+
+// the four slots of a lane's tokens; true if they are one aligned group of the cache
+__device__ inline bool slots_of(const KvMoveArgs& a, int64_t tok0, int64_t (&slot)[kQuad]) {
+    bool whole = true;
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i) {
+        slot[i] = tok0 + i < a.tokens ? a.slots[tok0 + i] : -1;
+        if (!in_cache(a.c, slot[i])) slot[i] = -1;
+        whole &= slot[i] == slot[0] + i;
+    }
+    return whole & (slot[0] >= 0) & ((slot[0] & 3) == 0);
+}
+
+// 4 x 16 bits of two tokens' halves -> the words (token 0, token 2) and (token 1, token 3)
+__device__ inline uint2 v_words(uint32_t t0, uint32_t t1, uint32_t t2, uint32_t t3, bool high) {
+    const uint32_t sel = high ? 0x07060302u : 0x05040100u;  // halves of (b, a): a low, b high
+    return make_uint2(__builtin_amdgcn_perm(t2, t0, sel), __builtin_amdgcn_perm(t3, t1, sel));
+}
+
+template <bool kBf16, int NB>
+__global__ __launch_bounds__(kThreads) void kv_write_kernel(KvMoveArgs a) {
+    const Lane<NB> l = lane_of<NB>(a);
+    if (!l.live) return;  // the 8 lanes of a block leave together
+    int64_t slot[kQuad];
+    const bool whole = slots_of(a, l.tok0, slot);
+    const int dim = l.b * 64 + l.part * 8;
+    const half_bits* ks = static_cast<const half_bits*>(a.k) + l.tok0 * a.ldk + l.h * a.hsk + dim;
+    const half_bits* vs = static_cast<const half_bits*>(a.v) + l.tok0 * a.ldv + l.h * a.hsv + dim;
+    uint4 k[kQuad], v[kQuad];
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i) {
+        const bool live = slot[i] >= 0;
+        k[i] = live ? *reinterpret_cast<const uint4*>(ks + i * a.ldk) : make_uint4(0, 0, 0, 0);
+        v[i] = live ? *reinterpret_cast<const uint4*>(vs + i * a.ldv) : make_uint4(0, 0, 0, 0);
+    }
+    uint32_t kc[kQuad], vc[kQuad], ka[kQuad], va[kQuad];
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i) {
+        kc[i] = quantize8<kBf16>(k[i], ka[i]);
+        vc[i] = quantize8<kBf16>(v[i], va[i]);
+    }
+    const int v_scales = a.c.page_size * 2 * NB;  // behind the K scales
+    if (whole) {
+        const Spot s = spot_of<NB>(a.c, slot[0], l);
+#pragma unroll
+        for (int i = 0; i < kQuad; ++i) *reinterpret_cast<uint32_t*>(s.k + i * 32 * NB) = kc[i];
+        *reinterpret_cast<uint2*>(s.v) = v_words(vc[0], vc[1], vc[2], vc[3], false);
+        *reinterpret_cast<uint2*>(s.v + 8 * NB) = v_words(vc[0], vc[1], vc[2], vc[3], true);
+        if (l.part < kQuad) {  // lane `part` of the block stores token part's scales
+            const uint32_t kk = l.part < 2 ? (l.part ? ka[1] : ka[0]) : (l.part == 2 ? ka[2] : ka[3]);
+            const uint32_t vv = l.part < 2 ? (l.part ? va[1] : va[0]) : (l.part == 2 ? va[2] : va[3]);
+            uint8_t* dst = s.s + l.part * 2 * NB;
+            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)kk;
+            *reinterpret_cast<uint16_t*>(dst + v_scales) = (uint16_t)vv;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i) {
+        if (slot[i] < 0) continue;
+        const Spot s = spot_of<NB>(a.c, slot[i], l);
+        *reinterpret_cast<uint32_t*>(s.k) = kc[i];
+        *reinterpret_cast<uint16_t*>(s.v) = (uint16_t)vc[i];
+        *reinterpret_cast<uint16_t*>(s.v + 8 * NB) = (uint16_t)(vc[i] >> 16);
+        if (l.part == 0) {
+            *reinterpret_cast<uint16_t*>(s.s) = (uint16_t)ka[i];
+            *reinterpret_cast<uint16_t*>(s.s + v_scales) = (uint16_t)va[i];
+        }
+    }
+}
+
+// one lane's 8 values of a token in the output's type
+template <int kType>
+__device__ inline void store8(void* base, int64_t at, const float (&x)[8]) {
+    if constexpr (kType == I8MP_DTYPE_F32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
         p[0] = make_float4(x[0], x[1], x[2], x[3]);
         p[1] = make_float4(x[4], x[5], x[6], x[7]);
     } else {
         uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[e] = a.out_dtype == I8MP_DTYPE_BF16 ? narrow<true>(x[2 * e]) | (narrow<true>(x[2 * e + 1]) << 16)
-                                                  : narrow<false>(x[2 * e]) | (narrow<false>(x[2 * e + 1]) << 16);
-        *reinterpret_cast<uint4*>(static_cast<half_bits*>(dst) + o) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (kType == I8MP_DTYPE_BF16) {
+                typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+                w[e] = __builtin_bit_cast(uint32_t, b2{(__bf16)x[2 * e], (__bf16)x[2 * e + 1]});
+            } else {
+                w[e] = __builtin_bit_cast(uint32_t, h2_t{(_Float16)x[2 * e], (_Float16)x[2 * e + 1]});
+            }
+        }
+        *reinterpret_cast<uint4*>(static_cast<half_bits*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
-dim3 move_grid(const KvMoveArgs& a) {
-    return dim3((unsigned)ceil_div(a.tokens * a.c.heads * a.c.blocks * 8, kThreads), 2);
+template <bool kBf16, int NB, int kType>
+__global__ __launch_bounds__(kThreads) void kv_read_kernel(KvMoveArgs a) {
+    const Lane<NB> l = lane_of<NB>(a);
+    if (!l.live) return;
+    int64_t slot[kQuad];
+    const bool whole = slots_of(a, l.tok0, slot);
+    const int v_scales = a.c.page_size * 2 * NB;
+    uint32_t kc[kQuad], vc[kQuad], ka[kQuad], va[kQuad];
+    if (whole) {
+        const Spot s = spot_of<NB>(a.c, slot[0], l);
+        const uint2 lo = *reinterpret_cast<const uint2*>(s.v), hi = *reinterpret_cast<const uint2*>(s.v + 8 * NB);
+#pragma unroll
+        for (int i = 0; i < kQuad; ++i) {
+            kc[i] = *reinterpret_cast<const uint32_t*>(s.k + i * 32 * NB);
+            ka[i] = *reinterpret_cast<const uint16_t*>(s.s + i * 2 * NB);
+            va[i] = *reinterpret_cast<const uint16_t*>(s.s + i * 2 * NB + v_scales);
+            // words (token 0, token 2) and (token 1, token 3), dims 0..3 in lo and 4..7 in hi
+            const uint32_t a0 = i & 1 ? lo.y : lo.x, a1 = i & 1 ? hi.y : hi.x;
+            vc[i] = __builtin_amdgcn_perm(a1, a0, i >> 1 ? 0x07060302u : 0x05040100u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kQuad; ++i) {
+            kc[i] = vc[i] = ka[i] = va[i] = 0;
+            if (slot[i] < 0) continue;
+            const Spot s = spot_of<NB>(a.c, slot[i], l);
+            kc[i] = *reinterpret_cast<const uint32_t*>(s.k);
+            vc[i] = *reinterpret_cast<const uint16_t*>(s.v) | ((uint32_t)*reinterpret_cast<const uint16_t*>(s.v + 8 * NB) << 16);
+            ka[i] = *reinterpret_cast<const uint16_t*>(s.s);
+            va[i] = *reinterpret_cast<const uint16_t*>(s.s + v_scales);
+        }
+    }
+    const int dim = l.b * 64 + l.part * 8;
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i) {
+        if (l.tok0 + i >= a.tokens) break;
+        float x[8];
+        values8<kBf16>(kc[i], ka[i], x);
+        store8<kType>(a.k, (l.tok0 + i) * a.ldk + l.h * a.hsk + dim, x);
+        values8<kBf16>(vc[i], va[i], x);
+        store8<kType>(a.v, (l.tok0 + i) * a.ldv + l.h * a.hsv + dim, x);
+    }
+}
+
+// workgroups for the tokens of one launch
+int64_t move_blocks(const KvMoveArgs& a, int64_t tokens) {
+    const int64_t per = (int64_t)a.c.heads * 8 * a.c.blocks, quads = ceil_div(tokens, kQuad);
+    return per >= kThreads ? quads * ceil_div(per, kThreads) : ceil_div(quads, kThreads / per);
+}
+
+// Tokens in launches of at most 2^22 workgroups (a grid holds fewer than 2^32 lanes).
+template <typename F>
+hipError_t in_pieces(const KvMoveArgs& args, int elem, F launch) {
+    const int64_t per = ceil_div((int64_t)args.c.heads * 8 * args.c.blocks, kThreads);
+    const int64_t most = ((int64_t)1 << 22) / per * kQuad;
+    for (int64_t t = 0; t < args.tokens; t += most) {
+        KvMoveArgs a = args;
+        a.tokens = args.tokens - t < most ? args.tokens - t : most;
+        a.slots = args.slots + t;
+        a.k = static_cast<uint8_t*>(args.k) + t * args.ldk * elem;
+        a.v = static_cast<uint8_t*>(args.v) + t * args.ldv * elem;
+        launch(a, dim3((unsigned)move_blocks(a, a.tokens)));
+        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <bool kBf16, int NB>
+hipError_t write(const KvMoveArgs& args, hipStream_t stream) {
+    return in_pieces(args, 2, [&](const KvMoveArgs& a, dim3 grid) {
+        hipLaunchKernelGGL((kv_write_kernel<kBf16, NB>), grid, dim3(kThreads), 0, stream, a);
+    });
+}
+
+template <bool kBf16, int NB>
+hipError_t read(const KvMoveArgs& args, hipStream_t stream) {
+    return in_pieces(args, args.out_dtype == I8MP_DTYPE_F32 ? 4 : 2, [&](const KvMoveArgs& a, dim3 grid) {
+        if (a.out_dtype == I8MP_DTYPE_F32)
+            hipLaunchKernelGGL((kv_read_kernel<kBf16, NB, I8MP_DTYPE_F32>), grid, dim3(kThreads), 0, stream, a);
+        else if (a.out_dtype == I8MP_DTYPE_F16)
+            hipLaunchKernelGGL((kv_read_kernel<kBf16, NB, I8MP_DTYPE_F16>), grid, dim3(kThreads), 0, stream, a);
+        else
+            hipLaunchKernelGGL((kv_read_kernel<kBf16, NB, I8MP_DTYPE_BF16>), grid, dim3(kThreads), 0, stream, a);
+    });
 }
 
 }  // namespace
 
 hipError_t launch_kv_write(const KvMoveArgs& a, hipStream_t stream) {
     if (a.c.bf16)
-        hipLaunchKernelGGL(kv_write_kernel<true>, move_grid(a), dim3(kThreads), 0, stream, a);
-    else
-        hipLaunchKernelGGL(kv_write_kernel<false>, move_grid(a), dim3(kThreads), 0, stream, a);
-    return hipGetLastError();
+        return a.c.blocks == 1 ? write<true, 1>(a, stream) : a.c.blocks == 2 ? write<true, 2>(a, stream) : write<true, 4>(a, stream);
+    return a.c.blocks == 1 ? write<false, 1>(a, stream) : a.c.blocks == 2 ? write<false, 2>(a, stream) : write<false, 4>(a, stream);
 }
 
 hipError_t launch_kv_read(const KvMoveArgs& a, hipStream_t stream) {
     if (a.c.bf16)
-        hipLaunchKernelGGL(kv_read_kernel<true>, move_grid(a), dim3(kThreads), 0, stream, a);
-    else
-        hipLaunchKernelGGL(kv_read_kernel<false>, move_grid(a), dim3(kThreads), 0, stream, a);
-    return hipGetLastError();
+        return a.c.blocks == 1 ? read<true, 1>(a, stream) : a.c.blocks == 2 ? read<true, 2>(a, stream) : read<true, 4>(a, stream);
+    return a.c.blocks == 1 ? read<false, 1>(a, stream) : a.c.blocks == 2 ? read<false, 2>(a, stream) : read<false, 4>(a, stream);
 }
 
 }  // namespace i8mp
