@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kQuad = 4;   // tokens of a lane
+constexpr int kSpan = 32;  // tokens whose quads are aligned together
 
 template <bool kBf16>
 __device__ inline float wide(uint32_t h) {
@@ -110,9 +111,13 @@ __device__ inline void values8(uint32_t codes, uint32_t a_bits, float (&x)[8]) {
 }
 
 // Which tokens and dims a lane has: 8 NB lanes a head, heads side by side, four tokens.
+// Tokens come in spans of 32, whose quads start where the span's first slot puts a
+// group's edge (a span has up to nine then): a prompt that starts inside a group still
+// has its tokens in whole groups.
 template <int NB>
 struct Lane {
-    int64_t tok0;
+    int64_t tok0;     // first token of the quad: may lie before the span
+    int64_t from, to; // the span's tokens
     int h, b, part;   // head, block, dims 8 part .. + 7 of it
     bool live;
 };
@@ -120,21 +125,28 @@ struct Lane {
 template <int NB>
 __device__ inline Lane<NB> lane_of(const KvMoveArgs& a) {
     Lane<NB> l;
-    const uint32_t per = (uint32_t)a.c.heads * 8 * NB;  // lanes of a token
-    uint32_t i;
+    const uint32_t per = (uint32_t)a.c.heads * 8 * NB;  // lanes of a quad
+    uint32_t i, quad;
     if (per >= kThreads) {  // several workgroups a quad of tokens
         const uint32_t groups = (per + kThreads - 1) / kThreads;
-        const uint32_t quad = blockIdx.x / groups;
-        l.tok0 = (int64_t)quad * kQuad;
+        quad = blockIdx.x / groups;
         i = (blockIdx.x - quad * groups) * kThreads + threadIdx.x;
         l.live = i < per;
     } else {                // several quads a workgroup
         const uint32_t quads = kThreads / per, q = threadIdx.x / per;
-        l.tok0 = ((int64_t)blockIdx.x * quads + q) * kQuad;
+        quad = blockIdx.x * quads + q;
         i = threadIdx.x - q * per;
         l.live = q < quads;
     }
-    l.live = l.live && l.tok0 < a.tokens;
+    const uint32_t span = quad / (kSpan / kQuad + 1);
+    l.from = (int64_t)span * kSpan;
+    l.to = l.from + kSpan < a.tokens ? l.from + kSpan : a.tokens;
+    if (l.from < a.tokens) {
+        l.tok0 = l.from - (int64_t)(a.slots[l.from] & 3) + (quad - span * (kSpan / kQuad + 1)) * kQuad;
+        l.live = l.live && l.tok0 < l.to;
+    } else {
+        l.live = false;
+    }
     l.part = (int)(i & 7);
     l.b = (int)(i >> 3) & (NB - 1);
     l.h = (int)(i / (8 * NB));
@@ -162,12 +174,14 @@ __device__ inline Spot spot_of(const KvCache& c, int64_t slot, const Lane<NB>& l
 
 __device__ inline bool in_cache(const KvCache& c, int64_t slot) { return slot >= 0 && slot < (c.pages << c.page_shift); }
 
-// the four slots of a lane's tokens; true if they are one aligned group of the cache
-__device__ inline bool slots_of(const KvMoveArgs& a, int64_t tok0, int64_t (&slot)[kQuad]) {
+// the four slots of a lane's tokens, -1 for none; true if they are one group of the cache
+template <int NB>
+__device__ inline bool slots_of(const KvMoveArgs& a, const Lane<NB>& l, int64_t (&slot)[kQuad]) {
     bool whole = true;
 #pragma unroll
     for (int i = 0; i < kQuad; ++i) {
-        slot[i] = tok0 + i < a.tokens ? a.slots[tok0 + i] : -1;
+        const int64_t t = l.tok0 + i;
+        slot[i] = t >= l.from && t < l.to ? a.slots[t] : -1;
         if (!in_cache(a.c, slot[i])) slot[i] = -1;
         whole &= slot[i] == slot[0] + i;
     }
@@ -185,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvMoveArgs a) {
     const Lane<NB> l = lane_of<NB>(a);
     if (!l.live) return;  // the 8 lanes of a block leave together
     int64_t slot[kQuad];
-    const bool whole = slots_of(a, l.tok0, slot);
+    const bool whole = slots_of(a, l, slot);
     const int dim = l.b * 64 + l.part * 8;
     const half_bits* ks = static_cast<const half_bits*>(a.k) + l.tok0 * a.ldk + l.h * a.hsk + dim;
     const half_bits* vs = static_cast<const half_bits*>(a.v) + l.tok0 * a.ldv + l.h * a.hsv + dim;
@@ -259,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvMoveArgs a) {
     const Lane<NB> l = lane_of<NB>(a);
     if (!l.live) return;
     int64_t slot[kQuad];
-    const bool whole = slots_of(a, l.tok0, slot);
+    const bool whole = slots_of(a, l, slot);
     const int v_scales = a.c.page_size * 2 * NB;
     uint32_t kc[kQuad], vc[kQuad], ka[kQuad], va[kQuad];
     if (whole) {
@@ -289,7 +303,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvMoveArgs a) {
     const int dim = l.b * 64 + l.part * 8;
 #pragma unroll
     for (int i = 0; i < kQuad; ++i) {
-        if (l.tok0 + i >= a.tokens) break;
+        if (l.tok0 + i < l.from || l.tok0 + i >= l.to) continue;
         float x[8];
         values8<kBf16>(kc[i], ka[i], x);
         store8<kType>(a.k, (l.tok0 + i) * a.ldk + l.h * a.hsk + dim, x);
@@ -300,7 +314,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvMoveArgs a) {
 
 // workgroups for the tokens of one launch
 int64_t move_blocks(const KvMoveArgs& a, int64_t tokens) {
-    const int64_t per = (int64_t)a.c.heads * 8 * a.c.blocks, quads = ceil_div(tokens, kQuad);
+    const int64_t per = (int64_t)a.c.heads * 8 * a.c.blocks, quads = ceil_div(tokens, kSpan) * (kSpan / kQuad + 1);
     return per >= kThreads ? quads * ceil_div(per, kThreads) : ceil_div(quads, kThreads / per);
 }
 
@@ -308,7 +322,7 @@ int64_t move_blocks(const KvMoveArgs& a, int64_t tokens) {
 template <typename F>
 hipError_t in_pieces(const KvMoveArgs& args, int elem, F launch) {
     const int64_t per = ceil_div((int64_t)args.c.heads * 8 * args.c.blocks, kThreads);
-    const int64_t most = ((int64_t)1 << 22) / per * kQuad;
+    const int64_t most = ((int64_t)1 << 22) / per / (kSpan / kQuad + 1) * kSpan;
     for (int64_t t = 0; t < args.tokens; t += most) {
         KvMoveArgs a = args;
         a.tokens = args.tokens - t < most ? args.tokens - t : most;
