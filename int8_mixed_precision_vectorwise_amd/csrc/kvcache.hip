@@ -22,6 +22,13 @@ constexpr int kThreads = 256;
 constexpr int kQuad = 4;   // tokens of a lane
 constexpr int kSpan = 32;  // tokens whose quads are aligned together
 
+// Calls that move more than the last-level cache holds (values and cache together) pass
+// it by with the 16-bit values (non-temporal).  32 heads of 128, us, passing by / not:
+// 16381 tokens (255 MiB of values) written 63 / 68, read 54 / 73; 32768 written 122 /
+// 139, read 105 / 138, read and summed 291 / 300.  Below that a neighbour finds the
+// values in the cache: 8000 tokens (125 MiB) read and summed 82 / 70, written 33 / 30.
+constexpr int64_t kLastLevel = 256 << 20;
+
 template <bool kBf16>
 __device__ inline float wide(uint32_t h) {
     return kBf16 ? __uint_as_float(h << 16) : h2f((half_bits)h);
@@ -35,6 +42,7 @@ __device__ inline uint32_t mag_code(float v) {
 
 typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 typedef float f2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 // largest value of the 8 lanes that share a block
 __device__ inline uint32_t block_max(uint32_t v) {
@@ -194,7 +202,19 @@ __device__ inline uint2 v_words(uint32_t t0, uint32_t t1, uint32_t t2, uint32_t 
     return make_uint2(__builtin_amdgcn_perm(t2, t0, sel), __builtin_amdgcn_perm(t3, t1, sel));
 }
 
-template <bool kBf16, int NB>
+template <bool kPast>
+__device__ inline uint4 load16(const half_bits* p) {
+    if constexpr (kPast) return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u4*>(p)));
+    return *reinterpret_cast<const uint4*>(p);
+}
+
+template <bool kPast>
+__device__ inline void store16(void* p, const u4& x) {
+    if constexpr (kPast) __builtin_nontemporal_store(x, static_cast<u4*>(p));
+    else *static_cast<u4*>(p) = x;
+}
+
+template <bool kBf16, int NB, bool kPast>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvMoveArgs a) {
     const Lane<NB> l = lane_of<NB>(a);
     if (!l.live) return;  // the 8 lanes of a block leave together
@@ -207,8 +227,8 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvMoveArgs a) {
 #pragma unroll
     for (int i = 0; i < kQuad; ++i) {
         const bool live = slot[i] >= 0;
-        k[i] = live ? *reinterpret_cast<const uint4*>(ks + i * a.ldk) : make_uint4(0, 0, 0, 0);
-        v[i] = live ? *reinterpret_cast<const uint4*>(vs + i * a.ldv) : make_uint4(0, 0, 0, 0);
+        k[i] = live ? load16<kPast>(ks + i * a.ldk) : make_uint4(0, 0, 0, 0);
+        v[i] = live ? load16<kPast>(vs + i * a.ldv) : make_uint4(0, 0, 0, 0);
     }
     uint32_t kc[kQuad], vc[kQuad], ka[kQuad], va[kQuad];
 #pragma unroll
@@ -247,12 +267,12 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvMoveArgs a) {
 }
 
 // one lane's 8 values of a token in the output's type
-template <int kType>
+template <int kType, bool kPast>
 __device__ inline void store8(void* base, int64_t at, const float (&x)[8]) {
     if constexpr (kType == I8MP_DTYPE_F32) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-        p[0] = make_float4(x[0], x[1], x[2], x[3]);
-        p[1] = make_float4(x[4], x[5], x[6], x[7]);
+        float* p = static_cast<float*>(base) + at;
+        store16<kPast>(p, __builtin_bit_cast(u4, make_float4(x[0], x[1], x[2], x[3])));
+        store16<kPast>(p + 4, __builtin_bit_cast(u4, make_float4(x[4], x[5], x[6], x[7])));
     } else {
         uint32_t w[4];
 #pragma unroll
@@ -264,11 +284,11 @@ __device__ inline void store8(void* base, int64_t at, const float (&x)[8]) {
                 w[e] = __builtin_bit_cast(uint32_t, h2_t{(_Float16)x[2 * e], (_Float16)x[2 * e + 1]});
             }
         }
-        *reinterpret_cast<uint4*>(static_cast<half_bits*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        store16<kPast>(static_cast<half_bits*>(base) + at, u4{w[0], w[1], w[2], w[3]});
     }
 }
 
-template <bool kBf16, int NB, int kType>
+template <bool kBf16, int NB, int kType, bool kPast>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvMoveArgs a) {
     const Lane<NB> l = lane_of<NB>(a);
     if (!l.live) return;
@@ -306,9 +326,9 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvMoveArgs a) {
         if (l.tok0 + i < l.from || l.tok0 + i >= l.to) continue;
         float x[8];
         values8<kBf16>(kc[i], ka[i], x);
-        store8<kType>(a.k, (l.tok0 + i) * a.ldk + l.h * a.hsk + dim, x);
+        store8<kType, kPast>(a.k, (l.tok0 + i) * a.ldk + l.h * a.hsk + dim, x);
         values8<kBf16>(vc[i], va[i], x);
-        store8<kType>(a.v, (l.tok0 + i) * a.ldv + l.h * a.hsv + dim, x);
+        store8<kType, kPast>(a.v, (l.tok0 + i) * a.ldv + l.h * a.hsv + dim, x);
     }
 }
 
@@ -335,23 +355,34 @@ hipError_t in_pieces(const KvMoveArgs& args, int elem, F launch) {
     return hipSuccess;
 }
 
+bool past_cache(const KvMoveArgs& a, int elem) {
+    return a.tokens * a.c.heads * (2 * a.c.blocks * (64 * elem + 34)) > kLastLevel;
+}
+
 template <bool kBf16, int NB>
 hipError_t write(const KvMoveArgs& args, hipStream_t stream) {
+    const bool past = past_cache(args, 2);
     return in_pieces(args, 2, [&](const KvMoveArgs& a, dim3 grid) {
-        hipLaunchKernelGGL((kv_write_kernel<kBf16, NB>), grid, dim3(kThreads), 0, stream, a);
+        if (past) hipLaunchKernelGGL((kv_write_kernel<kBf16, NB, true>), grid, dim3(kThreads), 0, stream, a);
+        else hipLaunchKernelGGL((kv_write_kernel<kBf16, NB, false>), grid, dim3(kThreads), 0, stream, a);
+    });
+}
+
+template <bool kBf16, int NB, int kType>
+hipError_t read_as(const KvMoveArgs& args, hipStream_t stream) {
+    constexpr int kElem = kType == I8MP_DTYPE_F32 ? 4 : 2;
+    const bool past = past_cache(args, kElem);
+    return in_pieces(args, kElem, [&](const KvMoveArgs& a, dim3 grid) {
+        if (past) hipLaunchKernelGGL((kv_read_kernel<kBf16, NB, kType, true>), grid, dim3(kThreads), 0, stream, a);
+        else hipLaunchKernelGGL((kv_read_kernel<kBf16, NB, kType, false>), grid, dim3(kThreads), 0, stream, a);
     });
 }
 
 template <bool kBf16, int NB>
-hipError_t read(const KvMoveArgs& args, hipStream_t stream) {
-    return in_pieces(args, args.out_dtype == I8MP_DTYPE_F32 ? 4 : 2, [&](const KvMoveArgs& a, dim3 grid) {
-        if (a.out_dtype == I8MP_DTYPE_F32)
-            hipLaunchKernelGGL((kv_read_kernel<kBf16, NB, I8MP_DTYPE_F32>), grid, dim3(kThreads), 0, stream, a);
-        else if (a.out_dtype == I8MP_DTYPE_F16)
-            hipLaunchKernelGGL((kv_read_kernel<kBf16, NB, I8MP_DTYPE_F16>), grid, dim3(kThreads), 0, stream, a);
-        else
-            hipLaunchKernelGGL((kv_read_kernel<kBf16, NB, I8MP_DTYPE_BF16>), grid, dim3(kThreads), 0, stream, a);
-    });
+hipError_t read(const KvMoveArgs& a, hipStream_t stream) {
+    return a.out_dtype == I8MP_DTYPE_F32   ? read_as<kBf16, NB, I8MP_DTYPE_F32>(a, stream)
+           : a.out_dtype == I8MP_DTYPE_F16 ? read_as<kBf16, NB, I8MP_DTYPE_F16>(a, stream)
+                                           : read_as<kBf16, NB, I8MP_DTYPE_BF16>(a, stream);
 }
 
 }  // namespace
