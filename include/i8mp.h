@@ -478,8 +478,10 @@ i8mp_status i8mp_fp4_cache_read(const i8mp_fp4_cache* cache /* host */, const in
  * every query sees: a prompt without causal order, or the first tokens kept in
  * sight beside a window.  A row that sees nothing (L = 0, or a query before the
  * first token) gets zeros and lse = -inf.  Sums, maxima and the softmax are fp32;
- * the weights e^s, times a block's A, are rounded once to the 16-bit type for the
- * product with the E2M1 values.
+ * the weights e^s, times a block's A, are rounded to the 16-bit type for the product
+ * with the E2M1 values (bfloat16: once; fp16: e^s is rounded, then its product).
+ * The rows of one sequence do not depend on the others' contents; how the keys are
+ * cut, and so the order of the sums, follows from the call's sizes.
  *
  * What is read on the device is bounded there: lengths are taken into [0, max_len],
  * query offsets into [0, tokens], a sequence's queries past max_q are left out, and
@@ -502,7 +504,11 @@ typedef struct i8mp_fp4_attention {
     int64_t tokens;           /* rows of q                                          */
     int32_t batch;
     int32_t q_heads;          /* a multiple of kv_heads                              */
-    int32_t max_q;            /* most queries of a sequence, >= 1                    */
+    int32_t max_q;            /* most queries of a sequence, >= 1.  Work is laid out
+                                 for batch * max_q rows: sequences of one query and
+                                 prompts are better two calls.  With g = q_heads /
+                                 kv_heads, max_q * g < 2^31 - 64 and batch * kv_heads
+                                 * ceil(max_q * g / 16) < 2^31                       */
     int32_t max_len;          /* bound on the lengths, <= table_cols * page_size     */
     int32_t window;           /* 0: none                                            */
     float scale;

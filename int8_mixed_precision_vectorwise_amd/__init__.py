@@ -679,7 +679,7 @@ def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, heads: Optional[int],
     if unit != 1:
         raise ValueError(f"{name} must have unit stride within a head")
     # the stride of an axis of one element is never taken: any that the library accepts will do
-    return (ld if shape[0] > 1 else max(ld, shape[1] * head_dim)), (hs if shape[1] > 1 else head_dim)
+    return (ld if shape[0] > 1 else head_dim), (hs if shape[1] > 1 else head_dim)
 
 
 def fp4_cache_write(cache: Fp4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:

@@ -751,6 +751,8 @@ bool kv_call(const i8mp_fp4_cache* cache, const i8mp_fp4_attention* p, KvAttnArg
     if (p->q_heads < 1 || p->q_heads > 65535 || p->q_heads % cache->kv_heads) return false;
     if (p->max_len > (1 << 30) || p->max_q > (1 << 30) || p->table_cols < 0 || p->ldt < p->table_cols) return false;
     if (p->max_len > (int64_t)p->table_cols * cache->page_size) return false;
+    const int64_t rows = (int64_t)p->max_q * (p->q_heads / cache->kv_heads);  // of a sequence and kv head
+    if (rows > INT32_MAX - 64 || (int64_t)p->batch * ceil_div(rows, 16) > INT32_MAX / cache->kv_heads) return false;
     if (!std::isfinite(p->scale) || !(p->softcap >= 0.0f) || !std::isfinite(p->softcap)) return false;
     if (!p->q_offsets && p->tokens != (int64_t)p->batch * p->max_q) return false;
     if (!kv_strides(p->ldq, p->hsq, cache, 8) || !kv_strides(p->ldo, p->hso, cache, 8)) return false;

@@ -327,21 +327,23 @@ __device__ inline float scale_at(const uint32_t (&w)[NB * 2], int i, int b) {
 typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 
 // How weights are kept in the 16-bit type's range.  A row's reference is a maximum that
-// it left as it was until a score passed it by 2^kSlack, so that few tiles rescale.
-// fp16: weights are 2^k times e^(s - reference), k such that they stay below 2^15 and
-// so do their products with the largest A that the wave has met (A < 2^e, k = 15 -
-// kSlack - e, e >= 0): a weight keeps its digits down to 2^-22 of the largest, which
-// counts where a few keys of small values draw nearly all the weight.
+// stays as it was until a score passes it by 2^kSlack, so that few tiles rescale (2048
+// queries behind 2048 tokens, 64 / 8 heads of 128, bfloat16: 268 us, 312 with no slack).
+// fp16: weights are 2^k times e^(s - reference), k = 8 - e with 2^e above every A the
+// wave has met (e >= 0; a larger A than before takes a smaller k and a rescale).  They
+// then stay below 2^(k + 7) and their products with A below 2^15, and a key's product
+// is kept down to 2^-25 where a scale of 1 has 2^8: few keys of small values may draw
+// nearly all the weight, beside large values that draw little.
 template <bool kBf16>
 constexpr float kSlack = kBf16 ? 8.0f : 7.0f;
 __device__ inline int weight_shift(int e) { return 8 - e; }
-constexpr int kFirstLarge = 3;
+constexpr int kFirstLarge = 0;
 
 // The products P A of a lane's 8 weights with a block's scales, in the order of the
 // keys.  bfloat16: fp32 products, rounded once, as the output is.  fp16: the weights are
-// rounded to fp16 and multiplied there, two roundings: packed products on scales that
-// are paired once a tile take half the instructions (of a 4096-token prompt's 435 VALU
-// instructions a tile for 48 rows, 72 fewer; 453 us against 486 us with one rounding).
+// rounded to fp16 and multiplied there, two roundings, each of the output's size: packed
+// products on scales that are paired once a tile take half the instructions (a
+// 4096-token prompt of 64 heads of 128: 453 us, 486 with one rounding).
 template <bool kBf16, int NB>
 struct Weights {
     uint32_t a[2][2 * NB];
@@ -386,17 +388,28 @@ struct Weights<false, NB> {
     }
 };
 
-// One workgroup: one sequence, kv head, row tile of 16 query rows (token-major,
-// then the heads of the group) and a run of key tiles.  S^T = K Q^T leaves a lane
-// with 4 keys of each half tile and one query column, which is the layout that P^T
-// needs as the second operand of O^T = V^T P^T, so P never moves between lanes.
-// Tiles come through a ring of kRing stages of LDS for each wave, filled by DMA: a
-// tile is read into registers whole and its stage requested anew before the products.
+// One workgroup: one sequence, kv head, row tile of 16 T query rows (token-major,
+// then the heads of the group) and a run of key tiles, which its waves take in turn.
+// S^T = K Q^T leaves a lane with 4 keys of each half tile and one query row, which is the
+// layout that P^T needs as the second operand of O^T = V^T P^T, so P never moves between
+// lanes.  Tiles come through a ring of kRing stages of LDS for each wave, filled by DMA:
+// a tile is read into registers whole and its stage requested anew before the products,
+// and waves meet only at the end.
 // kScored: scores get a cap, a distance term or a factor of 0 (else a factor alone,
 // which then rides on the exponential's argument).
-// Workgroups of a CU, by their registers (512 a lane for the waves of a SIMD).  A row
-// tile of 16 T rows is read once for all of them and its codes converted once, but T = 3
-// takes 248 registers with head_dim 128; with 256 two columns of rows already spill.
+//
+// What bounds it.  Few rows: HBM; 64 sequences of 8191 tokens, 64 / 8 heads of 128, are
+// read at 5.1 TB/s, one of 131072 tokens at 4.9; short contexts, a prologue and
+// epilogue of about 4 us.  Many rows: the VALU, about 75 % busy: converting 4-bit codes
+// (shared by the row tile), masks, exponentials and the scaling of weights take 443
+// instructions for 48 rows of 32 keys beside 48 matrix instructions, which hold the SIMD
+// for about 10 of their 16 cycles each.  A 4096-token prompt of 64 heads of 128: 700
+// TFLOP/s.
+//
+// workgroups(): those of a CU, by their registers (512 a lane for the waves of a SIMD).
+// T = 3 takes 248 registers with head_dim 128; with 256 two sets of rows already spill.
+// 2048 queries behind 2048 tokens, 64 / 8 heads of 128, bfloat16, in row tiles of 16, 32
+// and 48: 351, 305 and 268 us.
 constexpr int workgroups(int NB, int T) { return NB == 4 ? 2 : T == 1 ? 4 : NB == 1 ? 3 : 2; }
 template <int NB>
 constexpr int kRing() { return NB == 1 ? 4 : 2; }
@@ -416,7 +429,7 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
     // part-major: the later parts, which shorter sequences lack, come last
-    uint32_t id = blockIdx.x;
+    uint32_t id = a.block0 + blockIdx.x;
     const uint32_t segments = (uint32_t)a.batch * (uint32_t)a.row_tiles * (uint32_t)a.c.heads;
     const int chunk = (int)(id / segments);
     id -= chunk * segments;
@@ -903,11 +916,17 @@ inline bool scored_call(const KvAttnArgs& a) { return a.softcap > 0.0f || a.alib
 
 template <bool kBf16, int NB, int T, bool kOne>
 void launch_main(const KvAttnArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.batch * a.row_tiles * a.c.heads * a.chunks)), block(64 * kWaves);
-    if (scored_call(a))
-        hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, T, kOne, true>), grid, block, 0, stream, a);
-    else
-        hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, T, kOne, false>), grid, block, 0, stream, a);
+    const int64_t blocks = (int64_t)a.batch * a.row_tiles * a.c.heads * a.chunks, most = 1 << 23;
+    const dim3 block(64 * kWaves);
+    for (int64_t b0 = 0; b0 < blocks; b0 += most) {  // a grid holds fewer than 2^32 lanes
+        KvAttnArgs x = a;
+        x.block0 = (uint32_t)b0;
+        const dim3 grid((unsigned)(blocks - b0 < most ? blocks - b0 : most));
+        if (scored_call(a))
+            hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, T, kOne, true>), grid, block, 0, stream, x);
+        else
+            hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, T, kOne, false>), grid, block, 0, stream, x);
+    }
 }
 
 template <bool kBf16, int NB, int T>

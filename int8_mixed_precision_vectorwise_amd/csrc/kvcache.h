@@ -61,6 +61,7 @@ struct KvAttnArgs {
     int32_t chunk_tiles, chunks;     // most key tiles of a part, most parts of a segment (kv head of a row tile)
     int32_t slot_rows;               // rows that a part leaves (up to tile_rows)
     int32_t join_rows, join_groups;  // rows of a workgroup of the join, its workgroups for a segment
+    uint32_t block0;                 // first workgroup of the launch
     float* part;                     // [segments][chunks][slot_rows][head_dim] partial sums
     float* part_ml;                  // [segments][chunks][slot_rows][maximum, sum]
 };

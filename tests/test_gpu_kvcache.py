@@ -6,11 +6,14 @@ named slots changed) and what is read back.
 Attention, element by element, from the roundings it has (u = 2^-11 for fp16, 2^-8
 for bfloat16, the unit roundoff of the output and of the weights e^s A):
   |out - oracle| <= u |out| + (u + 2 e) sum_j p_j |v_j| + t,  |lse - oracle| <= e + 2^-21 |lse|
+(fp16 rounds e^s and then e^s A, so one u for both is less than their worst case)
 with t = 2^-24 sum of the type's smallest steps (fp16 only) and e the error of a
 score in fp32: products of up to 256 terms, summed in any order, err by at most
 2^-24 * 260 of scale * sum |q||k'|; 2^-20 covers the exponential, 2^-20 cap the tanh,
 2^-22 of the largest distance term the bias.
 """
+
+import ctypes
 
 import numpy as np
 import pytest
@@ -18,6 +21,7 @@ import torch
 
 import int8_mixed_precision_vectorwise_amd as i8
 from gpu_util import host, say
+from int8_mixed_precision_vectorwise_amd import _lib
 from oracle import kvcache as kv
 
 pytestmark = pytest.mark.gpu
@@ -135,6 +139,93 @@ def test_write_from_strided_views():
     want = np.full_like(host(a.data), 0xA5)
     kv.write(want, page, x[:, heads:2 * heads], x[:, 2 * heads:], host(slots), "f16")
     assert np.array_equal(host(a.data), want) and np.array_equal(host(b.data), want)
+
+
+@pytest.mark.parametrize("start", range(8))
+def test_runs_that_start_inside_a_group_of_four(start):
+    """Runs of tokens whose slots are consecutive from any place, with gaps and the runs' joints inside spans of 32."""
+    rng = np.random.default_rng([66, start])
+    heads, d, page, pages, kind = 3, 64, 16, 14, "f16"
+    order = rng.permutation(pages)
+    at = np.concatenate([np.arange(70) + start, np.arange(29) + 90 + (start * 3) % 7, np.arange(33) + 140])
+    slots = order[at // page] * page + at % page
+    slots[[1, 31, 32, 69]] = -1
+    slots[50] = pages * page + 3
+    n = len(slots)
+    k, v = draw(rng, (n, heads, d), kind), draw(rng, (n, heads, d), kind)
+    say(f"fp4_cache_write of runs from {start}")
+    c = make_cache(pages, heads, d, page, kind)
+    want = host(c.data).copy()
+    kv.write(want, page, k, v, slots, kind)
+    st = dev(slots, torch.int64)
+    i8.fp4_cache_write(c, dev16(k, kind), dev16(v, kind), st)
+    got = i8.fp4_cache_read(c, st, torch.float32)
+    torch.cuda.synchronize()
+    assert np.array_equal(host(c.data), want)
+    for g, r in zip(got, kv.read(want, page, d, slots, kind)):
+        assert np.array_equal(wide(g).view(np.int32), np.asarray(r, np.float32).view(np.int32))
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_calls_larger_than_the_last_level_cache(kind):
+    """One call that moves more than 256 MiB gives the bytes and values of small calls (which other tests pin)."""
+    heads, d, page, n = 40, 256, 128, 6001
+    gen = torch.Generator(device="cuda").manual_seed(67)
+    k, v = (torch.randn((n, heads, d), generator=gen, device="cuda").to(DTYPE[kind]) for _ in range(2))
+    slots = torch.arange(n, device="cuda") + 2
+    slots[700] = -1
+    say(f"fp4_cache_write and read of {n} tokens of {heads} heads of {d}, {kind}")
+    a, b = (make_cache(-(-(n + 2) // page), heads, d, page, kind) for _ in range(2))
+    i8.fp4_cache_write(a, k, v, slots)
+    for i in range(0, n, 997):
+        i8.fp4_cache_write(b, k[i:i + 997], v[i:i + 997], slots[i:i + 997])
+    torch.cuda.synchronize()
+    assert torch.equal(a.data, b.data)
+    for dtype in (torch.float32, DTYPE[kind]):
+        whole = i8.fp4_cache_read(a, slots, dtype)
+        for i in range(0, n, 997):
+            for x, y in zip(whole, i8.fp4_cache_read(a, slots[i:i + 997], dtype)):
+                assert torch.equal(x[i:i + 997], y)
+
+
+def test_calls_of_more_than_one_launch():
+    """Heads and tokens of more than 2^22 workgroups.  Rows that overlap keep the buffers small: every token's keys
+    are those of the one before it, moved by a head; the read is of empty slots, which are zeros."""
+    heads, d, n = 32768, 256, 4300
+    assert -(-n // 32) * 9 * (heads * 32 // 256) > 1 << 22
+    gen = torch.Generator(device="cuda").manual_seed(68)
+    flat = torch.randn((n + heads) * d, generator=gen, device="cuda").half()
+    k = flat.as_strided((n, heads, d), (d, d, 1))
+    keep = [0, 1, 2, 3, 1000, 3615, 3616, 3700, n - 2, n - 1]
+    slots = torch.full((n,), -1, dtype=torch.int64, device="cuda")
+    slots[keep] = torch.arange(len(keep), device="cuda") + 3
+    say(f"fp4_cache_write of {n} tokens of {heads} heads of {d}")
+    a, b = (make_cache(1, heads, d, 16, "f16") for _ in range(2))
+    i8.fp4_cache_write(a, k, k, slots)
+    i8.fp4_cache_write(b, k[keep].contiguous(), k[keep].contiguous(), slots[keep])
+    torch.cuda.synchronize()
+    assert torch.equal(a.data, b.data)
+    out = torch.full(((n + heads - 1) * d + 64,), 7.0, dtype=torch.float16, device="cuda")
+    none = torch.full((n,), -1, dtype=torch.int64, device="cuda")
+    c = a.struct()
+    say("fp4_cache_read of the same size")
+    status = _lib.lib().i8mp_fp4_cache_read(ctypes.byref(c), none.data_ptr(), n, 0, out.data_ptr(), d, d, out.data_ptr(), d,
+                                            d, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert status == 0 and bool((out[:-64] == 0).all()) and bool((out[-64:] == 7.0).all())
+
+
+def test_attention_of_more_than_one_launch():
+    """A bound on the queries that lays out more than 2^23 workgroups for each sequence."""
+    lens, heads, group, d = [(5, 50), (3, 33)], 4, 2, 64
+    c, table, lengths, seqs = build(lens, heads, group, d, 16, "f16", 26)
+    max_q = 1 << 26
+    assert -(-max_q * group // 48) * heads > 1 << 23
+    say("fp4_cache_attention with a large bound on the queries")
+    out, lse = i8.fp4_cache_attention(dev16(np.concatenate([s[0] for s in seqs]), "f16"), c, table, lengths,
+                                      dev(np.array([0, 5, 8]), torch.int32), max_q, return_lse=True)
+    torch.cuda.synchronize()
+    check(out, lse, seqs, d ** -0.5, "f16")
 
 
 def test_slots_past_32_bit_offsets():

@@ -94,7 +94,8 @@ def test_attention_validation(L):
                 dict(tokens=4), dict(batch=-1), dict(q_heads=3), dict(q_heads=0), dict(q_heads=1 << 17), dict(max_q=0),
                 dict(max_len=513), dict(max_len=-1), dict(window=-1), dict(table_cols=-1), dict(ldt=7),
                 dict(scale=float("nan")), dict(softcap=-1.0), dict(softcap=float("inf")),
-                dict(max_len=(1 << 30) + 1, table_cols=1 << 30, ldt=1 << 30)):
+                dict(max_len=(1 << 30) + 1, table_cols=1 << 30, ldt=1 << 30),
+                dict(q_offsets=A16, max_q=1 << 30), dict(q_offsets=A16, max_q=1 << 29, batch=32, tokens=32)):
         assert status(**bad) == EINVAL, bad
     assert status(batch=0, tokens=0, q=None, out=None) == OK
     assert status(batch=2, tokens=0, q_offsets=A16, q=None, out=None) == OK
