@@ -329,15 +329,17 @@ typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 // How weights are kept in the 16-bit type's range.  A row's reference is a maximum that
 // stays as it was until a score passes it by 2^kSlack, so that few tiles rescale (2048
 // queries behind 2048 tokens, 64 / 8 heads of 128, bfloat16: 268 us, 312 with no slack).
-// fp16: weights are 2^k times e^(s - reference), k = 8 - e with 2^e above every A the
-// wave has met (e >= 0; a larger A than before takes a smaller k and a rescale).  They
-// then stay below 2^(k + 7) and their products with A below 2^15, and a key's product
-// is kept down to 2^-25 where a scale of 1 has 2^8: few keys of small values may draw
-// nearly all the weight, beside large values that draw little.
+// In fp16 weights are 2^4 times e^(s - reference), at most 2^11 so, and the scales A
+// that they meet are taken times 2^(4 - e), 2^e the first power above every finite A the
+// wave has met (a larger one than before rescales the sums).  Products are then below
+// 2^15 whatever the values' size; a weight is rounded at 2^-29 of the reference's and a
+// scale at 2^-29 of the largest, so that the keys that draw the weight may have values
+// 2^17 below others that draw none.
 template <bool kBf16>
 constexpr float kSlack = kBf16 ? 8.0f : 7.0f;
-__device__ inline int weight_shift(int e) { return 8 - e; }
-constexpr int kFirstLarge = 0;
+template <bool kBf16>
+constexpr float kShift = kBf16 ? 0.0f : 4.0f;
+constexpr int kLeastLarge = -11;  // 2^(4 - e) is an fp16 number
 
 // The products P A of a lane's 8 weights with a block's scales, in the order of the
 // keys.  bfloat16: fp32 products, rounded once, as the output is.  fp16: the weights are
@@ -347,7 +349,7 @@ constexpr int kFirstLarge = 0;
 template <bool kBf16, int NB>
 struct Weights {
     uint32_t a[2][2 * NB];
-    __device__ Weights(const uint32_t (&vs)[2][2 * NB]) {
+    __device__ void take(const uint32_t (&vs)[2][2 * NB], int) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -365,7 +367,8 @@ struct Weights {
 template <int NB>
 struct Weights<false, NB> {
     Half<false>::v2 a[2][2][NB];  // half, pair of keys, block
-    __device__ Weights(const uint32_t (&vs)[2][2 * NB]) {
+    __device__ void take(const uint32_t (&vs)[2][2 * NB], int e) {
+        const _Float16 f = (_Float16)__builtin_amdgcn_exp2f((float)(4 - e));
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -374,7 +377,7 @@ struct Weights<false, NB> {
                 for (int b = 0; b < NB; ++b) {
                     const int j = 2 * i * NB + b, k = j + NB;  // block b of keys 2 i and 2 i + 1
                     const uint32_t lo = (vs[u][j >> 1] >> (16 * (j & 1))) & 0xffffu, hi = vs[u][k >> 1] >> (16 * (k & 1));
-                    a[u][i][b] = __builtin_bit_cast(Half<false>::v2, lo | hi << 16);
+                    a[u][i][b] = __builtin_bit_cast(Half<false>::v2, lo | hi << 16) * Half<false>::v2{f, f};
                 }
     }
     __device__ Half<false>::v8 times(const float (&w)[2][4], int b) const {
@@ -387,6 +390,56 @@ struct Weights<false, NB> {
         return Half<false>::v8{r[0].x, r[0].y, r[1].x, r[1].y, r[2].x, r[2].y, r[3].x, r[3].y};
     }
 };
+
+// Makes a tile's scales of V ready for the products with the weights.  `masked`: some of
+// its keys may lie past the sequence's end (the lane's i-th of half u does if 16 u + i >=
+// left) or on no page.
+template <bool kBf16, int NB, int T>
+__device__ inline __attribute__((always_inline)) void take_scales(Weights<kBf16, NB>& scales, uint32_t (&vs)[2][2 * NB],
+                                                                  v4f (&acc)[T][NB][4], int& large, bool masked,
+                                                                  bool live0, bool live1, int left) {
+    if (masked) {
+        // what a page holds past a sequence's end may be anything: its scales are taken as 0
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int bb = 0; bb < NB; ++bb) {
+                    const int w = i * NB + bb;
+                    const bool keep = (16 * u + i < left) & (u ? live1 : live0);
+                    vs[u][w >> 1] = keep ? vs[u][w >> 1] : vs[u][w >> 1] & (w & 1 ? 0xffffu : 0xffff0000u);
+                }
+    }
+    if constexpr (!kBf16) {  // an A past those met so far
+        us2 big = __builtin_bit_cast(us2, vs[0][0]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i) big = __builtin_elementwise_max(big, __builtin_bit_cast(us2, vs[u][i]));
+        const int top_bits = big.x > big.y ? big.x : big.y, limit = (large + 15) << 10;  // 2^large
+        if (__ballot(top_bits >= limit)) {
+            us2 fin = {0, 0};  // numbers moved up to 0x8400 and past it, the rest below
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 2 * NB; ++i)
+                    fin = __builtin_elementwise_max(fin, __builtin_bit_cast(us2, vs[u][i]) + us2{0x8400, 0x8400});
+            const int top_finite = fin.x > fin.y ? fin.x : fin.y;
+            int now = ((int)column_max((float)top_finite) - 0x8400 >> 10) - 14;
+            now = now > large ? now : large;
+            const float drop = __builtin_amdgcn_exp2f((float)(large - now));
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int bb = 0; bb < NB; ++bb)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[t][bb][j] *= drop;
+            large = now;
+        }
+    }
+    scales.take(vs, large);
+}
 
 // One workgroup: one sequence, kv head, row tile of 16 T query rows (token-major,
 // then the heads of the group) and a run of key tiles, which its waves take in turn.
@@ -420,6 +473,10 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
     typedef typename H::v8 v8;
     typedef Stage<NB, kOne> St;
     constexpr int R = kRing<NB>();
+    // V's scales are made ready before the scores or after them: before, with fp16 and
+    // kScored, where 101 registers spilled after (six pieces of prompts of up to 3701 tokens,
+    // 32 / 8 heads of 128: 270 us and 231); else after (181 us and 192)
+    constexpr bool kEarly = !kBf16 && kScored;
     // one LDS array: the waves' rings, later their sums [wave][row][64 NB + 4] and maxima
     // (a second object would make the compiler wait for every DMA before an LDS read)
     constexpr int kRows = kCols * T;
@@ -515,7 +572,7 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
     // exponent past which the reference moves (any, for a row that has seen no key yet);
     // the sum of this lane's weights
     float nb[T], thr[T], l[T];
-    int large = kFirstLarge;         // fp16: every A that the wave has met is below 2^large
+    int large = kLeastLarge;         // fp16: every A that the wave has met is below 2^large
     v4f acc[T][NB][4];
 #pragma unroll
     for (int t = 0; t < T; ++t) {
@@ -555,6 +612,12 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
             }
             stage = stage + 1 < R ? stage + 1 : 0;
         }
+        // every key of the tile visible to every row: no masks
+        const bool whole = live0 & live1 & (pos0 >= 0) &
+                           ((t0 + kTile <= s.prefix) |
+                            ((t0 + kTile - 1 <= pos0) & ((a.window == 0) | (pos1 - t0 < a.window))));
+        Weights<kBf16, NB> scales;
+        if constexpr (kEarly) take_scales<kBf16, NB, T>(scales, vs, acc, large, !whole, live0, live1, s.length - t0 - 4 * g);
         float x[T][2][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -619,10 +682,6 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
                 }
             }
         }
-        // every key of the tile visible to every row: no masks
-        const bool whole = live0 & live1 & (pos0 >= 0) &
-                           ((t0 + kTile <= s.prefix) |
-                            ((t0 + kTile - 1 <= pos0) & ((a.window == 0) | (pos1 - t0 < a.window))));
         if (!whole) {
 #pragma unroll
             for (int t = 0; t < T; ++t)
@@ -637,49 +696,8 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
                                          (u ? live1 : live0);
                         x[t][u][i] = see ? x[t][u][i] : -INFINITY;
                     }
-            // what a page holds past a sequence's end may be anything: its scales are taken as 0
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int bb = 0; bb < NB; ++bb) {
-                        const int w = i * NB + bb;
-                        const bool keep = (t0 + 16 * u + 4 * g + i < s.length) & (u ? live1 : live0);
-                        vs[u][w >> 1] = keep ? vs[u][w >> 1] : vs[u][w >> 1] & (w & 1 ? 0xffffu : 0xffff0000u);
-                    }
         }
-        if constexpr (!kBf16) {  // an A past those met so far takes another shift
-            us2 big = __builtin_bit_cast(us2, vs[0][0]);
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 2 * NB; ++i) big = __builtin_elementwise_max(big, __builtin_bit_cast(us2, vs[u][i]));
-            const int top_bits = big.x > big.y ? big.x : big.y, limit = (large + 15) << 10;  // 2^large
-            if (__ballot(top_bits >= limit)) {
-                const int now = ((int)column_max((float)top_bits) >> 10) - 14;
-                const float drop = __builtin_amdgcn_exp2f((float)(large - now));
-#pragma unroll
-                for (int t = 0; t < T; ++t) {
-                    l[t] *= drop;
-                    if (thr[t] != -INFINITY) {  // this tile's scores have the old shift in them
-                        nb[t] += (float)(large - now);
-                        thr[t] += (float)(large - now);
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) x[t][u][i] += (float)(large - now);
-                    }
-#pragma unroll
-                    for (int bb = 0; bb < NB; ++bb)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[t][bb][j] *= drop;
-                }
-                large = now;
-            }
-        }
-        const float shift = kBf16 ? 0.0f : (float)weight_shift(large);
-        const Weights<kBf16, NB> scales(vs);
+        if constexpr (!kEarly) take_scales<kBf16, NB, T>(scales, vs, acc, large, !whole, live0, live1, s.length - t0 - 4 * g);
         v8 pa[T][NB];
 #pragma unroll
         for (int t = 0; t < T; ++t) {
@@ -692,10 +710,10 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
                 top = column_max(top);
                 const bool fresh = thr[t] == -INFINITY;
                 // (a fresh row with no key in sight stays as it is)
-                float by = top - shift;
+                float by = top - kShift<kBf16>;
                 by = fresh ? (top == -INFINITY ? 0.0f : by) : fmaxf(by, 0.0f);
                 const float drop = fresh ? 0.0f : __builtin_amdgcn_exp2f(-by);
-                thr[t] = fresh & (top == -INFINITY) ? thr[t] : shift + kSlack<kBf16>;
+                thr[t] = fresh & (top == -INFINITY) ? thr[t] : kShift<kBf16> + kSlack<kBf16>;
                 nb[t] -= by;
                 l[t] *= drop;
 #pragma unroll
@@ -759,6 +777,7 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
     float2 (*ml)[kCols] = reinterpret_cast<float2 (*)[kCols]>(smem + sizeof(smem) - kWaves * kCols * 8);
     const int cr = tid >> 4, d0 = tid & 15;  // 16 lanes a row, 4 dims a step
     wait_loads<0>();  // this wave's DMA has landed; after the barrier every wave's
+    const float grow = kBf16 ? 1.0f : __builtin_amdgcn_exp2f((float)(large - 4));
 #pragma unroll
     for (int t = 0; t < T; ++t) {
     const float ls = column_sum(l[t]);
@@ -769,7 +788,7 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<v4f*>(&part[wave][c][64 * bb + 4 * (4 * g + i)]) =
-                v4f{acc[t][bb][0][i], acc[t][bb][1][i], acc[t][bb][2][i], acc[t][bb][3][i]};
+                v4f{acc[t][bb][0][i], acc[t][bb][1][i], acc[t][bb][2][i], acc[t][bb][3][i]} * grow;
     if (g == 0) ml[wave][c] = make_float2(ms, ls);
     __syncthreads();
     const int orow = r0 + kCols * t + cr;

@@ -384,6 +384,51 @@ def test_keys_split_over_workgroups(lens):
     attend(lens, 1, 2, 64, 64, "f16", 12, window=3000, prefix=[100] * len(lens))
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("scores", ["rising", "falling", "one"])
+@pytest.mark.parametrize("values", ["rising", "falling", "last", "small"])
+def test_sizes_that_change_along_a_sequence(values, scores, kind):
+    """Scores and values that grow or fall along the keys, so that maxima and the values' range move all the way."""
+    rng = np.random.default_rng(27)
+    heads, group, d, page, n = 2, 1, 64, 32, 700
+    for queries in (1, 40):
+        j = np.arange(n) / (n - 1)
+        up = {"rising": j * 12 - 6, "falling": 6 - 12 * j, "last": np.where(np.arange(n) == n - 1, 13.0, -3.0),
+              "small": np.full(n, -13.0)}[values]
+        q = draw(rng, (queries, heads, d), kind, 0.1)
+        along = q[0, 0] / np.abs(q[0, 0]).max()
+        lean = {"rising": 40 * j - 20, "falling": 20 - 40 * j, "one": np.where(np.arange(n) == 333, 20.0, 0.0)}[scores]
+        k = kv.round16(lean[:, None, None] * along * 0.3 + 0.2 * rng.standard_normal((n, heads, d)), kind)
+        v = kv.round16(rng.standard_normal((n, heads, d)) * np.exp2(up)[:, None, None], kind)
+        c = make_cache(-(-n // page), heads, d, page, kind)
+        table = dev(np.arange(-(-n // page))[None], torch.int32)
+        say(f"fp4_cache_attention with {values} values and {scores} scores, {queries} queries, {kind}")
+        i8.fp4_cache_write(c, dev16(k, kind), dev16(v, kind), torch.arange(n, device="cuda"))
+        out, lse = i8.fp4_cache_attention(dev16(q, kind), c, table, dev(np.array([n]), torch.int32), max_q=queries,
+                                          return_lse=True)
+        torch.cuda.synchronize()
+        check(out, lse, [(q, kv.dequantize(*kv.quantize(k)), kv.dequantize(*kv.quantize(v)))], d ** -0.5, kind)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_not_numbers_stay_where_they_are(kind):
+    """A block of V that holds an infinity, at a key in sight: the other heads and blocks are as without it."""
+    rng = np.random.default_rng(28)
+    heads, d, page, n = 2, 128, 16, 90
+    q, k, v = draw(rng, (3, heads, d), kind), draw(rng, (n, heads, d), kind, 0.3), draw(rng, (n, heads, d), kind)
+    table = dev(np.arange(6)[None], torch.int32)
+    outs = []
+    say(f"fp4_cache_attention beside an infinity {kind}")
+    for bad in (False, True):
+        c = make_cache(6, heads, d, page, kind)
+        if bad:
+            v[40, 1, 70] = np.inf
+        i8.fp4_cache_write(c, dev16(k, kind), dev16(v, kind), torch.arange(n, device="cuda"))
+        outs.append(wide(i8.fp4_cache_attention(dev16(q, kind), c, table, dev(np.array([n]), torch.int32), max_q=3)))
+    assert np.array_equal(outs[0][:, 0], outs[1][:, 0]) and np.array_equal(outs[0][:, 1, :64], outs[1][:, 1, :64])
+    assert not np.isfinite(outs[1][:, 1, 64:]).any()
+
+
 def test_strides_orders_and_out():
     """q and out as views (a fused projection's output, head-major), one kv head of a query count that is odd."""
     lens, heads, group, d = [(3, 50), (5, 33)], 2, 3, 128
