@@ -7,13 +7,23 @@ namespace i8mp {
 namespace {
 
 // How the keys are cut.  A part costs its workgroup a prologue and epilogue of about
-// 4 us and the join its sums, so there are no more parts than fill the chip once (one
-// sequence: all parts are alike) or twice (several, which may differ in length: 64
-// sequences of 2048 to 8192 tokens, 64 / 8 heads of 128, took 89 us at 0.75, 80 at 2
+// 4 us and the join its launch and sums, so there are no more parts than fill the chip
+// once (one sequence: all parts are alike) or twice (several, which may differ in length:
+// 64 sequences of 2048 to 8192 tokens, 64 / 8 heads of 128, took 89 us at 0.75, 80 at 2
 // and 78 us at 4 times the chip's 1024 workgroups; equal ones 109, 113 and 116; one
-// sequence of 131072 tokens 29, 32 and 39).  Up to kWhole tiles are not cut: the
-// second launch costs more than a longer loop.
-constexpr int kWhole = 16;
+// sequence of 131072 tokens 29, 32 and 39).
+//
+// Contexts of up to whole_tiles() are not cut, the join costs more than a longer loop.  Few
+// segments (one kv head of one row tile each) leave most CUs idle so, and the limit is low
+// (8 of them, 1024 tokens: 10.2 us whole, 11.9 cut; 2048: 15.1 and 12.0); many fill the
+// chip whole (128 of 2048 tokens: 16 and 21 us; 256 of 4096: 27 and 33).  Whole contexts
+// of up to 256 segments take workgroups of 8 waves (256 of 2048 tokens: 17.9 us, 19.8
+// with 4, 20.2 with 16; 512: 29.4 and 27.9).  Row tiles of several sets of rows (T > 1):
+// 176 segments of 1000 tokens 21 us whole, 29 and 5 cut, 64 of 4000 49 us, 24 and 5.
+int whole_tiles(int64_t segments, int T, int NB) {
+    const int n = segments < 64 ? 32 : segments < 128 || T > 1 ? 64 : 128;
+    return NB == 4 ? n / 2 : n;
+}
 
 void plan(KvAttnArgs& a) {
     const int64_t rows = (int64_t)a.max_q * a.group;
@@ -28,15 +38,18 @@ void plan(KvAttnArgs& a) {
     const int64_t chip = 256 * workgroups(NB, T);
     const int64_t tiles = ceil_div(near, kTile), most = ceil_div(a.prefix ? a.max_len : near, kTile);
     int64_t per = ceil_div(tiles * segments, a.batch > 1 ? 2 * chip : chip);
-    per = per < kWaves ? kWaves : per;
-    if (most <= kWhole || segments >= 4 * chip) per = most > 0 ? most : 1;
+    per = per < 4 ? 4 : per;
+    if (most <= whole_tiles(segments, T, NB) || segments >= 4 * chip) per = most > 0 ? most : 1;
     a.chunk_tiles = (int32_t)per;
     a.chunks = (int32_t)ceil_div(most > 0 ? most : 1, per);
+    a.waves = T == 1 && a.chunks == 1 && segments <= 256 && most >= 8 ? 8 : 4;
     a.slot_rows = (int32_t)(rows < a.tile_rows ? rows : a.tile_rows);
     a.join_rows = 1;
-    // few segments: their many parts are shared by a workgroup for each row; many: few
-    // parts each, and a workgroup takes all the rows there are
-    while (segments >= 256 && a.join_rows < 16 && a.join_rows < a.slot_rows) a.join_rows *= 2;
+    // a row's parts are shared by as many sets of lanes as have two each (one workgroup a row
+    // whatever the parts: 10 to 21 us for 64 to 176 segments of 48 rows, so 5); with many
+    // segments there are rows enough, and a workgroup takes all it can
+    while (a.join_rows < 16 && a.join_rows < a.slot_rows && (segments >= 256 || 16 / a.join_rows * 2 > a.chunks))
+        a.join_rows *= 2;
     a.join_groups = (int32_t)ceil_div(a.slot_rows, a.join_rows);
 }
 

@@ -15,7 +15,6 @@ namespace i8mp {
 
 namespace {
 
-constexpr int kWaves = 4;       // waves of a workgroup, each taking every kWaves-th key tile
 constexpr int kTile = 32;       // keys of a tile
 constexpr int kCols = 16;       // query rows of an MFMA's columns; a row tile has T times as many
 constexpr float kLog2e = 1.4426950408889634f;
@@ -142,18 +141,18 @@ struct Place {
     bool live[kOne ? 1 : 2];              // the page id was in range
 };
 
-// The pages of up to 64 of a wave's tiles, n, n + kWaves, ...: lane i loads those of
+// The pages of up to 64 of a wave's tiles, n, n + W, ... (W waves): lane i loads those of
 // the i-th, so that a tile's address later takes a lane read and no load.
 template <bool kOne>
 struct Pages {
     int32_t id[kOne ? 1 : 2];
 };
 
-template <bool kOne>
+template <bool kOne, int W>
 __device__ inline Pages<kOne> load_pages(const KvAttnArgs& a, const int32_t* table, const Span& span, int n, int n1,
                                          int length, int lane) {
     Pages<kOne> p;
-    const int nn = n + lane * kWaves;
+    const int nn = n + lane * W;
     const int t0 = tile_token(span, nn < n1 ? nn : n);
 #pragma unroll
     for (int u = 0; u < (kOne ? 1 : 2); ++u) {
@@ -467,8 +466,8 @@ constexpr int workgroups(int NB, int T) { return NB == 4 ? 2 : T == 1 ? 4 : NB =
 template <int NB>
 constexpr int kRing() { return NB == 1 ? 4 : 2; }
 
-template <bool kBf16, int NB, int T, bool kOne, bool kScored>
-__global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_kernel(KvAttnArgs a) {
+template <bool kBf16, int NB, int T, int W, bool kOne, bool kScored>
+__global__ __launch_bounds__(64 * W, workgroups(NB, T) * 4 / W) void kv_attention_kernel(KvAttnArgs a) {
     typedef Half<kBf16> H;
     typedef typename H::v8 v8;
     typedef Stage<NB, kOne> St;
@@ -480,8 +479,8 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
     // one LDS array: the waves' rings, later their sums [wave][row][64 NB + 4] and maxima
     // (a second object would make the compiler wait for every DMA before an LDS read)
     constexpr int kRows = kCols * T;
-    constexpr int kPart = kWaves * kCols * (64 * NB + 4) * 4, kRings = kWaves * R * St::kBytes;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[(kPart > kRings ? kPart : kRings) + kWaves * kCols * 8];
+    constexpr int kPart = W * kCols * (64 * NB + 4) * 4, kRings = W * R * St::kBytes;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[(kPart > kRings ? kPart : kRings) + W * kCols * 8];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c = lane & 15, g = lane >> 4;
@@ -534,17 +533,17 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
     int first = n0 + wave;
     // requests tile n into a stage, `place` tiles ahead of the one in use
     const auto ask = [&](int n, int stage, int place) {
-        int slot = (n - first) / kWaves;
+        int slot = (n - first) / W;
         const Place<kOne> w = place_of<NB, kOne>(a, pages, slot, h, tile_token(span, n));
         live |= ((uint32_t)w.live[0] | (uint32_t)w.live[kOne ? 0 : 1] << 1) << (2 * place);
         request<NB, kOne>(w, ring + stage * St::kBytes, lane, at_v, at_s);
     };
-    const int last = n0 + wave + (n1 - 1 - n0 - wave) / kWaves * kWaves;  // the wave's last tile, if it has any
+    const int last = n0 + wave + (n1 - 1 - n0 - wave) / W * W;  // the wave's last tile, if it has any
     if (first < n1) {
-        pages = load_pages<kOne>(a, table, span, first, n1, s.length, lane);
+        pages = load_pages<kOne, W>(a, table, span, first, n1, s.length, lane);
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            if (first + i * kWaves <= last) ask(first + i * kWaves, i, i);
+            if (first + i * W <= last) ask(first + i * W, i, i);
     }
 
     // a factor below 0 is taken into q's sign
@@ -586,7 +585,7 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
     }
 
     int stage = 0;
-    for (int n = first; n < n1; n += kWaves) {
+    for (int n = first; n < n1; n += W) {
         const int t0 = tile_token(span, n);
         const bool live0 = live & 1, live1 = live & 2;
         live >>= 2;
@@ -594,7 +593,7 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
         uint32_t ks[2][NB * 2];  // scales of keys 16 u + 4 g .. + 3
         uint32_t vc[2][NB * 2];  // values of keys 16 u + 4 g .. + 3: dims 64 b + 4 c .. + 3
         uint32_t vs[2][NB * 2];
-        if (n + (R - 1) * kWaves <= last)
+        if (n + (R - 1) * W <= last)
             wait_loads<(R - 1) * St::kIns>();  // the tiles requested after it stay in flight
         else
             wait_loads<0>();
@@ -602,11 +601,11 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
             const uint32_t st = ring_at + stage * St::kBytes;
             read_share(kc, vc, ks, vs, st + (c * 32 + g * 8) * NB, st + 1024 * NB + (g * 128 + c * 8) * NB,
                        st + St::kScales + g * 8 * NB);
-            const int nn = n + R * kWaves;
+            const int nn = n + R * W;
             if (nn <= last) {
-                if ((nn - first) / kWaves >= 64) {
+                if ((nn - first) / W >= 64) {
                     first = nn;
-                    pages = load_pages<kOne>(a, table, span, first, n1, s.length, lane);
+                    pages = load_pages<kOne, W>(a, table, span, first, n1, s.length, lane);
                 }
                 ask(nn, stage, R - 1);
             }
@@ -774,8 +773,8 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
 
     // join the waves, 16 rows at a time: O^T row 4 g + i of acc[bb][j] is dim 64 bb + 4 (4 g + i) + j
     float (*part)[kCols][64 * NB + 4] = reinterpret_cast<float (*)[kCols][64 * NB + 4]>(smem);
-    float2 (*ml)[kCols] = reinterpret_cast<float2 (*)[kCols]>(smem + sizeof(smem) - kWaves * kCols * 8);
-    const int cr = tid >> 4, d0 = tid & 15;  // 16 lanes a row, 4 dims a step
+    float2 (*ml)[kCols] = reinterpret_cast<float2 (*)[kCols]>(smem + sizeof(smem) - W * kCols * 8);
+    const int cr = (tid >> 4) & 15, d0 = tid & 15;  // 16 lanes a row, 4 dims a step
     wait_loads<0>();  // this wave's DMA has landed; after the barrier every wave's
     const float grow = kBf16 ? 1.0f : __builtin_amdgcn_exp2f((float)(large - 4));
 #pragma unroll
@@ -793,11 +792,11 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
     __syncthreads();
     const int orow = r0 + kCols * t + cr;
     if (orow < r1) {
-        float mm = -INFINITY, ll = 0.0f, f[kWaves];
+        float mm = -INFINITY, ll = 0.0f, f[W];
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, ml[w][cr].x);
+        for (int w = 0; w < W; ++w) mm = fmaxf(mm, ml[w][cr].x);
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < W; ++w) {
             f[w] = ml[w][cr].x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[w][cr].x - mm);
             ll = fmaf(ml[w][cr].y, f[w], ll);
         }
@@ -807,10 +806,10 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
         const int64_t slot = ((int64_t)segment * a.chunks + chunk) * a.slot_rows + kCols * t + cr;
         const float norm = parts > 1 ? 1.0f : ll > 0.0f ? 1.0f / (6.0f * ll) : 0.0f;
 #pragma unroll
-        for (int bb = 0; bb < NB; ++bb) {
+        for (int bb = W == 4 ? 0 : tid >> 8; bb < NB; bb += W / 4) {
             v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const v4f y = *reinterpret_cast<const v4f*>(&part[w][cr][64 * bb + 4 * d0]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[j] = fmaf(y[j], f[w], o[j]);
@@ -824,7 +823,7 @@ __global__ __launch_bounds__(64 * kWaves, workgroups(NB, T)) void kv_attention_k
                                                  (typename H::T)(o[2] * norm), (typename H::T)(o[3] * norm)};
             }
         }
-        if (d0 == 0) {
+        if (d0 == 0 && tid < 256) {
             if (parts > 1)
                 reinterpret_cast<float2*>(a.part_ml)[slot] = make_float2(mm, ll);
             else if (a.lse)
@@ -933,40 +932,40 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs a) {
 
 inline bool scored_call(const KvAttnArgs& a) { return a.softcap > 0.0f || a.alibi || fabsf(a.scale) < 1e-30f; }
 
-template <bool kBf16, int NB, int T, bool kOne>
+template <bool kBf16, int NB, int T, int W, bool kOne>
 void launch_main(const KvAttnArgs& a, hipStream_t stream) {
-    const int64_t blocks = (int64_t)a.batch * a.row_tiles * a.c.heads * a.chunks, most = 1 << 23;
-    const dim3 block(64 * kWaves);
+    const int64_t blocks = (int64_t)a.batch * a.row_tiles * a.c.heads * a.chunks, most = ((int64_t)1 << 25) / W;
+    const dim3 block(64 * W);
     for (int64_t b0 = 0; b0 < blocks; b0 += most) {  // a grid holds fewer than 2^32 lanes
         KvAttnArgs x = a;
         x.block0 = (uint32_t)b0;
         const dim3 grid((unsigned)(blocks - b0 < most ? blocks - b0 : most));
         if (scored_call(a))
-            hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, T, kOne, true>), grid, block, 0, stream, x);
+            hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, T, W, kOne, true>), grid, block, 0, stream, x);
         else
-            hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, T, kOne, false>), grid, block, 0, stream, x);
+            hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, T, W, kOne, false>), grid, block, 0, stream, x);
     }
 }
 
-template <bool kBf16, int NB, int T>
+template <bool kBf16, int NB, int T, int W>
 void launch_tiles(const KvAttnArgs& a, hipStream_t stream) {
     if (a.c.page_size >= kTile)
-        launch_main<kBf16, NB, T, true>(a, stream);
+        launch_main<kBf16, NB, T, W, true>(a, stream);
     else
-        launch_main<kBf16, NB, T, false>(a, stream);
+        launch_main<kBf16, NB, T, W, false>(a, stream);
 }
 
 template <bool kBf16, int NB>
 hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
-    if constexpr (NB == 4) {
-        launch_tiles<kBf16, NB, 1>(a, stream);
-    } else {
-        if (a.tile_rows == kCols)
-            launch_tiles<kBf16, NB, 1>(a, stream);
-        else if (a.tile_rows == 2 * kCols)
-            launch_tiles<kBf16, NB, 2>(a, stream);
-        else
-            launch_tiles<kBf16, NB, 3>(a, stream);
+    if (a.tile_rows == kCols && a.waves == 4)
+        launch_tiles<kBf16, NB, 1, 4>(a, stream);
+    else if (a.tile_rows == kCols && a.waves == 8)
+        launch_tiles<kBf16, NB, 1, 8>(a, stream);
+    if constexpr (NB < 4) {
+        if (a.tile_rows == 2 * kCols)
+            launch_tiles<kBf16, NB, 2, 4>(a, stream);
+        else if (a.tile_rows == 3 * kCols)
+            launch_tiles<kBf16, NB, 3, 4>(a, stream);
     }
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (a.chunks > 1) {

@@ -58,6 +58,7 @@ struct KvAttnArgs {
     int64_t max_len;                 // bound on the lengths
     // set by the launcher
     int32_t tile_rows, row_tiles;    // rows of a row tile, row tiles of the longest sequence
+    int32_t waves;                   // waves of a workgroup
     int32_t chunk_tiles, chunks;     // most key tiles of a part, most parts of a segment (kv head of a row tile)
     int32_t slot_rows;               // rows that a part leaves (up to tile_rows)
     int32_t join_rows, join_groups;  // rows of a workgroup of the join, its workgroups for a segment
