@@ -25,6 +25,19 @@ int whole_tiles(int64_t segments, int T, int NB) {
     return NB == 4 ? n / 2 : n;
 }
 
+// Row tiles that there are, where batch * row_tiles counts every sequence as the longest.
+int64_t real_segments(const KvAttnArgs& a) {
+    const int64_t most = (int64_t)a.batch * a.row_tiles, some = a.tokens * a.group / a.tile_rows + a.batch;
+    return (some < most ? some : most) * a.c.heads;
+}
+
+// Prompts of so many row tiles that single waves fill the chip 3/2 times (head_dim 128:
+// 3072 of them) take workgroups of one wave, which has its row tile's keys for itself: a
+// quarter of the prologues, no sums to join.  Waves of 4 / 1, us: 5504 row tiles of a
+// 4096-token prompt 386 / 349, 3520 of 8 prompts of 512 89 / 74, 2752 of a 2048-token
+// one 123 / 115, but 2736 behind 2048 tokens 272 / 276, with a distance bias 369 / 391,
+// and 1500 of ragged pieces 231 / 292.
+// head_dim 64 (3 waves a SIMD): 5504 row tiles 223 / 244, so 4 there.
 void plan(KvAttnArgs& a) {
     const int64_t rows = (int64_t)a.max_q * a.group;
     const int NB = a.c.blocks;
@@ -35,7 +48,7 @@ void plan(KvAttnArgs& a) {
     // keys that a row tile sees: beside a window, those of the prefix are not known here
     int64_t near = a.max_len;
     if (a.window > 0 && a.window + (int64_t)a.max_q + 2 * kTile < near) near = a.window + (int64_t)a.max_q + 2 * kTile;
-    const int64_t chip = 256 * workgroups(NB, T);
+    const int64_t chip = 256 * simd_waves(NB, T);
     const int64_t tiles = ceil_div(near, kTile), most = ceil_div(a.prefix ? a.max_len : near, kTile);
     int64_t per = ceil_div(tiles * segments, a.batch > 1 ? 2 * chip : chip);
     per = per < 4 ? 4 : per;
@@ -43,6 +56,7 @@ void plan(KvAttnArgs& a) {
     a.chunk_tiles = (int32_t)per;
     a.chunks = (int32_t)ceil_div(most > 0 ? most : 1, per);
     a.waves = T == 1 && a.chunks == 1 && segments <= 256 && most >= 8 ? 8 : 4;
+    if (T == 3 && NB == 2 && a.chunks == 1 && real_segments(a) * 2 >= 1024 * simd_waves(NB, T) * 3) a.waves = 1;
     a.slot_rows = (int32_t)(rows < a.tile_rows ? rows : a.tile_rows);
     a.join_rows = 1;
     // a row's parts are shared by as many sets of lanes as have two each (one workgroup a row

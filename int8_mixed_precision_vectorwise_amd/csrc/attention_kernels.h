@@ -455,19 +455,19 @@ __device__ inline __attribute__((always_inline)) void take_scales(Weights<kBf16,
 // epilogue of about 4 us.  Many rows: the VALU, about 75 % busy: converting 4-bit codes
 // (shared by the row tile), masks, exponentials and the scaling of weights take 443
 // instructions for 48 rows of 32 keys beside 48 matrix instructions, which hold the SIMD
-// for about 10 of their 16 cycles each.  A 4096-token prompt of 64 heads of 128: 700
+// for about 10 of their 16 cycles each.  A 4096-token prompt of 64 heads of 128: 780
 // TFLOP/s.
 //
-// workgroups(): those of a CU, by their registers (512 a lane for the waves of a SIMD).
+// simd_waves(): those of a SIMD, by their registers (512 a lane for all of them).
 // T = 3 takes 248 registers with head_dim 128; with 256 two sets of rows already spill.
 // 2048 queries behind 2048 tokens, 64 / 8 heads of 128, bfloat16, in row tiles of 16, 32
 // and 48: 351, 305 and 268 us.
-constexpr int workgroups(int NB, int T) { return NB == 4 ? 2 : T == 1 ? 4 : NB == 1 ? 3 : 2; }
+constexpr int simd_waves(int NB, int T) { return NB == 4 ? 2 : T == 1 ? 4 : NB == 1 ? 3 : 2; }
 template <int NB>
 constexpr int kRing() { return NB == 1 ? 4 : 2; }
 
 template <bool kBf16, int NB, int T, int W, bool kOne, bool kScored>
-__global__ __launch_bounds__(64 * W, workgroups(NB, T) * 4 / W) void kv_attention_kernel(KvAttnArgs a) {
+__global__ __launch_bounds__(64 * W, simd_waves(NB, T)) void kv_attention_kernel(KvAttnArgs a) {
     typedef Half<kBf16> H;
     typedef typename H::v8 v8;
     typedef Stage<NB, kOne> St;
@@ -774,62 +774,66 @@ __global__ __launch_bounds__(64 * W, workgroups(NB, T) * 4 / W) void kv_attentio
     // join the waves, 16 rows at a time: O^T row 4 g + i of acc[bb][j] is dim 64 bb + 4 (4 g + i) + j
     float (*part)[kCols][64 * NB + 4] = reinterpret_cast<float (*)[kCols][64 * NB + 4]>(smem);
     float2 (*ml)[kCols] = reinterpret_cast<float2 (*)[kCols]>(smem + sizeof(smem) - W * kCols * 8);
-    const int cr = (tid >> 4) & 15, d0 = tid & 15;  // 16 lanes a row, 4 dims a step
+    const int d0 = tid & 15;  // 16 lanes a row, 4 dims a step
     wait_loads<0>();  // this wave's DMA has landed; after the barrier every wave's
     const float grow = kBf16 ? 1.0f : __builtin_amdgcn_exp2f((float)(large - 4));
 #pragma unroll
     for (int t = 0; t < T; ++t) {
-    const float ls = column_sum(l[t]);
-    const float ms = thr[t] == -INFINITY ? -INFINITY : -nb[t];
-    __syncthreads();  // the rings, or the rows before these, are out of use
+        const float ls = column_sum(l[t]);
+        const float ms = thr[t] == -INFINITY ? -INFINITY : -nb[t];
+        __syncthreads();  // the rings, or the rows before these, are out of use
 #pragma unroll
-    for (int bb = 0; bb < NB; ++bb)
+        for (int bb = 0; bb < NB; ++bb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<v4f*>(&part[wave][c][64 * bb + 4 * (4 * g + i)]) =
-                v4f{acc[t][bb][0][i], acc[t][bb][1][i], acc[t][bb][2][i], acc[t][bb][3][i]} * grow;
-    if (g == 0) ml[wave][c] = make_float2(ms, ls);
-    __syncthreads();
-    const int orow = r0 + kCols * t + cr;
-    if (orow < r1) {
-        float mm = -INFINITY, ll = 0.0f, f[W];
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<v4f*>(&part[wave][c][64 * bb + 4 * (4 * g + i)]) =
+                    v4f{acc[t][bb][0][i], acc[t][bb][1][i], acc[t][bb][2][i], acc[t][bb][3][i]} * grow;
+        if (g == 0) ml[wave][c] = make_float2(ms, ls);
+        __syncthreads();
+        // fewer than 4 waves take the 16 rows in turns, more share the blocks of a row
 #pragma unroll
-        for (int w = 0; w < W; ++w) mm = fmaxf(mm, ml[w][cr].x);
+        for (int cr = (tid >> 4) & 15; cr < kCols; cr += 4 * W) {
+            const int orow = r0 + kCols * t + cr;
+            if (orow < r1) {
+                float mm = -INFINITY, ll = 0.0f, f[W];
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-            f[w] = ml[w][cr].x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[w][cr].x - mm);
-            ll = fmaf(ml[w][cr].y, f[w], ll);
-        }
-        const int oi = orow / a.group;
-        const int64_t tok = s.row0 + oi;
-        const int oh = h * a.group + orow - oi * a.group;
-        const int64_t slot = ((int64_t)segment * a.chunks + chunk) * a.slot_rows + kCols * t + cr;
-        const float norm = parts > 1 ? 1.0f : ll > 0.0f ? 1.0f / (6.0f * ll) : 0.0f;
+                for (int w = 0; w < W; ++w) mm = fmaxf(mm, ml[w][cr].x);
 #pragma unroll
-        for (int bb = W == 4 ? 0 : tid >> 8; bb < NB; bb += W / 4) {
-            v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int w = 0; w < W; ++w) {
+                    f[w] = ml[w][cr].x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[w][cr].x - mm);
+                    ll = fmaf(ml[w][cr].y, f[w], ll);
+                }
+                const int oi = orow / a.group;
+                const int64_t tok = s.row0 + oi;
+                const int oh = h * a.group + orow - oi * a.group;
+                const int64_t slot = ((int64_t)segment * a.chunks + chunk) * a.slot_rows + kCols * t + cr;
+                const float norm = parts > 1 ? 1.0f : ll > 0.0f ? 1.0f / (6.0f * ll) : 0.0f;
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const v4f y = *reinterpret_cast<const v4f*>(&part[w][cr][64 * bb + 4 * d0]);
+                for (int bb = W <= 4 ? 0 : tid >> 8; bb < NB; bb += W <= 4 ? 1 : W / 4) {
+                    v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] = fmaf(y[j], f[w], o[j]);
+                    for (int w = 0; w < W; ++w) {
+                        const v4f y = *reinterpret_cast<const v4f*>(&part[w][cr][64 * bb + 4 * d0]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[j] = fmaf(y[j], f[w], o[j]);
+                    }
+                    if (parts > 1) {
+                        *reinterpret_cast<v4f*>(a.part + slot * 64 * NB + 64 * bb + 4 * d0) = o;
+                    } else {
+                        typedef typename H::T t4 __attribute__((ext_vector_type(4)));
+                        typename H::T* dst = reinterpret_cast<typename H::T*>(a.out) + tok * a.ldo + oh * a.hso + 64 * bb + 4 * d0;
+                        *reinterpret_cast<t4*>(dst) = t4{(typename H::T)(o[0] * norm), (typename H::T)(o[1] * norm),
+                                                         (typename H::T)(o[2] * norm), (typename H::T)(o[3] * norm)};
+                    }
+                }
+                if (d0 == 0 && tid < 256) {
+                    if (parts > 1)
+                        reinterpret_cast<float2*>(a.part_ml)[slot] = make_float2(mm, ll);
+                    else if (a.lse)
+                        a.lse[tok * a.q_heads + oh] = ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+                }
             }
-            if (parts > 1) {
-                *reinterpret_cast<v4f*>(a.part + slot * 64 * NB + 64 * bb + 4 * d0) = o;
-            } else {
-                typedef typename H::T t4 __attribute__((ext_vector_type(4)));
-                typename H::T* dst = reinterpret_cast<typename H::T*>(a.out) + tok * a.ldo + oh * a.hso + 64 * bb + 4 * d0;
-                *reinterpret_cast<t4*>(dst) = t4{(typename H::T)(o[0] * norm), (typename H::T)(o[1] * norm),
-                                                 (typename H::T)(o[2] * norm), (typename H::T)(o[3] * norm)};
-            }
         }
-        if (d0 == 0 && tid < 256) {
-            if (parts > 1)
-                reinterpret_cast<float2*>(a.part_ml)[slot] = make_float2(mm, ll);
-            else if (a.lse)
-                a.lse[tok * a.q_heads + oh] = ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
-        }
-    }
     }
 }
 
@@ -964,8 +968,11 @@ hipError_t launch(const KvAttnArgs& a, hipStream_t stream) {
     if constexpr (NB < 4) {
         if (a.tile_rows == 2 * kCols)
             launch_tiles<kBf16, NB, 2, 4>(a, stream);
-        else if (a.tile_rows == 3 * kCols)
+        else if (a.tile_rows == 3 * kCols && a.waves == 4)
             launch_tiles<kBf16, NB, 3, 4>(a, stream);
+    }
+    if constexpr (NB == 2) {
+        if (a.waves == 1) launch_tiles<kBf16, NB, 3, 1>(a, stream);
     }
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (a.chunks > 1) {

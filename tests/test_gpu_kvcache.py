@@ -612,3 +612,28 @@ def test_refusals():
     with pytest.raises(i8.I8mpError):                  # a workspace that is too small
         attend_(big, c, torch.zeros((1, 4096), dtype=torch.int32, device="cuda"), lengths[:1],
                 workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_prompts_that_fill_the_chip(kind):
+    """Enough row tiles that each wave has one to itself: the rows of sampled heads and of all lengths' ends."""
+    heads, group, d, page = 40, 1, 128, 64
+    lens = [(500, 531), (420, 420), (511, 700), (333, 333), (480, 480), (470, 501), (509, 509), (390, 400), (1, 40)]
+    c, table, lengths, seqs = build(lens, heads, group, d, page, kind, 29)
+    counts = [n for n, _ in lens]
+    assert (sum(counts) // 48 + len(lens)) * heads * 2 >= 2048 * 3
+    q = dev16(np.concatenate([s[0] for s in seqs]), kind)
+    qo = dev(np.concatenate([[0], np.cumsum(counts)]), torch.int32)
+    say(f"fp4_cache_attention of {sum(counts)} queries, {heads} heads, {kind}")
+    out, lse = i8.fp4_cache_attention(q, c, table, lengths, qo, max(counts), window=300, return_lse=True)
+    torch.cuda.synchronize()
+    few = [0, 17, 39]
+    # rows near each sequence's start and end, as sequences that end there
+    at = 0
+    for (n, length), (qs, k, v) in zip(lens, seqs):
+        for i in sorted({0, 1, 47, 48, n // 2, n - 2, n - 1}):
+            if 0 <= i < n:
+                end = length - n + i + 1
+                check(out[at + i:at + i + 1, few], lse[at + i:at + i + 1, few],
+                      [(qs[i:i + 1, few], k[:end, few], v[:end, few])], d ** -0.5, kind, window=300)
+        at += n
