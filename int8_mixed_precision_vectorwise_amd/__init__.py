@@ -73,11 +73,15 @@ def _stream(device: torch.device):
 
 
 def _device_of(*tensors) -> torch.device:
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"all tensors must be on one device, got {sorted(map(str, devs))}")
-    dev = devs.pop()
-    if dev.type != "cuda":
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError("all tensors must be on one device, got "
+                                 f"{sorted({str(x.device) for x in tensors if x is not None})}")
+    if dev is None or dev.type != "cuda":
         raise ValueError(f"tensors must be on a GPU (got {dev}); there is no CPU path")
     return dev
 
@@ -660,12 +664,14 @@ class Fp4Cache:
 
 def _run(dev: torch.device, what: str, *args) -> None:
     """Calls a library entry point on dev with its current stream as the last argument."""
-    f = getattr(lib(), what)
-    if dev.index == torch.cuda.current_device():
-        check(f(*args, _raw_stream(dev.index)), what)
+    f, i = getattr(lib(), what), dev.index
+    if i == torch.cuda.current_device():
+        status = f(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            check(f(*args, _raw_stream(dev.index)), what)
+            status = f(*args, _raw_stream(i))
+    if status:
+        check(status, what)
 
 
 def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, heads: Optional[int], head_dim: int) -> Tuple[int, int]:
@@ -709,7 +715,7 @@ def fp4_cache_read(cache: Fp4Cache, slots: torch.Tensor, dtype: Optional[torch.d
     c = cache.struct()
     n = slots.shape[0]
     _vec(slots, "slots", torch.int64, n)
-    k = torch.empty((n, c.kv_heads, c.head_dim), dtype=dtype, device=dev)
+    k = slots.new_empty((n, c.kv_heads, c.head_dim), dtype=dtype)
     v = torch.empty_like(k)
     ld, hs = c.kv_heads * c.head_dim, c.head_dim
     _run(dev, "i8mp_fp4_cache_read", ctypes.byref(c), slots.data_ptr(), n, _DTYPE_CODE[dtype], k.data_ptr(), ld, hs,
@@ -757,11 +763,11 @@ def fp4_cache_attention(q: torch.Tensor, cache: Fp4Cache, table: torch.Tensor, l
     if q_offsets is None and max_q * batch != tokens:
         raise ValueError("without q_offsets every sequence has max_q queries: tokens must be batch * max_q")
     if out is None:
-        out = torch.empty((tokens, q_heads, c.head_dim), dtype=cache.dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     ldo, hso = _heads(out, "out", cache.dtype, q_heads, c.head_dim)
     if out.shape[0] != tokens:
         raise ValueError("out has the wrong shape")
-    lse = torch.empty((tokens, q_heads), dtype=torch.float32, device=dev) if return_lse else None
+    lse = q.new_empty((tokens, q_heads), dtype=torch.float32) if return_lse else None
     call = Fp4AttentionStruct(
         q.data_ptr(), ldq, hsq, out.data_ptr(), ldo, hso, None if lse is None else lse.data_ptr(), table.data_ptr(), ldt,
         cols, lengths.data_ptr(), None if q_offsets is None else q_offsets.data_ptr(),
