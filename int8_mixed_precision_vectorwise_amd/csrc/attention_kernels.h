@@ -328,16 +328,20 @@ typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 // How weights are kept in the 16-bit type's range.  A row's reference is a maximum that
 // stays as it was until a score passes it by 2^kSlack, so that few tiles rescale (2048
 // queries behind 2048 tokens, 64 / 8 heads of 128, bfloat16: 268 us, 312 with no slack).
-// In fp16 weights are 2^4 times e^(s - reference), at most 2^11 so, and the scales A
+// A weight that is far above a row's others is rounded less often the closer the reference
+// is to it (an equal one is a power of two): with two roundings, in fp16, the output's
+// error is 1.5 times that of its own rounding at a slack of 2^7, 1.3 at 2^2 and 1.25 at
+// none, for a 4096-token prompt, at 0, 3 and 9 % of its time (349 us).
+// In fp16 weights are 2^9 times e^(s - reference), at most 2^11 so, and the scales A
 // that they meet are taken times 2^(4 - e), 2^e the first power above every finite A the
 // wave has met (a larger one than before rescales the sums).  Products are then below
-// 2^15 whatever the values' size; a weight is rounded at 2^-29 of the reference's and a
+// 2^15 whatever the values' size; a weight is rounded at 2^-34 of the reference's and a
 // scale at 2^-29 of the largest, so that the keys that draw the weight may have values
 // 2^17 below others that draw none.
 template <bool kBf16>
-constexpr float kSlack = kBf16 ? 8.0f : 7.0f;
+constexpr float kSlack = kBf16 ? 8.0f : 2.0f;
 template <bool kBf16>
-constexpr float kShift = kBf16 ? 0.0f : 4.0f;
+constexpr float kShift = kBf16 ? 0.0f : 9.0f;
 constexpr int kLeastLarge = -11;  // 2^(4 - e) is an fp16 number
 
 // The products P A of a lane's 8 weights with a block's scales, in the order of the
@@ -455,7 +459,7 @@ __device__ inline __attribute__((always_inline)) void take_scales(Weights<kBf16,
 // epilogue of about 4 us.  Many rows: the VALU, about 75 % busy: converting 4-bit codes
 // (shared by the row tile), masks, exponentials and the scaling of weights take 443
 // instructions for 48 rows of 32 keys beside 48 matrix instructions, which hold the SIMD
-// for about 10 of their 16 cycles each.  A 4096-token prompt of 64 heads of 128: 780
+// for about 10 of their 16 cycles each.  A 4096-token prompt of 64 heads of 128: 760
 // TFLOP/s.
 //
 // simd_waves(): those of a SIMD, by their registers (512 a lane for all of them).
