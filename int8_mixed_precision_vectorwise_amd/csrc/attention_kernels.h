@@ -455,12 +455,11 @@ __device__ inline __attribute__((always_inline)) void take_scales(Weights<kBf16,
 // which then rides on the exponential's argument).
 //
 // What bounds it.  Few rows: HBM; 64 sequences of 8191 tokens, 64 / 8 heads of 128, are
-// read at 5.1 TB/s, one of 131072 tokens at 4.9; short contexts, a prologue and
-// epilogue of about 4 us.  Many rows: the VALU, about 75 % busy: converting 4-bit codes
-// (shared by the row tile), masks, exponentials and the scaling of weights take 443
-// instructions for 48 rows of 32 keys beside 48 matrix instructions, which hold the SIMD
-// for about 10 of their 16 cycles each.  A 4096-token prompt of 64 heads of 128: 760
-// TFLOP/s.
+// read at 5.1 TB/s, one of 131072 tokens at 4.7; short contexts, a prologue and
+// epilogue of about 4 us.  Many rows: the VALU: converting 4-bit codes (shared by the row
+// tile), exponentials and the scaling of weights take about 380 instructions for 48 rows
+// of 32 keys beside 48 matrix instructions, which hold the SIMD for about 10 of their 16
+// cycles each.  A 4096-token prompt of 64 heads of 128: 760 TFLOP/s.
 //
 // simd_waves(): those of a SIMD, by their registers (512 a lane for all of them).
 // T = 3 takes 248 registers with head_dim 128; with 256 two sets of rows already spill.
