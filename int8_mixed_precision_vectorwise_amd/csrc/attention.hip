@@ -32,7 +32,7 @@ int64_t real_segments(const KvAttnArgs& a) {
 }
 
 // Prompts of so many row tiles that single waves fill the chip 3/2 times (head_dim 128:
-// 3072 of them) take workgroups of one wave, which has its row tile's keys for itself: a
+// it holds 2048) take workgroups of one wave, which has its row tile's keys for itself: a
 // quarter of the prologues, no sums to join.  Waves of 4 / 1, us: 5504 row tiles of a
 // 4096-token prompt 386 / 349, 3520 of 8 prompts of 512 89 / 74, 2752 of a 2048-token
 // one 123 / 115, but 2736 behind 2048 tokens 272 / 276, with a distance bias 369 / 391,
