@@ -11,8 +11,8 @@
 // round to codes and widen them, in place of seven comparisons a value.
 //
 // Both are bound by HBM where tokens are many: 16381 tokens of 32 heads of 128 are written
-// in 62 us (5.5 TB/s) and read in 53 (6.4 TB/s); one lane for 8 dims of one token, with
-// V's halves in 2-byte accesses, took 112 and 146.  A few tokens are a launch: 3.7 us.
+// in 62 us (5.5 TB/s) and read in 53 (6.4 TB/s); with a lane for 8 dims of one token and
+// V in 2-byte accesses both took 251 us.  A few tokens are a launch: 3.7 us.
 #include "kvcache.h"
 #include "quant_util.h"
 
