@@ -512,7 +512,8 @@ typedef struct i8mp_fp4_attention {
     int32_t max_len;          /* bound on the lengths, <= table_cols * page_size     */
     int32_t window;           /* 0: none                                            */
     float scale;
-    float softcap;            /* 0: none                                            */
+    float softcap;            /* 0: none.  Any positive value; a capped score is within
+                                 2^-17 or 2^-20 of its value of cap tanh(s / cap)    */
 } i8mp_fp4_attention;
 
 /* Host.  Workspace of a call with these sizes (its pointers are not looked at): 0

@@ -1,5 +1,8 @@
 // Attention over the 4-bit key/value cache: the cut of a call into workgroups, and
 // the fp16 kernels.
+#include <cfloat>
+#include <cmath>
+
 #include "attention_kernels.h"
 
 namespace i8mp {
@@ -78,6 +81,14 @@ size_t kv_attention_workspace(const KvAttnArgs& args) {
 hipError_t launch_kv_attention(const KvAttnArgs& args, void* workspace, hipStream_t stream) {
     KvAttnArgs a = args;
     plan(a);
+    const float f = a.scale / 6.0f;
+    a.to_s = f * kLog2e;
+    // a cap past 1e20 leaves scores as one of 1e20 does; y is finite, so that a score of 0 stays 0 under the smallest
+    const float cap = std::fmin(a.softcap, 1e20f);
+    const auto finite = [](float y) { return std::fmax(std::fmin(y, FLT_MAX), -FLT_MAX); };
+    a.to_y = cap > 0.0f ? finite(f / cap) : 0.0f;
+    a.to_e = finite(2.0f * kLog2e * a.to_y);
+    a.cap = cap * kLog2e;
     a.part = static_cast<float*>(workspace);
     a.part_ml = a.part + (a.chunks == 1 ? 0 : (int64_t)a.batch * a.row_tiles * a.c.heads * a.chunks * a.slot_rows * 64 * a.c.blocks);
     if (a.c.bf16) return launch_kv_attention_bf16(a, stream);

@@ -394,6 +394,25 @@ struct Weights<false, NB> {
     }
 };
 
+// What is done to the scores: a factor alone, which then rides on the exponential's
+// argument; a cap or a distance term (or a factor of 0); a cap far above most scores.
+//
+// The cap is cap (1 - 2 / (1 + e^2y)), y = s / cap, which is off by up to 2^-23 of the cap:
+// 1e-5 of a weight at a cap of 64.  A larger one, which has to leave the scores far below it
+// as they are, takes cap (y + y z q(z)), z = y^2, at |y| <= 1/2, with q fitted to the least
+// largest error of (tanh y / y - 1) / z on [0, 1/4]: within 2^-23.7 of tanh y with fp32's
+// roundings; past 1/2 the other form is within 2^-20 of its value.  In kernels of their own,
+// since as branches of one they cost ordinary caps 5 to 18 % (a 4096-token prompt of 64
+// heads of 128, cap 50: 467 us, 488 to 500 so); cap 1000 takes 557.
+enum Form { kFactor, kTerms, kFarCap };
+constexpr float kFarFrom = 64.0f * kLog2e;  // in units of log2 e, as KvAttnArgs::cap
+constexpr float kTanhSmall = 0.5f;
+__device__ inline float tanh_small(float y) {
+    const float z = y * y;
+    const float q = fmaf(fmaf(fmaf(0.01725699193775654f, z, -0.05305295065045357f), z, 0.1332598775625229f), z, -0.33333149552345276f);
+    return fmaf(y, z * q, y);
+}
+
 // Makes a tile's scales of V ready for the products with the weights.  `masked`: some of
 // its keys may lie past the sequence's end (the lane's i-th of half u does if 16 u + i >=
 // left) or on no page.
@@ -451,8 +470,6 @@ __device__ inline __attribute__((always_inline)) void take_scales(Weights<kBf16,
 // lanes.  Tiles come through a ring of kRing stages of LDS for each wave, filled by DMA:
 // a tile is read into registers whole and its stage requested anew before the products,
 // and waves meet only at the end.
-// kScored: scores get a cap, a distance term or a factor of 0 (else a factor alone,
-// which then rides on the exponential's argument).
 //
 // What bounds it.  Few rows: HBM; 64 sequences of 8191 tokens, 64 / 8 heads of 128, are
 // read at 5.1 TB/s, one of 131072 tokens at 4.7; short contexts, a prologue and
@@ -469,11 +486,12 @@ constexpr int simd_waves(int NB, int T) { return NB == 4 ? 2 : T == 1 ? 4 : NB =
 template <int NB>
 constexpr int kRing() { return NB == 1 ? 4 : 2; }
 
-template <bool kBf16, int NB, int T, int W, bool kOne, bool kScored>
+template <bool kBf16, int NB, int T, int W, bool kOne, Form kForm>
 __global__ __launch_bounds__(64 * W, simd_waves(NB, T)) void kv_attention_kernel(KvAttnArgs a) {
     typedef Half<kBf16> H;
     typedef typename H::v8 v8;
     typedef Stage<NB, kOne> St;
+    constexpr bool kScored = kForm != kFactor;
     constexpr int R = kRing<NB>();
     // V's scales are made ready before the scores or after them: before, with fp16 and
     // kScored, where 101 registers spilled after (six pieces of prompts of up to 3701 tokens,
@@ -569,7 +587,7 @@ __global__ __launch_bounds__(64 * W, simd_waves(NB, T)) void kv_attention_kernel
     }
 
     // a score is x * unit, in units of log2 e
-    const float unit = kScored ? 1.0f : fabsf(a.scale) / 6.0f * kLog2e;
+    const float unit = kScored ? 1.0f : fabsf(a.to_s);
     // a row's reference, as what is added to a score to get its weight's exponent; the
     // exponent past which the reference moves (any, for a row that has seen no key yet);
     // the sum of this lane's weights
@@ -650,18 +668,36 @@ __global__ __launch_bounds__(64 * W, simd_waves(NB, T)) void kv_attention_kernel
             }
         }
         if (kScored) {
-            const float f = a.scale / 6.0f;
             if (a.softcap > 0.0f) {
-                const float arg = 2.0f * kLog2e * f / a.softcap, cap = a.softcap * kLog2e;
+                // the scores that may be past the polynomial: of a near cap all, of a far one few tiles'
+                bool past = true;
+                if constexpr (kForm == kFarCap) {
+                    float most = 0.0f;
+#pragma unroll
+                    for (int t = 0; t < T; ++t)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                x[t][u][i] *= a.to_y;
+                                most = fmaxf(most, fabsf(x[t][u][i]));
+                            }
+                    past = __ballot(most > kTanhSmall) != 0;
+                }
 #pragma unroll
                 for (int t = 0; t < T; ++t) {
-                    const float top = cap + nb[t];
+                    const float top = a.cap + nb[t];
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {  // tanh y = 1 - 2 / (1 + e^2y)
-                            const float e = __builtin_amdgcn_exp2f(x[t][u][i] * arg);
-                            x[t][u][i] = fmaf(__builtin_amdgcn_rcpf(1.0f + e), -2.0f * cap, top);
+                        for (int i = 0; i < 4; ++i) {
+                            const float y = x[t][u][i];
+                            if (past) {
+                                const float e = __builtin_amdgcn_exp2f(y * (kForm == kFarCap ? 2.0f * kLog2e : a.to_e));
+                                x[t][u][i] = fmaf(__builtin_amdgcn_rcpf(1.0f + e), -2.0f * a.cap, top);
+                            }
+                            if constexpr (kForm == kFarCap)
+                                x[t][u][i] = fabsf(y) > kTanhSmall ? x[t][u][i] : fmaf(tanh_small(y), a.cap, nb[t]);
                         }
                 }
             } else {
@@ -670,7 +706,7 @@ __global__ __launch_bounds__(64 * W, simd_waves(NB, T)) void kv_attention_kernel
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) x[t][u][i] = fmaf(x[t][u][i], f * kLog2e, nb[t]);
+                        for (int i = 0; i < 4; ++i) x[t][u][i] = fmaf(x[t][u][i], a.to_s, nb[t]);
             }
             if (a.alibi) {
 #pragma unroll
@@ -937,7 +973,10 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs a) {
     if (d0 == 0 && a.lse) a.lse[tok * a.q_heads + oh] = l > 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
 }
 
-inline bool scored_call(const KvAttnArgs& a) { return a.softcap > 0.0f || a.alibi || fabsf(a.scale) < 1e-30f; }
+inline Form form_of(const KvAttnArgs& a) {
+    if (a.softcap > 0.0f && a.cap > kFarFrom) return kFarCap;
+    return a.softcap > 0.0f || a.alibi || fabsf(a.scale) < 1e-30f ? kTerms : kFactor;
+}
 
 template <bool kBf16, int NB, int T, int W, bool kOne>
 void launch_main(const KvAttnArgs& a, hipStream_t stream) {
@@ -947,10 +986,11 @@ void launch_main(const KvAttnArgs& a, hipStream_t stream) {
         KvAttnArgs x = a;
         x.block0 = (uint32_t)b0;
         const dim3 grid((unsigned)(blocks - b0 < most ? blocks - b0 : most));
-        if (scored_call(a))
-            hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, T, W, kOne, true>), grid, block, 0, stream, x);
-        else
-            hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, T, W, kOne, false>), grid, block, 0, stream, x);
+        switch (form_of(a)) {
+            case kFarCap: hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, T, W, kOne, kFarCap>), grid, block, 0, stream, x); break;
+            case kTerms: hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, T, W, kOne, kTerms>), grid, block, 0, stream, x); break;
+            default: hipLaunchKernelGGL((kv_attention_kernel<kBf16, NB, T, W, kOne, kFactor>), grid, block, 0, stream, x);
+        }
     }
 }
 

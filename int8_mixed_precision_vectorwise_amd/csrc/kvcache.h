@@ -57,6 +57,9 @@ struct KvAttnArgs {
     float scale, softcap;            // softcap 0: none
     int64_t max_len;                 // bound on the lengths
     // set by the launcher
+    float to_s, to_y, to_e;          // factors of a product of q with E2M1 values and scales A: to its score, in units
+                                     // of log2 e, to y = score / cap, and to 2 y in the same units
+    float cap;                       // softcap in units of log2 e
     int32_t tile_rows, row_tiles;    // rows of a row tile, row tiles of the longest sequence
     int32_t waves;                   // waves of a workgroup
     int32_t chunk_tiles, chunks;     // most key tiles of a part, most parts of a segment (kv head of a row tile)

@@ -1,0 +1,57 @@
+"""The 4-bit cache and its attention at the edges of their ranges, against the CPU
+oracle: caps of any size, rows that see no number, values of very different sizes,
+blocks of the smallest bfloat16 numbers.
+
+Bounds are those of test_gpu_kvcache.py with e, the error of a score, free of the cap:
+the tanh is within 2^-19 of its value (a polynomial of five terms, or 1 - 2 / (1 + e^2y)
+at |y| > 1/2 where its roundings, 2^-21, are at most 2^-20 of it), which is 32 of the
+2^-24 of scale * sum |q||k'| that 260 of the products' roundings are counted in.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import int8_mixed_precision_vectorwise_amd as i8
+from gpu_util import host, say
+from oracle import kvcache as kv
+from test_gpu_kvcache import build, dev, dev16, draw, make_cache, wide
+
+pytestmark = pytest.mark.gpu
+
+
+def check(out, lse, seqs, scale, kind, window=0, softcap=0.0, alibi=None, prefix=None, heads=None):
+    """out, lse against the oracle over seqs = [(q, k', v')] (of the named kv heads' rows)."""
+    u, least = (2.0 ** -11, 2.0 ** -23) if kind == "f16" else (2.0 ** -8, 0.0)
+    got, got_l = wide(out).astype(np.float64), host(lse).astype(np.float64)
+    row = 0
+    for n, (q, k, v) in enumerate(seqs):
+        o, l, size, reach = kv.attention(q, k, v, scale, window, softcap, alibi, 0 if prefix is None else int(prefix[n]))
+        far = 0.0 if alibi is None else float(np.abs(alibi).max()) * max(len(k), 1)
+        e = 2.0 ** -24 * (260 + 32) * reach + 2.0 ** -20 + 2.0 ** -22 * far
+        g, gl = got[row:row + len(q)], got_l[row:row + len(q)]
+        row += len(q)
+        nothing = np.isneginf(l)
+        assert np.array_equal(np.isneginf(gl), nothing), (n, "which rows see nothing")
+        el = np.abs(gl[~nothing] - l[~nothing]) - (e[~nothing] + 2.0 ** -21 * np.abs(l[~nothing]))
+        assert el.size == 0 or el.max() <= 0, f"sequence {n}: lse off by {el.max()} more than its bound"
+        tol = u * np.abs(o) + (u + 2 * e[..., None]) * size + least
+        bad = ~(np.abs(g - o) <= tol)
+        assert not bad.any(), (f"sequence {n}: {int(bad.sum())} of {bad.size} outside; first at {tuple(np.argwhere(bad)[0])}: "
+                               f"{g[bad][0]} oracle {o[bad][0]} bound {tol[bad][0]}")
+    assert row == got.shape[0]
+
+
+@pytest.mark.parametrize("cap", [1e-45, 1e-3, 0.7, 7.0, 50.0, 1e3, 1e5, 1e8, 3e38])
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_caps_of_any_size(cap, kind):
+    """A cap far above the scores leaves them as they are, one far below makes them equal."""
+    for lens, group, d in (([(1, 300), (1, 77)], 4, 128), ([(40, 90)], 1, 64), ([(3, 50)], 2, 256)):
+        c, table, lengths, seqs = build(lens, 2, group, d, 32, kind, 40)
+        counts = [n for n, _ in lens]
+        q = dev16(np.concatenate([s[0] for s in seqs]), kind)
+        say(f"fp4_cache_attention capped at {cap}, {lens} {kind}")
+        out, lse = i8.fp4_cache_attention(q, c, table, lengths, dev(np.concatenate([[0], np.cumsum(counts)]), torch.int32),
+                                          max(counts), scale=0.5, softcap=cap, return_lse=True)
+        torch.cuda.synchronize()
+        check(out, lse, seqs, 0.5, kind, softcap=float(np.float32(cap)))
