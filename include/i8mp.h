@@ -477,7 +477,8 @@ i8mp_status i8mp_fp4_cache_read(const i8mp_fp4_cache* cache /* host */, const in
  * window > 0, p - j < window).  prefix names tokens at a sequence's start that
  * every query sees: a prompt without causal order, or the first tokens kept in
  * sight beside a window.  A row that sees nothing (L = 0, or a query before the
- * first token) gets zeros and lse = -inf.  Sums, maxima and the softmax are fp32;
+ * first token) gets zeros and lse = -inf; one that meets a score that is no number (an
+ * infinity in a key's block, a NaN in q) gets NaN in both.  Sums, maxima and the softmax are fp32;
  * the weights e^s, times a block's A, are rounded to the 16-bit type for the product
  * with the E2M1 values (bfloat16: once; fp16: e^s is rounded, then its product).
  * The rows of one sequence do not depend on the others' contents; how the keys are

@@ -323,6 +323,11 @@ __device__ inline float scale_at(const uint32_t (&w)[NB * 2], int i, int b) {
     return Half<false>::wide((w[j >> 1] >> (16 * (j & 1))) & 0xffffu);
 }
 
+// A row's end, from its reference m and the sum l of its weights: 0 for a row that sees
+// nothing, and NaN, like the row's output, where a score was no number.
+__device__ inline float norm_of(float l) { return l == 0.0f ? 0.0f : 1.0f / (6.0f * l); }
+__device__ inline float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
+
 typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 
 // How weights are kept in the 16-bit type's range.  A row's reference is a maximum that
@@ -846,7 +851,7 @@ __global__ __launch_bounds__(64 * W, simd_waves(NB, T)) void kv_attention_kernel
                 const int64_t tok = s.row0 + oi;
                 const int oh = h * a.group + orow - oi * a.group;
                 const int64_t slot = ((int64_t)segment * a.chunks + chunk) * a.slot_rows + kCols * t + cr;
-                const float norm = parts > 1 ? 1.0f : ll > 0.0f ? 1.0f / (6.0f * ll) : 0.0f;
+                const float norm = parts > 1 ? 1.0f : norm_of(ll);
 #pragma unroll
                 for (int bb = W <= 4 ? 0 : tid >> 8; bb < NB; bb += W <= 4 ? 1 : W / 4) {
                     v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -869,7 +874,7 @@ __global__ __launch_bounds__(64 * W, simd_waves(NB, T)) void kv_attention_kernel
                     if (parts > 1)
                         reinterpret_cast<float2*>(a.part_ml)[slot] = make_float2(mm, ll);
                     else if (a.lse)
-                        a.lse[tok * a.q_heads + oh] = ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+                        a.lse[tok * a.q_heads + oh] = lse_of(mm, ll);
                 }
             }
         }
@@ -962,7 +967,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs a) {
     const int qi = row / a.group;
     const int64_t tok = s.row0 + qi;
     const int oh = h * a.group + row - qi * a.group;
-    const float norm = l > 0.0f ? 1.0f / (6.0f * l) : 0.0f;
+    const float norm = norm_of(l);
 #pragma unroll
     for (int bb = 0; bb < NB; ++bb) {
         typedef typename H::T t4 __attribute__((ext_vector_type(4)));
@@ -970,7 +975,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttnArgs a) {
         *reinterpret_cast<t4*>(dst) = t4{(typename H::T)(o[bb][0] * norm), (typename H::T)(o[bb][1] * norm),
                                          (typename H::T)(o[bb][2] * norm), (typename H::T)(o[bb][3] * norm)};
     }
-    if (d0 == 0 && a.lse) a.lse[tok * a.q_heads + oh] = l > 0.0f ? (top + log2f(l)) * kLn2 : -INFINITY;
+    if (d0 == 0 && a.lse) a.lse[tok * a.q_heads + oh] = lse_of(top, l);
 }
 
 inline Form form_of(const KvAttnArgs& a) {

@@ -55,3 +55,32 @@ def test_caps_of_any_size(cap, kind):
                                           max(counts), scale=0.5, softcap=cap, return_lse=True)
         torch.cuda.synchronize()
         check(out, lse, seqs, 0.5, kind, softcap=float(np.float32(cap)))
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("n", [40, 700, 5000], ids=["one_tile", "whole", "cut"])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_log_sum_exp_of_rows_that_meet_no_number(n, kind, softcap):
+    """A key that holds an infinity, or a query that does: out and lse are NaN where it is in sight, and only there."""
+    rng = np.random.default_rng(41)
+    heads, group, d, page = 2, 2, 64, 32
+    q, k, v = draw(rng, (3, heads * group, d), kind), draw(rng, (n, heads, d), kind, 0.3), draw(rng, (n, heads, d), kind)
+    k[n - 2, 1, 7] = np.inf                    # seen by the last two queries, heads 2 and 3
+    q[0, 0, 5] = np.nan
+    c = make_cache(-(-n // page) + 1, heads, d, page, kind)
+    table = dev(np.arange(-(-n // page))[None], torch.int32)
+    say(f"fp4_cache_attention with scores that are no numbers, {n} keys {kind} cap {softcap}")
+    i8.fp4_cache_write(c, dev16(k, kind), dev16(v, kind), torch.arange(n, device="cuda"))
+    lengths = dev(np.array([n]), torch.int32)
+    out, lse = i8.fp4_cache_attention(dev16(q, kind), c, table, lengths, max_q=3, softcap=softcap, return_lse=True)
+    one, one_lse = i8.fp4_cache_attention(dev16(q[:1], kind), c, table, lengths, max_q=1, softcap=softcap, window=2,
+                                          return_lse=True)
+    none, none_lse = i8.fp4_cache_attention(dev16(q, kind), c, table, 0 * lengths, max_q=3, return_lse=True)
+    torch.cuda.synchronize()
+    want = np.zeros((3, 4), bool)
+    want[0, 0] = want[1:, 2:] = True
+    assert np.array_equal(np.isnan(host(lse)), want) and np.isfinite(host(lse)[~want]).all()
+    assert np.array_equal(np.isnan(wide(out)).all(-1), want) and np.array_equal(np.isnan(wide(out)).any(-1), want)
+    assert np.array_equal(np.isnan(host(one_lse))[0], [True, False, True, True])
+    assert np.array_equal(np.isnan(wide(one)).all(-1)[0], [True, False, True, True])
+    assert bool((none == 0).all()) and bool(torch.isneginf(none_lse).all())
