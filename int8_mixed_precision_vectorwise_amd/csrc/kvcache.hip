@@ -63,6 +63,9 @@ __device__ inline uint32_t chunk_top(const uint4& x) {
     return m.x > m.y ? m.x : m.y;
 }
 
+// what a block's values are multiplied by, from its A; IEEE reciprocal
+__device__ inline float factor(float a) { return a > 0.0f ? 6.0f * (1.0f / a) : 0.0f; }
+
 // The 8 codes of a lane's chunk and the bits of its block's A.  All lanes of a block call.
 template <bool kBf16>
 __device__ inline uint32_t quantize8(const uint4& x, uint32_t& a_bits) {
@@ -70,9 +73,9 @@ __device__ inline uint32_t quantize8(const uint4& x, uint32_t& a_bits) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t top = block_max(chunk_top(x));
     uint32_t packed = 0;
-    if (top < kInf) {
-        const float mx = wide<kBf16>(top);
-        const float inv = mx > 0.0f ? 6.0f * (1.0f / mx) : 0.0f;  // IEEE reciprocal
+    const float inv = factor(wide<kBf16>(top));
+    // 6 / A passes the largest fp32 number where A < 1.76e-38 (bfloat16 only)
+    if (top < kInf && (!kBf16 || inv < INFINITY)) {
         // an element's magnitude is at most A, so products are within 6 and an ulp
 #define I8MP_PAIR(i)                                                                                            \
     packed = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(packed, wide<kBf16>(w[i] & 0xffffu) * inv,                \
@@ -82,7 +85,7 @@ __device__ inline uint32_t quantize8(const uint4& x, uint32_t& a_bits) {
         I8MP_PAIR(2);
         I8MP_PAIR(3);
 #undef I8MP_PAIR
-    } else {  // an infinity or a NaN: NaNs are left out of A, and count as zeros
+    } else {  // an infinity, a NaN (left out of A) or such an A: products that are NaN count as zeros
         float f[8], mx = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -91,11 +94,11 @@ __device__ inline uint32_t quantize8(const uint4& x, uint32_t& a_bits) {
         }
         top = block_max(__float_as_uint(mx));
         mx = __uint_as_float(top);
-        const float inv = mx > 0.0f ? 6.0f * (1.0f / mx) : 0.0f;
+        const float by = factor(mx);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const uint32_t sign = (w[e >> 1] >> (16 * (e & 1) + 15)) & 1u;
-            packed |= (mag_code(f[e] * inv) | (sign << 3)) << (4 * e);
+            packed |= (mag_code(f[e] * by) | (sign << 3)) << (4 * e);
         }
         top = kBf16 ? top >> 16 : (uint32_t)f2h(mx);
     }

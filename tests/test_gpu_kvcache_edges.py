@@ -84,3 +84,28 @@ def test_log_sum_exp_of_rows_that_meet_no_number(n, kind, softcap):
     assert np.array_equal(np.isnan(host(one_lse))[0], [True, False, True, True])
     assert np.array_equal(np.isnan(wide(one)).all(-1)[0], [True, False, True, True])
     assert bool((none == 0).all()) and bool(torch.isneginf(none_lse).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_write_blocks_of_the_smallest_numbers(d):
+    """bfloat16 blocks whose factor 6 / A passes the largest fp32 number: every byte is the oracle's."""
+    rng = np.random.default_rng([44, d])
+    n, page, kind = 64, 16, "bf16"
+    top = rng.integers(1, 0x100, (n, 1, 1))             # A: subnormals, and the first normal numbers (0x0080 = 2^-126)
+    top[:8, 0, 0] = [1, 2, 0x7F, 0x80, 0xBF, 0xC0, 0xC1, 0xFF]          # 6 / FLT_MAX = 1.76e-38 lies at 0x00c0
+    bits = rng.integers(0, 0x10000, (2, n, 1, d)) % (top + 1)
+    bits[..., ::64] = top
+    bits[..., 3::64] = 0
+    bits = bits | np.where(rng.integers(0, 2, bits.shape) > 0, 0x8000, 0)
+    k, v = (kv.from_bits16(x.astype(np.uint16), kind) for x in bits)
+    say(f"fp4_cache_write of the smallest bfloat16 numbers, head_dim {d}")
+    c = make_cache(n // page, 1, d, page, kind)
+    want = host(c.data).copy()
+    kv.write(want, page, k, v, range(n), kind)
+    t = [torch.from_numpy(x.astype(np.uint16).view(np.int16)).view(torch.bfloat16).cuda() for x in bits]
+    i8.fp4_cache_write(c, *t, torch.arange(n, device="cuda"))
+    got = i8.fp4_cache_read(c, torch.arange(n, device="cuda"), torch.float32)
+    torch.cuda.synchronize()
+    assert np.array_equal(host(c.data), want)
+    for g, r in zip(got, kv.read(want, page, d, range(n), kind)):
+        assert np.array_equal(wide(g).view(np.int32), np.asarray(r, np.float32).view(np.int32))
