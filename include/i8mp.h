@@ -480,7 +480,8 @@ i8mp_status i8mp_fp4_cache_read(const i8mp_fp4_cache* cache /* host */, const in
  * first token) gets zeros and lse = -inf; one that meets a score that is no number (an
  * infinity in a key's block, a NaN in q) gets NaN in both.  Sums, maxima and the softmax are fp32;
  * the weights e^s, times a block's A, are rounded to the 16-bit type for the product
- * with the E2M1 values (bfloat16: once; fp16: e^s is rounded, then its product).
+ * with the E2M1 values (bfloat16: once; fp16: e^s is rounded, then its product, or, in
+ * waves whose A's span more than 2^14, their fp32 product to 2^-18).
  * The rows of one sequence do not depend on the others' contents; how the keys are
  * cut, and so the order of the sums, follows from the call's sizes.
  *

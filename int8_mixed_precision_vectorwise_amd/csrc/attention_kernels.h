@@ -9,6 +9,8 @@
 // the 64-deep partial sums of q . k, and on the weights e^s of v.
 #pragma once
 
+#include <type_traits>
+
 #include "kvcache.h"
 
 namespace i8mp {
@@ -340,14 +342,28 @@ typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 // In fp16 weights are 2^9 times e^(s - reference), at most 2^11 so, and the scales A
 // that they meet are taken times 2^(4 - e), 2^e the first power above every finite A the
 // wave has met (a larger one than before rescales the sums).  Products are then below
-// 2^15 whatever the values' size; a weight is rounded at 2^-34 of the reference's and a
-// scale at 2^-29 of the largest, so that the keys that draw the weight may have values
-// 2^17 below others that draw none.
+// 2^15, and a weight is rounded at 2^-34 of the reference's: enough as long as the key that
+// draws the weight does not have values far below others that draw next to none.  So once
+// the A's that a wave has met (of keys in sight or not) span more than 2^kSpan, it goes on
+// with fp32 products, each as two bfloat16 numbers that hold it to 2^-18, in two matrix
+// instructions.  A 4096-token prompt of 64 heads of 128 takes 372 us, 366 without the
+// sizes, 560 in the wide form; 64 sequences of 8192, 64 / 8 heads, 93, 92 and 105.
 template <bool kBf16>
 constexpr float kSlack = kBf16 ? 8.0f : 2.0f;
 template <bool kBf16>
 constexpr float kShift = kBf16 ? 0.0f : 9.0f;
 constexpr int kLeastLarge = -11;  // 2^(4 - e) is an fp16 number
+constexpr int kSpan = 14;
+
+// The sizes of A that a wave has met (fp16): all that are finite are below 2^large, and
+// those that are not 0 have bits of at least `low`, a power of 2 or 0.  The guess that it
+// starts with, 2^-5 .. 2^3, spares most waves the search in their first tile (decode of 64
+// sequences in a window of 1024 tokens: 23.4 us without it, 22.6 with it); where that
+// tile does not fit, its own sizes take the guess's place.
+struct Sizes {
+    int large = 3, low = 10 << 10;
+    bool guess = true;
+};
 
 // The products P A of a lane's 8 weights with a block's scales, in the order of the
 // keys.  bfloat16: fp32 products, rounded once, as the output is.  fp16: the weights are
@@ -399,6 +415,31 @@ struct Weights<false, NB> {
     }
 };
 
+// V^T for dims 64 b + 4 m + j of a block: a word holds two tokens' dims 0 .. 3; pairing the
+// words' nibbles makes bytes (token 0, token 1) and (token 2, token 3) of one dim
+struct Nibbles {
+    uint32_t ev[2], od[2];  // dims 0 and 2, dims 1 and 3
+};
+__device__ inline Nibbles pair_nibbles(uint32_t a0, uint32_t b0, uint32_t a1, uint32_t b1) {
+    Nibbles n;
+    n.ev[0] = (a0 & 0x0f0f0f0fu) | ((b0 << 4) & 0xf0f0f0f0u);
+    n.od[0] = ((a0 >> 4) & 0x0f0f0f0fu) | (b0 & 0xf0f0f0f0u);
+    n.ev[1] = (a1 & 0x0f0f0f0fu) | ((b1 << 4) & 0xf0f0f0f0u);
+    n.od[1] = ((a1 >> 4) & 0x0f0f0f0fu) | (b1 & 0xf0f0f0f0u);
+    return n;
+}
+template <bool kBf16>
+__device__ inline typename Half<kBf16>::v8 values_of(const Nibbles& n, int j) {
+    typedef Half<kBf16> H;
+    const uint32_t x0 = j & 1 ? n.od[0] : n.ev[0], x1 = j & 1 ? n.od[1] : n.ev[1];
+    typename H::v2 e[4];
+    e[0] = j < 2 ? H::template codes<0>(x0) : H::template codes<1>(x0);
+    e[1] = j < 2 ? H::template codes<2>(x0) : H::template codes<3>(x0);
+    e[2] = j < 2 ? H::template codes<0>(x1) : H::template codes<1>(x1);
+    e[3] = j < 2 ? H::template codes<2>(x1) : H::template codes<3>(x1);
+    return typename H::v8{e[0].x, e[0].y, e[1].x, e[1].y, e[2].x, e[2].y, e[3].x, e[3].y};
+}
+
 // What is done to the scores: a factor alone, which then rides on the exponential's
 // argument; a cap or a distance term (or a factor of 0); a cap far above most scores.
 //
@@ -408,7 +449,7 @@ struct Weights<false, NB> {
 // largest error of (tanh y / y - 1) / z on [0, 1/4]: within 2^-23.7 of tanh y with fp32's
 // roundings; past 1/2 the other form is within 2^-20 of its value.  In kernels of their own,
 // since as branches of one they cost ordinary caps 5 to 18 % (a 4096-token prompt of 64
-// heads of 128, cap 50: 467 us, 488 to 500 so); cap 1000 takes 557.
+// heads of 128, cap 50: 467 us, 488 to 500 so); cap 1000 takes 630.
 enum Form { kFactor, kTerms, kFarCap };
 constexpr float kFarFrom = 64.0f * kLog2e;  // in units of log2 e, as KvAttnArgs::cap
 constexpr float kTanhSmall = 0.5f;
@@ -418,54 +459,67 @@ __device__ inline float tanh_small(float y) {
     return fmaf(y, z * q, y);
 }
 
-// Makes a tile's scales of V ready for the products with the weights.  `masked`: some of
-// its keys may lie past the sequence's end (the lane's i-th of half u does if 16 u + i >=
-// left) or on no page.
-template <bool kBf16, int NB, int T>
-__device__ inline __attribute__((always_inline)) void take_scales(Weights<kBf16, NB>& scales, uint32_t (&vs)[2][2 * NB],
-                                                                  v4f (&acc)[T][NB][4], int& large, bool masked,
-                                                                  bool live0, bool live1, int left) {
-    if (masked) {
-        // what a page holds past a sequence's end may be anything: its scales are taken as 0
+// What a page holds past a sequence's end may be anything: the scales of V are taken as 0
+// there (the lane's i-th key of half u if 16 u + i >= left), and on no page.
+template <int NB>
+__device__ inline void mask_scales(uint32_t (&vs)[2][2 * NB], bool live0, bool live1, int left) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int bb = 0; bb < NB; ++bb) {
-                    const int w = i * NB + bb;
-                    const bool keep = (16 * u + i < left) & (u ? live1 : live0);
-                    vs[u][w >> 1] = keep ? vs[u][w >> 1] : vs[u][w >> 1] & (w & 1 ? 0xffffu : 0xffff0000u);
-                }
-    }
-    if constexpr (!kBf16) {  // an A past those met so far
-        us2 big = __builtin_bit_cast(us2, vs[0][0]);
+            for (int bb = 0; bb < NB; ++bb) {
+                const int w = i * NB + bb;
+                const bool keep = (16 * u + i < left) & (u ? live1 : live0);
+                vs[u][w >> 1] = keep ? vs[u][w >> 1] : vs[u][w >> 1] & (w & 1 ? 0xffffu : 0xffff0000u);
+            }
+}
+
+// Takes a tile's scales of V into the sizes met, and the sums to a larger power of 2 if
+// one is needed.  False, and nothing changed, if the sizes would span more than 2^kSpan.
+template <int NB, int T>
+__device__ inline __attribute__((always_inline)) bool meet(const uint32_t (&vs)[2][2 * NB], v4f (&acc)[T][NB][4], Sizes& sizes) {
+    // none is negative, so the numbers are in the order of their bits (and take three a step)
+    typedef Half<false>::v2 h2;
+    h2 big = __builtin_bit_cast(h2, vs[0][0]), small = big;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 2 * NB; ++i) big = __builtin_elementwise_max(big, __builtin_bit_cast(us2, vs[u][i]));
-        const int top_bits = big.x > big.y ? big.x : big.y, limit = (large + 15) << 10;  // 2^large
-        if (__ballot(top_bits >= limit)) {
-            us2 fin = {0, 0};  // numbers moved up to 0x8400 and past it, the rest below
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 2 * NB; ++i)
-                    fin = __builtin_elementwise_max(fin, __builtin_bit_cast(us2, vs[u][i]) + us2{0x8400, 0x8400});
-            const int top_finite = fin.x > fin.y ? fin.x : fin.y;
-            int now = ((int)column_max((float)top_finite) - 0x8400 >> 10) - 14;
-            now = now > large ? now : large;
-            const float drop = __builtin_amdgcn_exp2f((float)(large - now));
-#pragma unroll
-            for (int t = 0; t < T; ++t)
-#pragma unroll
-                for (int bb = 0; bb < NB; ++bb)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[t][bb][j] *= drop;
-            large = now;
+        for (int i = 0; i < 2 * NB; ++i) {
+            big = __builtin_elementwise_maximum(big, __builtin_bit_cast(h2, vs[u][i]));
+            small = __builtin_elementwise_minimum(small, __builtin_bit_cast(h2, vs[u][i]));
         }
+    const us2 b = __builtin_bit_cast(us2, big), l = __builtin_bit_cast(us2, small);
+    const int top_bits = b.x > b.y ? b.x : b.y, low_bits = l.x < l.y ? l.x : l.y;
+    if (__ballot((top_bits >= (sizes.large + 15) << 10) | (low_bits < sizes.low))) {
+        us2 finite = {0, 0};           // numbers moved up to 0x8400 and past it, the rest below
+        us2 least = {0xffff, 0xffff};  // less 1: a 0 is the largest
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i) {
+                finite = __builtin_elementwise_max(finite, __builtin_bit_cast(us2, vs[u][i]) + us2{0x8400, 0x8400});
+                least = __builtin_elementwise_min(least, __builtin_bit_cast(us2, vs[u][i]) - us2{1, 1});
+            }
+        const int top = finite.x > finite.y ? finite.x : finite.y, not_0 = least.x < least.y ? least.x : least.y;
+        const Sizes met = sizes.guess ? Sizes{kLeastLarge, 0x7c00} : sizes;
+        int large = (((int)column_max((float)top) - 0x8400) >> 10) - 14;
+        large = __builtin_amdgcn_readfirstlane(large > met.large ? large : met.large);
+        int low = (1 - (int)column_max((float)-not_0)) & 0x1fc00;
+        low = __builtin_amdgcn_readfirstlane(low < met.low ? low : met.low);
+        // subnormal numbers reach 2^10 below the first exponent
+        if (large + 15 - (low ? low >> 10 : -10) > kSpan + 1) return false;
+        const float drop = __builtin_amdgcn_exp2f((float)(sizes.large - large));
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int bb = 0; bb < NB; ++bb)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[t][bb][j] *= drop;
+        sizes = Sizes{large, low};
     }
-    scales.take(vs, large);
+    sizes.guess = false;
+    return true;
 }
 
 // One workgroup: one sequence, kv head, row tile of 16 T query rows (token-major,
@@ -499,8 +553,9 @@ __global__ __launch_bounds__(64 * W, simd_waves(NB, T)) void kv_attention_kernel
     constexpr bool kScored = kForm != kFactor;
     constexpr int R = kRing<NB>();
     // V's scales are made ready before the scores or after them: before, with fp16 and
-    // kScored, where 101 registers spilled after (six pieces of prompts of up to 3701 tokens,
-    // 32 / 8 heads of 128: 270 us and 231); else after (181 us and 192)
+    // kScored (a 4096-token prompt of 64 heads of 128, cap 50, pages of 16 tokens: 478 us,
+    // after 500; of 64: 466 and 473); else after (six pieces of prompts of up to 3701
+    // tokens, 32 / 8 heads of 128: 202 us, before 207)
     constexpr bool kEarly = !kBf16 && kScored;
     // one LDS array: the waves' rings, later their sums [wave][row][64 NB + 4] and maxima
     // (a second object would make the compiler wait for every DMA before an LDS read)
@@ -565,12 +620,16 @@ __global__ __launch_bounds__(64 * W, simd_waves(NB, T)) void kv_attention_kernel
         request<NB, kOne>(w, ring + stage * St::kBytes, lane, at_v, at_s);
     };
     const int last = n0 + wave + (n1 - 1 - n0 - wave) / W * W;  // the wave's last tile, if it has any
-    if (first < n1) {
+    // requests the tiles from n on, with none under way
+    const auto start = [&](int n) __attribute__((always_inline)) {
+        first = n;
         pages = load_pages<kOne, W>(a, table, span, first, n1, s.length, lane);
+        live = 0;
 #pragma unroll
         for (int i = 0; i < R; ++i)
             if (first + i * W <= last) ask(first + i * W, i, i);
-    }
+    };
+    if (first < n1) start(first);
 
     // a factor below 0 is taken into q's sign
     const uint32_t flip = !kScored && a.scale < 0.0f ? 0x80008000u : 0u;
@@ -597,7 +656,7 @@ __global__ __launch_bounds__(64 * W, simd_waves(NB, T)) void kv_attention_kernel
     // exponent past which the reference moves (any, for a row that has seen no key yet);
     // the sum of this lane's weights
     float nb[T], thr[T], l[T];
-    int large = kLeastLarge;         // fp16: every A that the wave has met is below 2^large
+    Sizes sizes;
     v4f acc[T][NB][4];
 #pragma unroll
     for (int t = 0; t < T; ++t) {
@@ -610,23 +669,26 @@ __global__ __launch_bounds__(64 * W, simd_waves(NB, T)) void kv_attention_kernel
             for (int j = 0; j < 4; ++j) acc[t][bb][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    int stage = 0;
-    for (int n = first; n < n1; n += W) {
-        const int t0 = tile_token(span, n);
-        const bool live0 = live & 1, live1 = live & 2;
-        live >>= 2;
-        uint32_t kc[2][NB * 2];  // keys 16 u + c: group g's dims, 8 bytes a block
-        uint32_t ks[2][NB * 2];  // scales of keys 16 u + 4 g .. + 3
-        uint32_t vc[2][NB * 2];  // values of keys 16 u + 4 g .. + 3: dims 64 b + 4 c .. + 3
-        uint32_t vs[2][NB * 2];
-        if (n + (R - 1) * W <= last)
-            wait_loads<(R - 1) * St::kIns>();  // the tiles requested after it stay in flight
-        else
-            wait_loads<0>();
-        {
+    int stage = 0, n = first;
+    // The loop over the tiles, with V's scales in the 16-bit type until one does not fit in
+    // (fp16: then the loop with kWide takes up that tile again)
+    const auto run = [&](auto wide) __attribute__((always_inline)) {
+        constexpr bool kWide = decltype(wide)::value;
+        for (; n < n1; n += W) {
+            const int t0 = tile_token(span, n);
+            const bool live0 = live & 1, live1 = live & 2;
+            uint32_t kc[2][NB * 2];  // keys 16 u + c: group g's dims, 8 bytes a block
+            uint32_t ks[2][NB * 2];  // scales of keys 16 u + 4 g .. + 3
+            uint32_t vc[2][NB * 2];  // values of keys 16 u + 4 g .. + 3: dims 64 b + 4 c .. + 3
+            uint32_t vs[2][NB * 2];
+            if (n + (R - 1) * W <= last)
+                wait_loads<(R - 1) * St::kIns>();  // the tiles requested after it stay in flight
+            else
+                wait_loads<0>();
             const uint32_t st = ring_at + stage * St::kBytes;
             read_share(kc, vc, ks, vs, st + (c * 32 + g * 8) * NB, st + 1024 * NB + (g * 128 + c * 8) * NB,
                        st + St::kScales + g * 8 * NB);
+            live >>= 2;
             const int nn = n + R * W;
             if (nn <= last) {
                 if ((nn - first) / W >= 64) {
@@ -636,182 +698,205 @@ __global__ __launch_bounds__(64 * W, simd_waves(NB, T)) void kv_attention_kernel
                 ask(nn, stage, R - 1);
             }
             stage = stage + 1 < R ? stage + 1 : 0;
-        }
-        // every key of the tile visible to every row: no masks
-        const bool whole = live0 & live1 & (pos0 >= 0) &
-                           ((t0 + kTile <= s.prefix) |
-                            ((t0 + kTile - 1 <= pos0) & ((a.window == 0) | (pos1 - t0 < a.window))));
-        Weights<kBf16, NB> scales;
-        if constexpr (kEarly) take_scales<kBf16, NB, T>(scales, vs, acc, large, !whole, live0, live1, s.length - t0 - 4 * g);
-        float x[T][2][4];
+            // every key of the tile visible to every row: no masks
+            const bool whole = live0 & live1 & (pos0 >= 0) &
+                               ((t0 + kTile <= s.prefix) |
+                                ((t0 + kTile - 1 <= pos0) & ((a.window == 0) | (pos1 - t0 < a.window))));
+            Weights<kBf16, NB> scales;  // not with kWide
+            const auto take = [&]() __attribute__((always_inline)) {
+                if (!whole) mask_scales<NB>(vs, live0, live1, s.length - t0 - 4 * g);
+                if constexpr (!kBf16 && !kWide)
+                    if (!meet<NB, T>(vs, acc, sizes)) return false;
+                if constexpr (!kWide) scales.take(vs, sizes.large);
+                return true;
+            };
+            if constexpr (kEarly)
+                if (!take()) break;
+            float x[T][2][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            v8 k[NB][2];
+            for (int u = 0; u < 2; ++u) {
+                v8 k[NB][2];
 #pragma unroll
-            for (int bb = 0; bb < NB; ++bb)
+                for (int bb = 0; bb < NB; ++bb)
 #pragma unroll
-                for (int st = 0; st < 2; ++st) k[bb][st] = codes8<kBf16>(kc[u][2 * bb + st]);
-            float sk[4][NB];
+                    for (int st = 0; st < 2; ++st) k[bb][st] = codes8<kBf16>(kc[u][2 * bb + st]);
+                float sk[4][NB];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int bb = 0; bb < NB; ++bb) sk[i][bb] = scale_at<kBf16, NB>(ks[u], i, bb) * unit;
+                    for (int bb = 0; bb < NB; ++bb) sk[i][bb] = scale_at<kBf16, NB>(ks[u], i, bb) * unit;
 #pragma unroll
-            for (int t = 0; t < T; ++t) {
-                v4f p[NB];
+                for (int t = 0; t < T; ++t) {
+                    v4f p[NB];
 #pragma unroll
-                for (int bb = 0; bb < NB; ++bb) {
-                    p[bb] = H::mfma(k[bb][0], q[t][bb][0], v4f{0.0f, 0.0f, 0.0f, 0.0f});
-                    p[bb] = H::mfma(k[bb][1], q[t][bb][1], p[bb]);
-                }
+                    for (int bb = 0; bb < NB; ++bb) {
+                        p[bb] = H::mfma(k[bb][0], q[t][bb][0], v4f{0.0f, 0.0f, 0.0f, 0.0f});
+                        p[bb] = H::mfma(k[bb][1], q[t][bb][1], p[bb]);
+                    }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[t][u][i] = kScored ? p[0][i] * sk[i][0] : fmaf(p[0][i], sk[i][0], nb[t]);
+                    for (int i = 0; i < 4; ++i) {
+                        x[t][u][i] = kScored ? p[0][i] * sk[i][0] : fmaf(p[0][i], sk[i][0], nb[t]);
 #pragma unroll
-                    for (int bb = 1; bb < NB; ++bb) x[t][u][i] = fmaf(p[bb][i], sk[i][bb], x[t][u][i]);
+                        for (int bb = 1; bb < NB; ++bb) x[t][u][i] = fmaf(p[bb][i], sk[i][bb], x[t][u][i]);
+                    }
                 }
             }
-        }
-        if (kScored) {
-            if (a.softcap > 0.0f) {
-                // the scores that may be past the polynomial: of a near cap all, of a far one few tiles'
-                bool past = true;
-                if constexpr (kForm == kFarCap) {
-                    float most = 0.0f;
+            if (kScored) {
+                if (a.softcap > 0.0f) {
+                    // the scores that may be past the polynomial: of a near cap all, of a far one few tiles'
+                    bool past = true;
+                    if constexpr (kForm == kFarCap) {
+                        float most = 0.0f;
+#pragma unroll
+                        for (int t = 0; t < T; ++t)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    x[t][u][i] *= a.to_y;
+                                    most = fmaxf(most, fabsf(x[t][u][i]));
+                                }
+                        past = __ballot(most > kTanhSmall) != 0;
+                    }
+#pragma unroll
+                    for (int t = 0; t < T; ++t) {
+                        const float top = a.cap + nb[t];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float y = x[t][u][i];
+                                if (past) {
+                                    const float e = __builtin_amdgcn_exp2f(y * (kForm == kFarCap ? 2.0f * kLog2e : a.to_e));
+                                    x[t][u][i] = fmaf(__builtin_amdgcn_rcpf(1.0f + e), -2.0f * a.cap, top);
+                                }
+                                if constexpr (kForm == kFarCap)
+                                    x[t][u][i] = fabsf(y) > kTanhSmall ? x[t][u][i] : fmaf(tanh_small(y), a.cap, nb[t]);
+                            }
+                    }
+                } else {
 #pragma unroll
                     for (int t = 0; t < T; ++t)
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                x[t][u][i] *= a.to_y;
-                                most = fmaxf(most, fabsf(x[t][u][i]));
-                            }
-                    past = __ballot(most > kTanhSmall) != 0;
+                            for (int i = 0; i < 4; ++i) x[t][u][i] = fmaf(x[t][u][i], a.to_s, nb[t]);
                 }
+                if (a.alibi) {
 #pragma unroll
-                for (int t = 0; t < T; ++t) {
-                    const float top = a.cap + nb[t];
+                    for (int t = 0; t < T; ++t) {
+                        const float away = (float)(pos[t] - t0 - 4 * g);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
+                        for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float y = x[t][u][i];
-                            if (past) {
-                                const float e = __builtin_amdgcn_exp2f(y * (kForm == kFarCap ? 2.0f * kLog2e : a.to_e));
-                                x[t][u][i] = fmaf(__builtin_amdgcn_rcpf(1.0f + e), -2.0f * a.cap, top);
-                            }
-                            if constexpr (kForm == kFarCap)
-                                x[t][u][i] = fabsf(y) > kTanhSmall ? x[t][u][i] : fmaf(tanh_small(y), a.cap, nb[t]);
-                        }
+                            for (int i = 0; i < 4; ++i)
+                                x[t][u][i] = fmaf(-slope[t], fabsf(away - (float)(16 * u + i)), x[t][u][i]);
+                    }
                 }
-            } else {
+            }
+            if (!whole) {
 #pragma unroll
                 for (int t = 0; t < T; ++t)
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) x[t][u][i] = fmaf(x[t][u][i], a.to_s, nb[t]);
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = t0 + 16 * u + 4 * g + i;
+                            // bitwise, so that this is compares and a select: short circuits became
+                            // branches, and among them the compiler lost a copy of a score
+                            const bool see = (((j < s.prefix) & (pos[t] >= 0)) | ((j <= pos[t]) & (pos[t] - j < reach))) &
+                                             (u ? live1 : live0);
+                            x[t][u][i] = see ? x[t][u][i] : -INFINITY;
+                        }
             }
-            if (a.alibi) {
+            if constexpr (!kEarly)
+                if (!take()) break;
+            typedef Half<kBf16 || kWide> V;
+            typename V::v8 pa[T][NB], rest[kWide ? T : 1][NB];
 #pragma unroll
-                for (int t = 0; t < T; ++t) {
-                    const float away = (float)(pos[t] - t0 - 4 * g);
+            for (int t = 0; t < T; ++t) {
+                float top = x[t][0][0];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = fmaxf(top, x[t][u][i]);
+                if (__ballot(top > thr[t])) {  // some row's reference moves, or is its first
+                    top = column_max(top);
+                    const bool fresh = thr[t] == -INFINITY;
+                    // (a fresh row with no key in sight stays as it is)
+                    float by = top - kShift<kBf16>;
+                    by = fresh ? (top == -INFINITY ? 0.0f : by) : fmaxf(by, 0.0f);
+                    const float drop = fresh ? 0.0f : __builtin_amdgcn_exp2f(-by);
+                    thr[t] = fresh & (top == -INFINITY) ? thr[t] : kShift<kBf16> + kSlack<kBf16>;
+                    nb[t] -= by;
+                    l[t] *= drop;
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            x[t][u][i] = fmaf(-slope[t], fabsf(away - (float)(16 * u + i)), x[t][u][i]);
-                }
-            }
-        }
-        if (!whole) {
+                        for (int i = 0; i < 4; ++i) x[t][u][i] -= by;
 #pragma unroll
-            for (int t = 0; t < T; ++t)
+                    for (int bb = 0; bb < NB; ++bb)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[t][bb][j] *= drop;
+                }
+                float w[2][4];
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int j = t0 + 16 * u + 4 * g + i;
-                        // bitwise, so that this is compares and a select: short circuits became
-                        // branches, and among them the compiler lost a copy of a score
-                        const bool see = (((j < s.prefix) & (pos[t] >= 0)) | ((j <= pos[t]) & (pos[t] - j < reach))) &
-                                         (u ? live1 : live0);
-                        x[t][u][i] = see ? x[t][u][i] : -INFINITY;
+                        w[u][i] = __builtin_amdgcn_exp2f(x[t][u][i]);
+                        l[t] += w[u][i];
                     }
-        }
-        if constexpr (!kEarly) take_scales<kBf16, NB, T>(scales, vs, acc, large, !whole, live0, live1, s.length - t0 - 4 * g);
-        v8 pa[T][NB];
+                if constexpr (kWide) {
+                    const float f = __builtin_amdgcn_exp2f((float)(4 - sizes.large));
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
-            float top = x[t][0][0];
+                    for (int bb = 0; bb < NB; ++bb)
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+                        for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, x[t][u][i]);
-            if (__ballot(top > thr[t])) {  // some row's reference moves, or is its first
-                top = column_max(top);
-                const bool fresh = thr[t] == -INFINITY;
-                // (a fresh row with no key in sight stays as it is)
-                float by = top - kShift<kBf16>;
-                by = fresh ? (top == -INFINITY ? 0.0f : by) : fmaxf(by, 0.0f);
-                const float drop = fresh ? 0.0f : __builtin_amdgcn_exp2f(-by);
-                thr[t] = fresh & (top == -INFINITY) ? thr[t] : kShift<kBf16> + kSlack<kBf16>;
-                nb[t] -= by;
-                l[t] *= drop;
+                            for (int i = 0; i < 4; ++i) {
+                                const bool masked = !whole && x[t][u][i] == -INFINITY;
+                                const float p = masked ? 0.0f : w[u][i] * f * scale_at<false, NB>(vs[u], i, bb);
+                                pa[t][bb][4 * u + i] = (__bf16)p;
+                                rest[t][bb][4 * u + i] = (__bf16)(p - (float)pa[t][bb][4 * u + i]);
+                            }
+                } else {
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                    for (int bb = 0; bb < NB; ++bb) pa[t][bb] = scales.times(w, bb);
+                    // a masked key's value may be no number: its product is 0
+                    if (!whole) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[t][u][i] -= by;
+                        for (int bb = 0; bb < NB; ++bb)
 #pragma unroll
-                for (int bb = 0; bb < NB; ++bb)
+                            for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[t][bb][j] *= drop;
-            }
-            float w[2][4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    w[u][i] = __builtin_amdgcn_exp2f(x[t][u][i]);
-                    l[t] += w[u][i];
+                                for (int i = 0; i < 4; ++i)
+                                    pa[t][bb][4 * u + i] = x[t][u][i] == -INFINITY ? (typename H::T)0.0f : pa[t][bb][4 * u + i];
+                    }
                 }
+            }
 #pragma unroll
-            for (int bb = 0; bb < NB; ++bb) pa[t][bb] = scales.times(w, bb);
-            // a masked key's value may be no number: its product is 0
-            if (!whole) {
+            for (int bb = 0; bb < NB; ++bb) {
+                const Nibbles v = pair_nibbles(vc[0][2 * bb], vc[0][2 * bb + 1], vc[1][2 * bb], vc[1][2 * bb + 1]);
 #pragma unroll
-                for (int bb = 0; bb < NB; ++bb)
+                for (int j = 0; j < 4; ++j) {
+                    const typename V::v8 va = values_of<kBf16 || kWide>(v, j);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            pa[t][bb][4 * u + i] = x[t][u][i] == -INFINITY ? (typename H::T)0.0f : pa[t][bb][4 * u + i];
+                    for (int t = 0; t < T; ++t) {
+                        acc[t][bb][j] = V::mfma(va, pa[t][bb], acc[t][bb][j]);
+                        if constexpr (kWide) acc[t][bb][j] = V::mfma(va, rest[t][bb], acc[t][bb][j]);
+                    }
+                }
             }
         }
-        // V^T: a word holds two tokens' dims 0 .. 3; pairing the words' nibbles makes
-        // bytes (token 0, token 1) and (token 2, token 3) of one dim
-#pragma unroll
-        for (int bb = 0; bb < NB; ++bb) {
-            uint32_t ev[2], od[2];  // dims 0 and 2, dims 1 and 3
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint32_t wa = vc[u][2 * bb], wb = vc[u][2 * bb + 1];
-                ev[u] = (wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u);
-                od[u] = ((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t x0 = j & 1 ? od[0] : ev[0], x1 = j & 1 ? od[1] : ev[1];
-                typename H::v2 e[4];
-                e[0] = j < 2 ? H::template codes<0>(x0) : H::template codes<1>(x0);
-                e[1] = j < 2 ? H::template codes<2>(x0) : H::template codes<3>(x0);
-                e[2] = j < 2 ? H::template codes<0>(x1) : H::template codes<1>(x1);
-                e[3] = j < 2 ? H::template codes<2>(x1) : H::template codes<3>(x1);
-                const v8 va{e[0].x, e[0].y, e[1].x, e[1].y, e[2].x, e[2].y, e[3].x, e[3].y};
-#pragma unroll
-                for (int t = 0; t < T; ++t) acc[t][bb][j] = H::mfma(va, pa[t][bb], acc[t][bb][j]);
-            }
+    };
+    run(std::false_type{});
+    if constexpr (!kBf16) {
+        if (n < n1) {
+            wait_loads<0>();
+            start(n);
+            stage = 0;
+            run(std::true_type{});
         }
     }
 
@@ -820,7 +905,7 @@ __global__ __launch_bounds__(64 * W, simd_waves(NB, T)) void kv_attention_kernel
     float2 (*ml)[kCols] = reinterpret_cast<float2 (*)[kCols]>(smem + sizeof(smem) - W * kCols * 8);
     const int d0 = tid & 15;  // 16 lanes a row, 4 dims a step
     wait_loads<0>();  // this wave's DMA has landed; after the barrier every wave's
-    const float grow = kBf16 ? 1.0f : __builtin_amdgcn_exp2f((float)(large - 4));
+    const float grow = kBf16 ? 1.0f : __builtin_amdgcn_exp2f((float)(sizes.large - 4));
 #pragma unroll
     for (int t = 0; t < T; ++t) {
         const float ls = column_sum(l[t]);

@@ -86,6 +86,66 @@ def test_log_sum_exp_of_rows_that_meet_no_number(n, kind, softcap):
     assert bool((none == 0).all()) and bool(torch.isneginf(none_lse).all())
 
 
+SPREADS = {
+    # log2 of the sizes of V's blocks by key and block, and where the scores lean to
+    "block": lambda j, b: np.where(b == 0, 12.0, -10.0) + 0 * j,
+    "first_key": lambda j, b: np.where(j == 0, 14.0, -9.0) + 0 * b,
+    "last_key": lambda j, b: np.where(j == j.max(), 14.0, -9.0) + 0 * b,
+    "small_key": lambda j, b: np.where(j == 5, -10.0, 13.0) + 0 * b,
+    "small_last": lambda j, b: np.where(j == j.max(), -10.0, 13.0) + 0 * b,
+    "every_other": lambda j, b: np.where(j % 2 == 0, 14.0, -10.0) + 0 * b,
+    "falling": lambda j, b: 15.0 - 27.0 * j / j.max() + 0 * b,
+    "rising": lambda j, b: 27.0 * j / j.max() - 12.0 + 0 * b,
+}
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("lean", [24.0, 7.0], ids=["none", "some"])
+@pytest.mark.parametrize("spread", SPREADS)
+def test_values_of_very_different_sizes(spread, lean, kind):
+    """The keys that draw a row's weight hold values 2^20 and more below others' that draw none, or about e^-20 of it."""
+    rng = np.random.default_rng([42, len(spread)])
+    heads, d, page = 1, 128, 32
+    for n, queries in ((100, 1), (700, 1), (700, 20), (700, 45), (5000, 1)):
+        j, b = np.arange(n)[:, None], np.arange(2)[None]
+        size = np.asarray(SPREADS[spread](j, b), np.float64)
+        q = draw(rng, (queries, heads, d), kind, 0.1)
+        along = q[0, 0] / np.abs(q[0, 0]).max()
+        to = np.where(size.min(1) < 0, lean, -lean)       # keys of small values draw the weight
+        k = kv.round16(to[:, None, None] * along * 0.3 + 0.1 * rng.standard_normal((n, heads, d)), kind)
+        q[:] = q[0]
+        v = kv.round16(np.clip(rng.standard_normal((n, heads, 2, 64)) * 0.4, -1, 1) * np.exp2(size)[:, None, :, None], kind)
+        v = v.reshape(n, heads, d)
+        c = make_cache(-(-n // page), heads, d, page, kind)
+        say(f"fp4_cache_attention, {spread} values, lean {lean}, {n} keys, {queries} queries {kind}")
+        i8.fp4_cache_write(c, dev16(k, kind), dev16(v, kind), torch.arange(n, device="cuda"))
+        out, lse = i8.fp4_cache_attention(dev16(q, kind), c, dev(np.arange(-(-n // page))[None], torch.int32),
+                                          dev(np.array([n]), torch.int32), max_q=queries, return_lse=True)
+        torch.cuda.synchronize()
+        check(out, lse, [(q, kv.dequantize(*kv.quantize(k)), kv.dequantize(*kv.quantize(v)))], d ** -0.5, kind)
+
+
+@pytest.mark.parametrize("mask", [dict(window=20), dict(window=20, softcap=30.0), dict()], ids=["window", "cap", "causal"])
+def test_hidden_keys_of_large_values(mask):
+    """Keys out of sight, in the tiles of those in sight, hold values 2^24 above them."""
+    rng = np.random.default_rng(43)
+    heads, d, page, n, kind = 2, 64, 64, 90, "f16"
+    for queries in (1, 18, 50):
+        q = draw(rng, (queries, heads, d), kind, 0.3)
+        k, v = draw(rng, (n, heads, d), kind, 0.3), draw(rng, (n, heads, d), kind, 0.3) * 2.0 ** -8
+        seen = n - 1 if mask else n - queries           # the first query's last key
+        big = np.arange(seen - 22, seen - 20) if mask else np.arange(seen + 1, n)
+        v[big] = kv.round16(np.clip(v[big] * 2.0 ** 24, -6e4, 6e4), kind)
+        v = kv.round16(v, kind)
+        c = make_cache(2, heads, d, page, kind)
+        say(f"fp4_cache_attention with large values out of sight, {queries} queries {mask}")
+        i8.fp4_cache_write(c, dev16(k, kind), dev16(v, kind), torch.arange(n, device="cuda"))
+        out, lse = i8.fp4_cache_attention(dev16(q, kind), c, dev(np.array([[0, 1]]), torch.int32),
+                                          dev(np.array([n]), torch.int32), max_q=queries, return_lse=True, **mask)
+        torch.cuda.synchronize()
+        check(out, lse, [(q, kv.dequantize(*kv.quantize(k)), kv.dequantize(*kv.quantize(v)))], d ** -0.5, kind, **mask)
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_write_blocks_of_the_smallest_numbers(d):
     """bfloat16 blocks whose factor 6 / A passes the largest fp32 number: every byte is the oracle's."""
