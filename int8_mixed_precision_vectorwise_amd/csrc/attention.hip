@@ -53,11 +53,17 @@ void plan(KvAttnArgs& a) {
     if (a.window > 0 && a.window + (int64_t)a.max_q + 2 * kTile < near) near = a.window + (int64_t)a.max_q + 2 * kTile;
     const int64_t chip = 256 * simd_waves(NB, T);
     const int64_t tiles = ceil_div(near, kTile), most = ceil_div(a.prefix ? a.max_len : near, kTile);
-    int64_t per = ceil_div(tiles * segments, a.batch > 1 ? 2 * chip : chip);
+    const int64_t fill = a.batch > 1 ? 2 * chip : chip;
+    int64_t per = ceil_div(tiles * segments, fill);
     per = per < 4 ? 4 : per;
     if (most <= whole_tiles(segments, T, NB) || segments >= 4 * chip) per = most > 0 ? most : 1;
     a.chunk_tiles = (int32_t)per;
-    a.chunks = (int32_t)ceil_div(most > 0 ? most : 1, per);
+    // No more parts than fill the chip, whatever a prefix beside a window may reach (all of a
+    // table of 131072 tokens took 64 sequences of 64 / 8 heads 926 MiB of workspace and 233000
+    // workgroups for 35 tiles each, 354 us; 8 MiB and 33 us so): where it does reach further,
+    // the parts are longer.
+    const int64_t parts = ceil_div(most > 0 ? most : 1, per), full = ceil_div(fill, segments);
+    a.chunks = (int32_t)(parts < full ? parts : full);
     a.waves = T == 1 && a.chunks == 1 && segments <= 256 && most >= 8 ? 8 : 4;
     if (T == 3 && NB == 2 && a.chunks == 1 && real_segments(a) * 2 >= 1024 * simd_waves(NB, T) * 3) a.waves = 1;
     a.slot_rows = (int32_t)(rows < a.tile_rows ? rows : a.tile_rows);

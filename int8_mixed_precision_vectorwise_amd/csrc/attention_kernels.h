@@ -127,7 +127,8 @@ __device__ inline Span span_of(const Seq& s, int i0, int i1, int window) {
 // parts, nearly equal, each for one workgroup (at least one part: rows that see
 // nothing still get their zeros).
 __device__ inline int parts_of(const KvAttnArgs& a, int n) {
-    const int p = (n + a.chunk_tiles - 1) / a.chunk_tiles;
+    int p = (n + a.chunk_tiles - 1) / a.chunk_tiles;
+    p = p > a.chunks ? a.chunks : p;
     return p < 1 ? 1 : p;
 }
 

@@ -62,7 +62,7 @@ struct KvAttnArgs {
     float cap;                       // softcap in units of log2 e
     int32_t tile_rows, row_tiles;    // rows of a row tile, row tiles of the longest sequence
     int32_t waves;                   // waves of a workgroup
-    int32_t chunk_tiles, chunks;     // most key tiles of a part, most parts of a segment (kv head of a row tile)
+    int32_t chunk_tiles, chunks;     // key tiles of a part, most parts of a segment (kv head of a row tile)
     int32_t slot_rows;               // rows that a part leaves (up to tile_rows)
     int32_t join_rows, join_groups;  // rows of a workgroup of the join, its workgroups for a segment
     uint32_t block0;                 // first workgroup of the launch
