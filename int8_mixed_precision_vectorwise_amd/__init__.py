@@ -94,6 +94,8 @@ def _rowmajor(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
         raise ValueError(f"{name} must be 2-D")
     if t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit column stride")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must not have rows that overlap (an expanded tensor: make it contiguous)")
     return max(t.stride(0), t.shape[1], 1)
 
 

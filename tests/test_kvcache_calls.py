@@ -1,7 +1,9 @@
 """Host side of the 4-bit cache's calls: what they ask for and what they refuse."""
 
 import pytest
+import torch
 
+import int8_mixed_precision_vectorwise_amd as i8
 from int8_mixed_precision_vectorwise_amd import _lib
 from test_kvcache_abi import A16, cache, call, ref
 
@@ -19,3 +21,17 @@ def test_workspace_of_a_window_and_a_prefix_does_not_grow_with_the_table(d, kv_h
         sizes.append(need(ref(c), ref(p)))
     assert len(set(sizes)) == 1, sizes
     assert sizes[0] <= 64 << 20
+
+
+def test_rows_that_overlap_are_refused():
+    """An expanded table has one row in memory: as rows of its width it would be read past its end."""
+    one = torch.zeros((1, 5), dtype=torch.int32)
+    for t in (one.expand(3, 5), torch.zeros(9, dtype=torch.int32).as_strided((3, 5), (2, 1)), torch.zeros((1, 1), dtype=torch.int32).expand(4, 1)):
+        with pytest.raises(ValueError, match="overlap"):
+            i8._rowmajor(t, "table", torch.int32)
+    assert i8._rowmajor(one, "table", torch.int32) == 5
+    assert i8._rowmajor(one.expand(1, 5), "table", torch.int32) == 5
+    assert i8._rowmajor(torch.zeros((4, 9), dtype=torch.int32)[:, :5], "table", torch.int32) == 9
+    assert i8._rowmajor(torch.zeros((0, 5), dtype=torch.int32), "table", torch.int32) == 5
+    assert i8._rowmajor(torch.zeros((3, 0), dtype=torch.int32), "table", torch.int32) == 1
+    assert i8._rowmajor(torch.zeros((3, 1), dtype=torch.int32), "table", torch.int32) == 1
