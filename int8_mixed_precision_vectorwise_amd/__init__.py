@@ -104,6 +104,12 @@ def _vec(t: torch.Tensor, name: str, dtype: torch.dtype, n: int) -> None:
         raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n}")
 
 
+def _bytes(t: torch.Tensor, name: str) -> None:
+    """t can be written as a run of t.numel() bytes."""
+    if t.dtype != torch.uint8 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {torch.uint8} tensor")
+
+
 def vectorwise_quant(x: torch.Tensor, threshold: float = DEFAULT_THRESHOLD,
                      ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """int8_vectorwise_quant: (codes int8 [m,k], row absmax fp32 [m], outlier bitmap uint32-as-int32)."""
@@ -742,8 +748,8 @@ def fp4_cache_attention(q: torch.Tensor, cache: Fp4Cache, table: torch.Tensor, l
     (int32 [batch]) tokens.  ``softcap`` > 0 caps scores by a tanh; ``alibi`` (fp32
     [q_heads]) subtracts alibi * distance.  ``scale`` defaults to head_dim ** -0.5,
     ``max_len`` (a bound on the lengths) to the table's width.  A row that sees
-    nothing is zeros, its lse -inf.  ``workspace``: uint8, reused by the caller
-    (default: allocated here)."""
+    nothing is zeros, its lse -inf.  ``workspace``: contiguous uint8, reused by the
+    caller (default: allocated here)."""
     dev = _device_of(q, cache.data, table, lengths, q_offsets, alibi, prefix, out, workspace)
     c = cache.struct()
     ldq, hsq = _heads(q, "q", cache.dtype, None, c.head_dim)
@@ -776,7 +782,9 @@ def fp4_cache_attention(q: torch.Tensor, cache: Fp4Cache, table: torch.Tensor, l
         None if alibi is None else alibi.data_ptr(), None if prefix is None else prefix.data_ptr(), tokens, batch,
         q_heads, max(max_q, 1), cols * cache.page_size if max_len is None else max_len, window,
         c.head_dim ** -0.5 if scale is None else scale, softcap)
-    if workspace is None:
+    if workspace is not None:
+        _bytes(workspace, "workspace")
+    else:
         need = lib().i8mp_fp4_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(call))
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _run(dev, "i8mp_fp4_cache_attention", ctypes.byref(c), ctypes.byref(call),

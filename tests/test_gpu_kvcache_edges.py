@@ -169,3 +169,15 @@ def test_write_blocks_of_the_smallest_numbers(d):
     assert np.array_equal(host(c.data), want)
     for g, r in zip(got, kv.read(want, page, d, range(n), kind)):
         assert np.array_equal(wide(g).view(np.int32), np.asarray(r, np.float32).view(np.int32))
+
+
+def test_views_that_would_be_read_or_written_past_their_end():
+    c = make_cache(4, 1, 64, 16, "f16")
+    q = torch.zeros((2, 1, 64), dtype=torch.float16, device="cuda")
+    table, lengths = torch.zeros((2, 4), dtype=torch.int32, device="cuda"), torch.ones(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="overlap"):
+        i8.fp4_cache_attention(q, c, table[:1].expand(2, 4), lengths)
+    for bad in (torch.zeros(1, dtype=torch.uint8, device="cuda").expand(1 << 20), torch.zeros(1 << 20, device="cuda"),
+                torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            i8.fp4_cache_attention(q, c, table, lengths, workspace=bad)

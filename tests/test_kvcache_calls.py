@@ -35,3 +35,12 @@ def test_rows_that_overlap_are_refused():
     assert i8._rowmajor(torch.zeros((0, 5), dtype=torch.int32), "table", torch.int32) == 5
     assert i8._rowmajor(torch.zeros((3, 0), dtype=torch.int32), "table", torch.int32) == 1
     assert i8._rowmajor(torch.zeros((3, 1), dtype=torch.int32), "table", torch.int32) == 1
+
+
+def test_a_workspace_is_a_run_of_bytes():
+    """numel() is taken for the bytes that may be written: not so for an expanded tensor, or one with gaps."""
+    for t in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(64, dtype=torch.uint8)[::2],
+              torch.zeros(64), torch.zeros((8, 8), dtype=torch.uint8).t()):
+        with pytest.raises(ValueError, match="workspace must be a contiguous"):
+            i8._bytes(t, "workspace")
+    i8._bytes(torch.zeros((4, 16), dtype=torch.uint8)[1:], "workspace")
