@@ -696,6 +696,20 @@ def _heads(t: torch.Tensor, name: str, dtype: torch.dtype, heads: Optional[int],
     return (ld if shape[0] > 1 else head_dim), (hs if shape[1] > 1 else head_dim)
 
 
+def _int32(**values: int) -> None:
+    """The values are whole in an int32 of a C structure (ctypes keeps the low 32 bits of others)."""
+    for name, value in values.items():
+        if not -1 << 31 <= value < 1 << 31:
+            raise ValueError(f"{name} is out of range: {value}")
+
+
+def _float32(**values: float) -> None:
+    """The values that are not 0 are not 0 in fp32 either."""
+    for name, value in values.items():
+        if value != 0.0 and ctypes.c_float(value).value == 0.0:
+            raise ValueError(f"{name} is less than any fp32 number: {value}")
+
+
 def fp4_cache_write(cache: Fp4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
     """Quantizes k and v [tokens, kv_heads, head_dim] into the cache's slots (int64 [tokens], distinct).
 
@@ -776,12 +790,14 @@ def fp4_cache_attention(q: torch.Tensor, cache: Fp4Cache, table: torch.Tensor, l
     if out.shape[0] != tokens:
         raise ValueError("out has the wrong shape")
     lse = q.new_empty((tokens, q_heads), dtype=torch.float32) if return_lse else None
+    max_len = cols * cache.page_size if max_len is None else max_len
+    _int32(max_q=max_q, max_len=max_len, window=window)
+    _float32(softcap=softcap)
     call = Fp4AttentionStruct(
         q.data_ptr(), ldq, hsq, out.data_ptr(), ldo, hso, None if lse is None else lse.data_ptr(), table.data_ptr(), ldt,
         cols, lengths.data_ptr(), None if q_offsets is None else q_offsets.data_ptr(),
         None if alibi is None else alibi.data_ptr(), None if prefix is None else prefix.data_ptr(), tokens, batch,
-        q_heads, max(max_q, 1), cols * cache.page_size if max_len is None else max_len, window,
-        c.head_dim ** -0.5 if scale is None else scale, softcap)
+        q_heads, max(max_q, 1), max_len, window, c.head_dim ** -0.5 if scale is None else scale, softcap)
     if workspace is not None:
         _bytes(workspace, "workspace")
     else:

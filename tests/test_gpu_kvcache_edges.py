@@ -181,3 +181,14 @@ def test_views_that_would_be_read_or_written_past_their_end():
                 torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")[::2]):
         with pytest.raises(ValueError, match="workspace"):
             i8.fp4_cache_attention(q, c, table, lengths, workspace=bad)
+
+
+def test_values_past_32_bits_are_refused():
+    c = make_cache(4, 1, 64, 16, "f16")
+    q = torch.zeros((2, 1, 64), dtype=torch.float16, device="cuda")
+    table, lengths = torch.zeros((2, 4), dtype=torch.int32, device="cuda"), torch.ones(2, dtype=torch.int32, device="cuda")
+    offsets = torch.arange(3, dtype=torch.int32, device="cuda")
+    for bad in (dict(window=(1 << 32) + 1), dict(max_len=(1 << 32) + 16), dict(q_offsets=offsets, max_q=(1 << 32) + 1),
+                dict(softcap=1e-50)):
+        with pytest.raises(ValueError):
+            i8.fp4_cache_attention(q, c, table, lengths, **bad)

@@ -44,3 +44,17 @@ def test_a_workspace_is_a_run_of_bytes():
         with pytest.raises(ValueError, match="workspace must be a contiguous"):
             i8._bytes(t, "workspace")
     i8._bytes(torch.zeros((4, 16), dtype=torch.uint8)[1:], "workspace")
+
+
+def test_values_that_the_c_call_cannot_hold():
+    """ctypes keeps an int's low 32 bits (a window of 2^32 + 1 became one of 1) and rounds a tiny cap to none."""
+    call_ = _lib.Fp4AttentionStruct(window=(1 << 32) + 1, softcap=1e-50)
+    assert call_.window == 1 and call_.softcap == 0.0
+    for bad in ((1 << 32) + 1, 1 << 31, -(1 << 31) - 1):
+        with pytest.raises(ValueError, match="window is out of range"):
+            i8._int32(max_q=1, window=bad)
+    i8._int32(a=(1 << 31) - 1, b=-(1 << 31), c=0)
+    for bad in (1e-50, -1e-50):
+        with pytest.raises(ValueError, match="softcap is less"):
+            i8._float32(softcap=bad)
+    i8._float32(a=0.0, b=1e-44, c=float("nan"), d=1e60)
