@@ -623,8 +623,9 @@ def fp4_linear(x: torch.Tensor, fw: Fp4Weight, bias: Optional[torch.Tensor] = No
 
 _DTYPE_CODE = {torch.float16: 0, torch.float32: 1, torch.bfloat16: 2}
 _CACHE_CODE = {torch.float16: 0, torch.bfloat16: 2}
-# the handle of a device's current stream, without a Stream object around it (2 us a call)
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# the handle of a device's current stream, without a Stream object around it (2 us a call);
+# a torch built without GPU support has none, and no tensor that would need it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 @dataclass

@@ -1,5 +1,9 @@
 """Host side of the 4-bit cache's calls: what they ask for and what they refuse."""
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -58,3 +62,16 @@ def test_values_that_the_c_call_cannot_hold():
         with pytest.raises(ValueError, match="softcap is less"):
             i8._float32(softcap=bad)
     i8._float32(a=0.0, b=1e-44, c=float("nan"), d=1e60)
+
+
+def test_the_package_imports_without_gpu_support_in_torch():
+    """A torch built for the CPU alone has no raw stream handle."""
+    code = ("import torch\n"
+            "del torch._C._cuda_getCurrentRawStream\n"
+            "import int8_mixed_precision_vectorwise_amd as i8\n"
+            "c = i8.Fp4Cache.create(2, 1, 64, 16, device='cpu')\n"
+            "try:\n    i8.fp4_cache_read(c, torch.zeros(1, dtype=torch.int64))\n"
+            "except ValueError as e:\n    print('refused:', e)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=100)
+    assert r.returncode == 0 and "no CPU path" in r.stdout, r.stderr
