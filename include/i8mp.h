@@ -486,8 +486,9 @@ i8mp_status i8mp_fp4_cache_read(const i8mp_fp4_cache* cache /* host */, const in
  * cut, and so the order of the sums, follows from the call's sizes.
  *
  * What is read on the device is bounded there: lengths are taken into [0, max_len],
- * query offsets into [0, tokens], a sequence's queries past max_q are left out, and
- * tokens on a page outside [0, pages) are not visible.  Tokens past a sequence's
+ * query offsets into [0, tokens], a sequence's queries past max_q are left out (their
+ * rows of out and lse, as those in no sequence, are left as they are, or get zeros and
+ * -inf with `fill`), and tokens on a page outside [0, pages) are not visible.  Tokens past a sequence's
  * length may hold anything. */
 typedef struct i8mp_fp4_attention {
     const void* q;            /* [tokens x q_heads x head_dim], strides ldq, hsq     */
@@ -516,6 +517,7 @@ typedef struct i8mp_fp4_attention {
     float scale;
     float softcap;            /* 0: none.  Any positive value; a capped score is within
                                  2^-17 or 2^-20 of its value of cap tanh(s / cap)    */
+    int32_t fill;             /* 1: rows of q that are no sequence's queries are filled  */
 } i8mp_fp4_attention;
 
 /* Host.  Workspace of a call with these sizes (its pointers are not looked at): 0

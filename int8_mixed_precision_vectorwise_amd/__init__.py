@@ -763,7 +763,9 @@ def fp4_cache_attention(q: torch.Tensor, cache: Fp4Cache, table: torch.Tensor, l
     (int32 [batch]) tokens.  ``softcap`` > 0 caps scores by a tanh; ``alibi`` (fp32
     [q_heads]) subtracts alibi * distance.  ``scale`` defaults to head_dim ** -0.5,
     ``max_len`` (a bound on the lengths) to the table's width.  A row that sees
-    nothing is zeros, its lse -inf.  ``workspace``: contiguous uint8, reused by the
+    nothing is zeros, its lse -inf; so are rows of q that are no sequence's queries
+    (before the first offset, past the last, past ``max_q``), but those of a given
+    ``out`` keep what they hold.  No gradient is recorded.  ``workspace``: contiguous uint8, reused by the
     caller (default: allocated here)."""
     dev = _device_of(q, cache.data, table, lengths, q_offsets, alibi, prefix, out, workspace)
     c = cache.struct()
@@ -785,12 +787,19 @@ def fp4_cache_attention(q: torch.Tensor, cache: Fp4Cache, table: torch.Tensor, l
         max_q = tokens if q_offsets is not None else tokens // max(batch, 1)
     if q_offsets is None and max_q * batch != tokens:
         raise ValueError("without q_offsets every sequence has max_q queries: tokens must be batch * max_q")
-    if out is None:
+    fill = out is None
+    if fill:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if batch == 0:                                  # no launch
+            out.zero_()
     ldo, hso = _heads(out, "out", cache.dtype, q_heads, c.head_dim)
     if out.shape[0] != tokens:
         raise ValueError("out has the wrong shape")
-    lse = q.new_empty((tokens, q_heads), dtype=torch.float32) if return_lse else None
+    lse = None
+    if return_lse:
+        lse = q.new_empty((tokens, q_heads), dtype=torch.float32)
+        if q_offsets is not None and not (fill and batch):
+            lse.fill_(float("-inf"))
     max_len = cols * cache.page_size if max_len is None else max_len
     _int32(max_q=max_q, max_len=max_len, window=window)
     _float32(softcap=softcap)
@@ -798,7 +807,7 @@ def fp4_cache_attention(q: torch.Tensor, cache: Fp4Cache, table: torch.Tensor, l
         q.data_ptr(), ldq, hsq, out.data_ptr(), ldo, hso, None if lse is None else lse.data_ptr(), table.data_ptr(), ldt,
         cols, lengths.data_ptr(), None if q_offsets is None else q_offsets.data_ptr(),
         None if alibi is None else alibi.data_ptr(), None if prefix is None else prefix.data_ptr(), tokens, batch,
-        q_heads, max(max_q, 1), max_len, window, c.head_dim ** -0.5 if scale is None else scale, softcap)
+        q_heads, max(max_q, 1), max_len, window, c.head_dim ** -0.5 if scale is None else scale, softcap, fill)
     if workspace is not None:
         _bytes(workspace, "workspace")
     else:

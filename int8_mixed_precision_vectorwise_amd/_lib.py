@@ -120,6 +120,7 @@ class Fp4AttentionStruct(Structure):
         ("window", c_int32),
         ("scale", c_float),
         ("softcap", c_float),
+        ("fill", c_int32),
     ]
 
 

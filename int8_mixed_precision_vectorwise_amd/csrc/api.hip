@@ -111,7 +111,7 @@ const char* i8mp_status_string(i8mp_status s) {
     }
 }
 
-int32_t i8mp_abi_version(void) { return (3 << 16) | 1; }
+int32_t i8mp_abi_version(void) { return (3 << 16) | 2; }
 
 size_t i8mp_quant_workspace_bytes(int64_t m, int64_t k) {
     if (m <= 0 || k < 1 || k > I8MP_MAX_K) return 0;
@@ -779,6 +779,7 @@ bool kv_call(const i8mp_fp4_cache* cache, const i8mp_fp4_attention* p, KvAttnArg
     a->scale = p->scale;
     a->softcap = p->softcap;
     a->max_len = p->max_len;
+    a->fill = p->fill && p->q_offsets;
     return true;
 }
 }  // namespace

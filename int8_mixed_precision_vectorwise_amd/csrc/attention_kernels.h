@@ -101,6 +101,29 @@ __device__ inline Seq sequence(const KvAttnArgs& a, int b) {
     return s;
 }
 
+// Rows of q that are no sequence's queries get zeros and lse = -inf where the call asks for
+// it (a.fill): those in front of the first offset and behind the last, shared out among
+// the row tiles of all sequences, and a sequence's queries past max_q among its own.
+__device__ inline void fill_rows(const KvAttnArgs& a, int64_t from, int64_t to, int64_t stripe, int64_t stripes, int h) {
+    const int lanes = a.c.blocks * 8;  // 8 dims each
+    for (int64_t r = from + stripe; r < to; r += stripes)
+        for (int i = threadIdx.x; i < a.group * lanes; i += blockDim.x) {
+            const int oh = h * a.group + i / lanes;
+            *reinterpret_cast<uint4*>(a.out + r * a.ldo + oh * a.hso + i % lanes * 8) = make_uint4(0, 0, 0, 0);
+            if (a.lse && i % lanes == 0) a.lse[r * a.q_heads + oh] = -INFINITY;
+        }
+}
+__device__ inline void fill_rest(const KvAttnArgs& a, const Seq& s, int b, int rt, int h) {
+    const auto row = [&](int i) {
+        const int64_t r = a.q_offsets[i];
+        return r < 0 ? 0 : (r > a.tokens ? a.tokens : r);
+    };
+    const int64_t stripe = (int64_t)b * a.row_tiles + rt, stripes = (int64_t)a.batch * a.row_tiles;
+    fill_rows(a, 0, row(0), stripe, stripes, h);
+    fill_rows(a, row(a.batch), a.tokens, stripe, stripes, h);
+    fill_rows(a, s.row0 + s.q_len, s.row0 + (s.length - s.past), rt, a.row_tiles, h);
+}
+
 // Key tiles that the queries [i0, i1] can see: tiles [0, head) for the prefix, then
 // [low, low + n - head): a run of n tiles, numbered 0 .. n - 1.
 struct Span {
@@ -580,6 +603,7 @@ __global__ __launch_bounds__(64 * W, simd_waves(NB, T)) void kv_attention_kernel
     const Seq s = sequence(a, b);
     const int rows = s.q_len * a.group;
     const int r0 = rt * kRows;
+    if (a.fill && chunk == 0) fill_rest(a, s, b, rt, h);
     if (r0 >= rows) return;
     const int r1 = r0 + kRows < rows ? r0 + kRows : rows;
     const int i0 = r0 / a.group, i1 = (r1 - 1) / a.group;

@@ -56,6 +56,7 @@ struct KvAttnArgs {
     int64_t tokens;                  // rows of q
     float scale, softcap;            // softcap 0: none
     int64_t max_len;                 // bound on the lengths
+    bool fill;                       // zeros for rows of q that are no sequence's queries
     // set by the launcher
     float to_s, to_y, to_e;          // factors of a product of q with E2M1 values and scales A: to its score, in units
                                      // of log2 e, to y = score / cap, and to 2 y in the same units

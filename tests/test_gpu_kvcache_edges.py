@@ -192,3 +192,38 @@ def test_values_past_32_bits_are_refused():
                 dict(softcap=1e-50)):
         with pytest.raises(ValueError):
             i8.fp4_cache_attention(q, c, table, lengths, **bad)
+
+
+@pytest.mark.parametrize("heads,group,d", [(2, 3, 64), (1, 8, 128), (3, 1, 256)])
+def test_rows_of_no_sequence(heads, group, d):
+    """Padding around the sequences' queries and queries past max_q: zeros and -inf, or what a given out holds."""
+    kind, page = "f16", 16
+    lens = [(3, 50), (0, 20), (9, 4000), (1, 1), (2, 0)]
+    c, table, lengths, seqs = build(lens, heads, group, d, page, kind, 45)
+    rows = np.concatenate([s[0] for s in seqs])
+    n, hq = len(rows) + 31, heads * group
+    q = np.concatenate([np.full((7, hq, d), np.nan), rows, np.full((24, hq, d), np.nan)])
+    offsets = dev(7 + np.concatenate([[0], np.cumsum([x for x, _ in lens])]), torch.int32)
+    say(f"fp4_cache_attention with rows of no sequence, {heads} x {group} heads of {d}")
+    dirty = [torch.full((n * hq * d,), 3.0, dtype=torch.float16, device="cuda") for _ in range(4)]
+    dirty += [torch.full((n * hq,), 3.0, device="cuda") for _ in range(4)]
+    del dirty                                   # what the call allocates is not zero
+    mark = torch.full((n, hq, d), 5.0, dtype=torch.float16, device="cuda")
+    for most, out in ((9, None), (2, None), (9, mark.clone()), (2, mark.clone())):
+        got, lse = i8.fp4_cache_attention(dev16(q, kind), c, table, lengths, offsets, most, out=out, return_lse=True)
+        torch.cuda.synchronize()
+        own = np.zeros(n, bool)
+        at = 7
+        for (count, length), (qs, k, v) in zip(lens, seqs):
+            for i in range(min(count, most)):
+                own[at + i] = True
+                end = length - count + i + 1
+                check(got[at + i:at + i + 1], lse[at + i:at + i + 1], [(qs[i:i + 1], k[:max(end, 0)], v[:max(end, 0)])],
+                      d ** -0.5, kind)
+            at += count
+        rest = torch.from_numpy(~own).cuda()
+        assert bool((got[rest] == (0.0 if out is None else 5.0)).all()) and bool(torch.isneginf(lse[rest]).all())
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    got, lse = i8.fp4_cache_attention(dev16(q, kind), c, table[:0], none, torch.zeros(1, dtype=torch.int32, device="cuda"), 1,
+                                      return_lse=True)
+    assert bool((got == 0).all()) and bool(torch.isneginf(lse).all())
