@@ -801,8 +801,10 @@ def fp4_cache_attention(q: torch.Tensor, cache: Fp4Cache, table: torch.Tensor, l
         if q_offsets is not None and not (fill and batch):
             lse.fill_(float("-inf"))
     max_len = cols * cache.page_size if max_len is None else max_len
-    _int32(max_q=max_q, max_len=max_len, window=window)
-    _float32(softcap=softcap)
+    if (max_q | max_len | window) >> 31:                # not all of them in 0 .. 2^31 - 1
+        _int32(max_q=max_q, max_len=max_len, window=window)
+    if softcap:
+        _float32(softcap=softcap)
     call = Fp4AttentionStruct(
         q.data_ptr(), ldq, hsq, out.data_ptr(), ldo, hso, None if lse is None else lse.data_ptr(), table.data_ptr(), ldt,
         cols, lengths.data_ptr(), None if q_offsets is None else q_offsets.data_ptr(),
