@@ -481,7 +481,8 @@ i8mp_status i8mp_fp4_cache_read(const i8mp_fp4_cache* cache /* host */, const in
  * infinity in a key's block, a NaN in q) gets NaN in both.  Sums, maxima and the softmax are fp32;
  * the weights e^s, times a block's A, are rounded to the 16-bit type for the product
  * with the E2M1 values (bfloat16: once; fp16: e^s is rounded, then its product, or, in
- * waves whose A's span more than 2^14, their fp32 product to 2^-18).
+ * waves whose A's span more than 2^14, their fp32 product to 2^-18); bfloat16 sums hold
+ * values of V up to about 2^100.
  * The rows of one sequence do not depend on the others' contents; how the keys are
  * cut, and so the order of the sums, follows from the call's sizes.
  *
@@ -515,8 +516,8 @@ typedef struct i8mp_fp4_attention {
     int32_t max_len;          /* bound on the lengths, <= table_cols * page_size     */
     int32_t window;           /* 0: none                                            */
     float scale;
-    float softcap;            /* 0: none.  Any positive value; a capped score is within
-                                 2^-17 or 2^-20 of its value of cap tanh(s / cap)    */
+    float softcap;            /* 0: none.  Any positive value: a capped score is off by up
+                                 to 2^-17 (caps up to 64) or 2^-20 of itself (above)  */
     int32_t fill;             /* 1: rows of q that are no sequence's queries are filled  */
 } i8mp_fp4_attention;
 

@@ -37,9 +37,9 @@ int64_t real_segments(const KvAttnArgs& a) {
 // Prompts of so many row tiles that single waves fill the chip 3/2 times (head_dim 128:
 // it holds 2048) take workgroups of one wave, which has its row tile's keys for itself: a
 // quarter of the prologues, no sums to join.  Waves of 4 / 1, us: 5504 row tiles of a
-// 4096-token prompt 386 / 349, 3520 of 8 prompts of 512 89 / 74, 2752 of a 2048-token
-// one 123 / 115, but 2736 behind 2048 tokens 272 / 276, with a distance bias 369 / 391,
-// and 1500 of ragged pieces 231 / 292.
+// 4096-token prompt 422 / 368, 3520 of 8 prompts of 512 97 / 82, 2752 of a 2048-token
+// one 138 / 127, but 2736 behind 2048 tokens 301 / 296, with a distance bias 378 / 411,
+// and 1500 of ragged pieces 239 / 282.
 // head_dim 64 (3 waves a SIMD): 5504 row tiles 223 / 244, so 4 there.
 void plan(KvAttnArgs& a) {
     const int64_t rows = (int64_t)a.max_q * a.group;

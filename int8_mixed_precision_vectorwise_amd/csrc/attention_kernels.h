@@ -362,7 +362,7 @@ typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 // A weight that is far above a row's others is rounded less often the closer the reference
 // is to it (an equal one is a power of two): with two roundings, in fp16, the output's
 // error is 1.5 times that of its own rounding at a slack of 2^7, 1.3 at 2^2 and 1.25 at
-// none, for a 4096-token prompt, at 0, 3 and 9 % of its time (349 us).
+// none, for a 4096-token prompt, at 0, 4 and 11 % of its time (355 us).
 // In fp16 weights are 2^9 times e^(s - reference), at most 2^11 so, and the scales A
 // that they meet are taken times 2^(4 - e), 2^e the first power above every finite A the
 // wave has met (a larger one than before rescales the sums).  Products are then below
@@ -555,11 +555,11 @@ __device__ inline __attribute__((always_inline)) bool meet(const uint32_t (&vs)[
 // and waves meet only at the end.
 //
 // What bounds it.  Few rows: HBM; 64 sequences of 8191 tokens, 64 / 8 heads of 128, are
-// read at 5.1 TB/s, one of 131072 tokens at 4.7; short contexts, a prologue and
+// read at 4.9 TB/s, one of 131072 tokens at 4.6; short contexts, a prologue and
 // epilogue of about 4 us.  Many rows: the VALU: converting 4-bit codes (shared by the row
 // tile), exponentials and the scaling of weights take about 380 instructions for 48 rows
 // of 32 keys beside 48 matrix instructions, which hold the SIMD for about 10 of their 16
-// cycles each.  A 4096-token prompt of 64 heads of 128: 760 TFLOP/s.
+// cycles each.  A 4096-token prompt of 64 heads of 128: 745 TFLOP/s.
 //
 // simd_waves(): those of a SIMD, by their registers (512 a lane for all of them).
 // T = 3 takes 248 registers with head_dim 128; with 256 two sets of rows already spill.
