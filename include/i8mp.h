@@ -482,7 +482,7 @@ i8mp_status i8mp_fp4_cache_read(const i8mp_fp4_cache* cache /* host */, const in
  * the weights e^s, times a block's A, are rounded to the 16-bit type for the product
  * with the E2M1 values (bfloat16: once; fp16: e^s is rounded, then its product, or, in
  * waves whose A's span more than 2^14, their fp32 product to 2^-18); bfloat16 sums hold
- * values of V up to about 2^100.
+ * values of V up to about 2^100.  Weights below 2^-126 of a row's largest count as 0.
  * The rows of one sequence do not depend on the others' contents; how the keys are
  * cut, and so the order of the sums, follows from the call's sizes.
  *

@@ -60,6 +60,7 @@ class Store:
     def compare(self, out, lse, picks, heads=None, **kw):
         """picks: (sequence, query) to compare; heads: kv heads (all of their query heads)."""
         heads = list(range(self.heads)) if heads is None else heads
+        scale = kw.pop("scale", self.d ** -0.5)
         hq = [h * self.group + g for h in heads for g in range(self.group)]
         kw["prefix"] = None if kw.get("prefix") is None else host(kw["prefix"])
         if kw.get("alibi") is not None:
@@ -74,7 +75,7 @@ class Store:
             end = max(end, 0)
             check(out[row:row + 1, hq], lse[row:row + 1, hq],
                   [(self.q[row:row + 1, hq], self.k[at:at + end, heads], self.v[at:at + end, heads])],
-                  self.d ** -0.5, self.kind, **more)
+                  scale, self.kind, **more)
 
 
 def test_a_prefix_longer_than_the_parts_allow_for():
@@ -209,3 +210,15 @@ def test_rows_are_the_same_alone_and_in_a_batch(kind):
         assert torch.equal(one[0], out[b]) and torch.equal(one_lse[0], lse[b])
     again, _ = s.run(max_len=800)
     assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_far_caps_beside_the_other_terms(kind):
+    s = Store([(1, 700), (5, 333), (38, 90)], 2, 2, 128, 16, kind, 9)
+    pre = dev(np.array([40, 0, 1000]), torch.int32)
+    for cap in (65.0, 400.0):
+        for scale in (0.3, -0.3):
+            for more in (dict(alibi=alibi_of(4)), dict(prefix=pre, window=20), dict(alibi=alibi_of(4), prefix=pre)):
+                kw = dict(more, softcap=cap, scale=scale)
+                say(f"fp4_cache_attention capped at {cap}, factor {scale}, {list(more)} {kind}")
+                s.compare(*s.run(**kw), picks=[(0, 0), (1, 4), (2, 37)], **kw)
