@@ -515,32 +515,38 @@ __device__ inline __attribute__((always_inline)) bool meet(const uint32_t (&vs)[
         }
     const us2 b = __builtin_bit_cast(us2, big), l = __builtin_bit_cast(us2, small);
     const int top_bits = b.x > b.y ? b.x : b.y, low_bits = l.x < l.y ? l.x : l.y;
-    if (__ballot((top_bits >= (sizes.large + 15) << 10) | (low_bits < sizes.low))) {
-        us2 finite = {0, 0};           // numbers moved up to 0x8400 and past it, the rest below
+    const bool above = top_bits >= (sizes.large + 15) << 10;
+    if (__ballot(above | (low_bits < sizes.low))) {
         us2 least = {0xffff, 0xffff};  // less 1: a 0 is the largest
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 2 * NB; ++i) {
-                finite = __builtin_elementwise_max(finite, __builtin_bit_cast(us2, vs[u][i]) + us2{0x8400, 0x8400});
-                least = __builtin_elementwise_min(least, __builtin_bit_cast(us2, vs[u][i]) - us2{1, 1});
-            }
-        const int top = finite.x > finite.y ? finite.x : finite.y, not_0 = least.x < least.y ? least.x : least.y;
-        const Sizes met = sizes.guess ? Sizes{kLeastLarge, 0x7c00} : sizes;
-        int large = (((int)column_max((float)top) - 0x8400) >> 10) - 14;
-        large = __builtin_amdgcn_readfirstlane(large > met.large ? large : met.large);
-        int low = (1 - (int)column_max((float)-not_0)) & 0x1fc00;
-        low = __builtin_amdgcn_readfirstlane(low < met.low ? low : met.low);
-        // subnormal numbers reach 2^10 below the first exponent
-        if (large + 15 - (low ? low >> 10 : -10) > kSpan + 1) return false;
-        const float drop = __builtin_amdgcn_exp2f((float)(sizes.large - large));
+            for (int i = 0; i < 2 * NB; ++i) least = __builtin_elementwise_min(least, __builtin_bit_cast(us2, vs[u][i]) - us2{1, 1});
+        const int not_0 = least.x < least.y ? least.x : least.y;
+        if (__ballot(above | (not_0 + 1 < sizes.low))) {  // and not only blocks of zeros
+            us2 finite = {0, 0};  // numbers moved up to 0x8400 and past it, the rest below
 #pragma unroll
-        for (int t = 0; t < T; ++t)
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int bb = 0; bb < NB; ++bb)
+                for (int i = 0; i < 2 * NB; ++i)
+                    finite = __builtin_elementwise_max(finite, __builtin_bit_cast(us2, vs[u][i]) + us2{0x8400, 0x8400});
+            const int top = finite.x > finite.y ? finite.x : finite.y;
+            const Sizes met = sizes.guess ? Sizes{kLeastLarge, 0x7c00} : sizes;
+            int large = (((int)column_max((float)top) - 0x8400) >> 10) - 14;
+            large = __builtin_amdgcn_readfirstlane(large > met.large ? large : met.large);
+            int low = (1 - (int)column_max((float)-not_0)) & 0x1fc00;
+            low = __builtin_amdgcn_readfirstlane(low < met.low ? low : met.low);
+            // subnormal numbers reach 2^10 below the first exponent
+            if (large + 15 - (low ? low >> 10 : -10) > kSpan + 1) return false;
+            const float drop = __builtin_amdgcn_exp2f((float)(sizes.large - large));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[t][bb][j] *= drop;
-        sizes = Sizes{large, low};
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int bb = 0; bb < NB; ++bb)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[t][bb][j] *= drop;
+            sizes = Sizes{large, low};
+        }
     }
     sizes.guess = false;
     return true;

@@ -227,3 +227,24 @@ def test_rows_of_no_sequence(heads, group, d):
     got, lse = i8.fp4_cache_attention(dev16(q, kind), c, table[:0], none, torch.zeros(1, dtype=torch.int32, device="cuda"), 1,
                                       return_lse=True)
     assert bool((got == 0).all()) and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("where", ["one_block", "first_tile", "some_keys", "all"])
+def test_blocks_of_zeros(where, kind):
+    """Values that are zero (a padded head, padding tokens), alone and among values of ordinary and of very different sizes."""
+    rng = np.random.default_rng(47)
+    heads, d, page, n = 2, 128, 16, 300
+    for queries, spread in ((1, 0), (40, 0), (40, 24)):
+        q, k = draw(rng, (queries, heads, d), kind, 0.3), draw(rng, (n, heads, d), kind, 0.3)
+        v = draw(rng, (n, heads, d), kind, 0.3)
+        if spread:
+            v = kv.round16(np.clip(v, -3, 3) * np.exp2(rng.choice([-spread / 2, spread / 2], (n, 1, 1))), kind)
+        v[{"one_block": np.s_[:, :, 64:], "first_tile": np.s_[:32], "some_keys": np.s_[::3], "all": np.s_[:]}[where]] = 0
+        c = make_cache(-(-n // page), heads, d, page, kind)
+        say(f"fp4_cache_attention with zeros in V, {where}, {queries} queries, spread {spread} {kind}")
+        i8.fp4_cache_write(c, dev16(k, kind), dev16(v, kind), torch.arange(n, device="cuda"))
+        out, lse = i8.fp4_cache_attention(dev16(q, kind), c, dev(np.arange(-(-n // page))[None], torch.int32),
+                                          dev(np.array([n]), torch.int32), max_q=queries, return_lse=True)
+        torch.cuda.synchronize()
+        check(out, lse, [(q, kv.dequantize(*kv.quantize(k)), kv.dequantize(*kv.quantize(v)))], d ** -0.5, kind)
