@@ -185,7 +185,7 @@ i8mp_status i8mp_int8_mm_dequant(const int32_t* c, int64_t ldc, const float* row
  */
 #define I8MP_DTYPE_F16 0
 #define I8MP_DTYPE_F32 1
-#define I8MP_DTYPE_BF16 2 /* the 4-bit key/value cache only */
+#define I8MP_DTYPE_BF16 2 /* the 4-bit key/value cache and the microscaled matrices only */
 i8mp_status i8mp_int8_vectorwise_dequant(const int8_t* q, int64_t ldq, int64_t m, int64_t k,
                                          const float* absmax, int32_t out_dtype, void* out, int64_t ldout,
                                          hipStream_t stream);
@@ -528,6 +528,103 @@ size_t i8mp_fp4_attention_workspace_bytes(const i8mp_fp4_cache* cache /* host */
 
 i8mp_status i8mp_fp4_cache_attention(const i8mp_fp4_cache* cache /* host */, const i8mp_fp4_attention* call /* host */,
                                      void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* A write of new tokens whose keys are rotated by position on the way, and the
+ * rotation of their queries: what an attention layer does between its projection
+ * and i8mp_fp4_cache_attention.  The first `rotary` dims of a head turn in pairs,
+ * pair i of a token at position p by row p of the tables:
+ *   (a, b) -> (a cos[p, i] - b sin[p, i], b cos[p, i] + a sin[p, i])
+ * with (a, b) the dims (i, i + rotary / 2), or (2 i, 2 i + 1) if interleaved; each
+ * result is rounded to fp32 from the exact value (formed in 64 bits), then to the
+ * cache's type.  The keys so rounded and the values are written as
+ * i8mp_fp4_cache_write does; a token whose slot is outside the cache is not written,
+ * its queries are turned all the same.  Positions are taken into [0, table_rows). */
+typedef struct i8mp_fp4_append {
+    const void* k; int64_t ldk, hsk;   /* as for i8mp_fp4_cache_write                     */
+    const void* v; int64_t ldv, hsv;
+    const int64_t* slots;              /* [tokens], distinct                              */
+    const int64_t* positions;          /* [tokens]                                        */
+    const float* cos;                  /* [table_rows x rotary / 2], ldcos elements a row */
+    const float* sin;                  /* the same, ldsin                                 */
+    int64_t ldcos, ldsin, table_rows;  /* table_rows >= 1                                 */
+    const void* q; int64_t ldq, hsq;   /* [tokens x q_heads x head_dim]: strides that are */
+    void* out; int64_t ldo, hso;       /* multiples of 8, 16-byte aligned.  out is q
+                                          itself with q's strides, or shares no element
+                                          with q, k and v                                 */
+    int64_t tokens;
+    int32_t q_heads;                   /* 0: no queries (q and out are not looked at)     */
+    int32_t rotary;                    /* a multiple of 16, 16 .. head_dim                */
+    int32_t interleaved;
+} i8mp_fp4_append;
+
+i8mp_status i8mp_fp4_cache_append(const i8mp_fp4_cache* cache /* host */, const i8mp_fp4_append* call /* host */,
+                                  hipStream_t stream);
+
+/* ------------------------------------------------------------------------- */
+/* Microscaled 4-bit matrices: E2M1 elements in blocks of 32 along a row, each
+ * under a power of two (the OCP microscaling format MXFP4: element format E2M1,
+ * scale format E8M0), 4.25 bits an element.  The matrix cores of gfx950 multiply
+ * them directly.  For a block of x:
+ *   E    = max(floor(log2 max |x|) - 2, -127), held as the byte E + 127;
+ *   code = sign bit of x | the E2M1 magnitude nearest to |x| / 2^E, ties to the even
+ *          mantissa bit, at most 6 (magnitudes of 7 and more times 2^E become 6 too);
+ *   x'   = E2M1 value * 2^E.
+ * A block of zeros has the byte 0.  A block that holds a NaN or an infinity has the
+ * byte 255, codes of 0, and stands for NaNs.  Every code is decided exactly.
+ *
+ * A [rows x k] matrix is held by rows, padded with zeros to kp = k rounded up to
+ * 128: codes [rows x ldc bytes], two a byte, element 2 j in the low nibble of byte j,
+ * and scales [rows x lds bytes].  i8mp_mx4_quantize writes the padding; who fills a
+ * matrix by other means writes codes of 0 and any scale but 255 there. */
+typedef struct i8mp_mx4 {
+    uint8_t* codes;   /* device, 16-byte aligned                          */
+    uint8_t* scales;  /* device, 4-byte aligned                           */
+    int64_t rows;     /* >= 0, < 2^31                                     */
+    int64_t k;        /* >= 0                                             */
+    int64_t ldc;      /* bytes: >= kp / 2, a multiple of 16, <= I8MP_MAX_LD */
+    int64_t lds;      /* bytes: >= kp / 32, a multiple of 4, <= I8MP_MAX_LD */
+} i8mp_mx4;
+
+/* x [m x k] (I8MP_DTYPE_F16 or _BF16, ldx >= k, any alignment) quantized by rows into
+ * out [m x k], or with `columns` its transpose into out [k x m] (blocks of 32 rows of
+ * x's columns).  Bytes of out past each row's kp are left as they are. */
+i8mp_status i8mp_mx4_quantize(const void* x, int32_t dtype, int64_t m, int64_t k, int64_t ldx, int32_t columns,
+                              const i8mp_mx4* out /* host */, hipStream_t stream);
+
+/* out [a->rows x a->k], ldout >= a->k: x' rounded once to out_dtype (any of the three). */
+i8mp_status i8mp_mx4_dequantize(const i8mp_mx4* a /* host */, int32_t out_dtype, void* out, int64_t ldout,
+                                hipStream_t stream);
+
+/* out [m x n] = a . b^T + bias for a [m x k], b [n x k]: products of x' exact, sums in
+ * fp32, one rounding to out_dtype (any of the three).  bias: optional [n] of out_dtype.
+ * ldout >= n, <= I8MP_MAX_LD.  k = 0 gives the bias, or zeros.  workspace: at least the
+ * query's bytes for these sizes, 16-byte aligned (NULL if that is 0). */
+size_t i8mp_mx4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
+i8mp_status i8mp_mx4_matmul(const i8mp_mx4* a /* host */, const i8mp_mx4* b /* host */, const void* bias,
+                            int32_t out_dtype, void* out, int64_t ldout, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+
+/* The linear with 4-bit weights and activations: out [m x n] = mx4(x) . w^T + bias, x
+ * [m x k] quantized by rows on the way; x, bias and out of one 16-bit type.  The same
+ * numbers, up to the order of the sums, as i8mp_mx4_quantize and i8mp_mx4_matmul. */
+size_t i8mp_mx4_linear_workspace_bytes(int64_t m, int64_t n, int64_t k);
+i8mp_status i8mp_mx4_linear(const void* x, int32_t dtype, int64_t m, int64_t ldx, const i8mp_mx4* w /* host */,
+                            const void* bias, void* out, int64_t ldout, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+
+/* Both gradients of out = x . w^T for grad_out [m x n], every operand quantized along
+ * its contraction:
+ *   grad_x [m x k] = mx4(grad_out) . mx4(w, by columns)^T         (over n)
+ *   grad_w [n x k] = mx4(grad_out, by columns) . mx4(x, by columns)^T  (over m)
+ * grad_out, x [m x k], w [n x k] (the 16-bit weight kept for training) and the
+ * gradients are of one 16-bit type.  A gradient whose pointer is NULL is not computed
+ * (grad_x does not read x, grad_w does not read w).  The bias gradient is the column
+ * sum of grad_out and is not part of this call.  m and n at most 2 I8MP_MAX_LD. */
+size_t i8mp_mx4_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k);
+i8mp_status i8mp_mx4_linear_backward(const void* grad_out, int64_t ldg, const void* x, int64_t ldx, const void* w,
+                                     int64_t ldw, int32_t dtype, int64_t m, int64_t n, int64_t k, void* grad_x,
+                                     int64_t ldgx, void* grad_w, int64_t ldgw, void* workspace, size_t workspace_bytes,
+                                     hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -19,12 +19,14 @@ import torch
 from ._lib import (  # noqa: F401
     EXPORTS,
     BackwardWorkspaceLayout,
+    Fp4AppendStruct,
     Fp4AttentionStruct,
     Fp4CacheStruct,
     I8MP_MAX_K,
     I8MP_NOALLOC_SCRATCH_BYTES,
     I8mpError,
     LinearWorkspaceLayout,
+    Mx4Struct,
     check,
     lib,
     status_string,
@@ -57,6 +59,13 @@ __all__ = [
     "fp4_cache_write",
     "fp4_cache_read",
     "fp4_cache_attention",
+    "fp4_cache_append",
+    "Mx4Tensor",
+    "mx4_quantize",
+    "mx4_dequantize",
+    "mx4_matmul",
+    "mx4_linear",
+    "mx4_linear_backward",
     "I8mpError",
 ]
 
@@ -818,3 +827,230 @@ def fp4_cache_attention(q: torch.Tensor, cache: Fp4Cache, table: torch.Tensor, l
     _run(dev, "i8mp_fp4_cache_attention", ctypes.byref(c), ctypes.byref(call),
          None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
     return out if lse is None else (out, lse)
+
+
+def _turning(t: torch.Tensor, name: str) -> int:
+    """Leading dimension of an angle table [rows, rotary / 2], fp32."""
+    ld = _rowmajor(t, name, torch.float32)
+    if t.shape[0] == 0:
+        raise ValueError(f"{name} has no rows")
+    return ld
+
+
+def fp4_cache_append(cache: Fp4Cache, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                     positions: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor, interleaved: bool = False,
+                     out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Rotates q [tokens, q_heads, head_dim] and k by position, writes k and v [tokens, kv_heads,
+    head_dim] into the cache's slots, and returns the rotated q (None for q None).
+
+    Row positions[t] (int64 [tokens]) of ``cos`` and ``sin`` (fp32 [rows, rotary / 2]) turns token t:
+    dims (i, i + rotary / 2) of a head, or (2 i, 2 i + 1) if ``interleaved``, for the first ``rotary`` dims (a
+    multiple of 16).  A position is taken into the tables' rows; a slot (int64 [tokens], distinct) outside
+    the cache (-1) is skipped.  ``out`` may be q itself; other tensors must not share elements with it.  No
+    gradient is recorded."""
+    dev = _device_of(cache.data, q, k, v, slots, positions, cos, sin, out)
+    c = cache.struct()
+    ldk, hsk = _heads(k, "k", cache.dtype, c.kv_heads, c.head_dim)
+    ldv, hsv = _heads(v, "v", cache.dtype, c.kv_heads, c.head_dim)
+    n = k.shape[0]
+    if v.shape[0] != n:
+        raise ValueError("k and v differ in tokens")
+    _vec(slots, "slots", torch.int64, n)
+    _vec(positions, "positions", torch.int64, n)
+    ldcos, ldsin = _turning(cos, "cos"), _turning(sin, "sin")
+    if cos.shape != sin.shape:
+        raise ValueError("cos and sin differ in shape")
+    ldq = hsq = ldo = hso = heads = 0
+    if q is not None:
+        ldq, hsq = _heads(q, "q", cache.dtype, None, c.head_dim)
+        if q.shape[0] != n:
+            raise ValueError("q and k differ in tokens")
+        heads = q.shape[1]
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ldo, hso = _heads(out, "out", cache.dtype, heads, c.head_dim)
+        if out.shape[0] != n:
+            raise ValueError("out has the wrong shape")
+    elif out is not None:
+        raise ValueError("out without q")
+    call = Fp4AppendStruct(k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv, slots.data_ptr(), positions.data_ptr(),
+                           cos.data_ptr(), sin.data_ptr(), ldcos, ldsin, cos.shape[0],
+                           q.data_ptr() if heads else None, ldq, hsq, out.data_ptr() if heads else None, ldo, hso, n, heads,
+                           2 * cos.shape[1], bool(interleaved))
+    _run(dev, "i8mp_fp4_cache_append", ctypes.byref(c), ctypes.byref(call))
+    return out
+
+
+@dataclass
+class Mx4Tensor:
+    """A microscaled 4-bit matrix [rows, k] in the layout of include/i8mp.h: packed E2M1 ``codes`` uint8
+    [rows, kp / 2] and E8M0 ``scales`` uint8 [rows, kp / 32], kp = k rounded up to 128 (``create`` allocates them)."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+    k: int
+
+    @classmethod
+    def create(cls, rows: int, k: int, device="cuda") -> "Mx4Tensor":
+        kp = (k + 127) // 128 * 128
+        return cls(torch.empty((rows, kp // 2), dtype=torch.uint8, device=device),
+                   torch.empty((rows, kp // 32), dtype=torch.uint8, device=device), k)
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def shape(self) -> Tuple[int, int]:
+        return self.codes.shape[0], self.k
+
+    def struct(self) -> Mx4Struct:
+        """The C form, after checking that the fields go together (the library checks ranges and alignment)."""
+        codes, scales, kp = self.codes, self.scales, (self.k + 127) // 128 * 128
+        ldc, lds = _rowmajor(codes, "codes", torch.uint8), _rowmajor(scales, "scales", torch.uint8)
+        rows = codes.shape[0]
+        if scales.shape[0] != rows or codes.shape[1] < kp // 2 or scales.shape[1] < kp // 32:
+            raise ValueError(f"codes and scales must hold [{rows}, {kp // 2}] and [{rows}, {kp // 32}] bytes for k = {self.k}")
+        # the stride of a single row, or of empty ones, is never taken
+        return Mx4Struct(codes.data_ptr(), scales.data_ptr(), rows, self.k, ldc if rows > 1 and kp else kp // 2,
+                         lds if rows > 1 and kp else kp // 32)
+
+
+def _half(t: torch.Tensor, name: str) -> int:
+    """The code of a 16-bit type."""
+    code = _CACHE_CODE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    return code
+
+
+def _space(need: int, workspace: Optional[torch.Tensor], dev: torch.device) -> Optional[torch.Tensor]:
+    """A call's workspace: the caller's, or one of ``need`` bytes (none for 0)."""
+    if workspace is not None:
+        _bytes(workspace, "workspace")
+        return workspace
+    return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+
+
+def _run_of(ws: Optional[torch.Tensor]) -> Tuple[Optional[int], int]:
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+
+
+def mx4_quantize(x: torch.Tensor, columns: bool = False, out: Optional[Mx4Tensor] = None) -> Mx4Tensor:
+    """Microscaled 4-bit form of a 16-bit matrix x [m, k]: blocks of 32 along its rows, or with ``columns`` along
+    its columns, which gives the transpose [k, m]."""
+    dev = _device_of(x, None if out is None else out.codes, None if out is None else out.scales)
+    ldx = _rowmajor(x, "x", x.dtype)
+    code = _half(x, "x")
+    m, k = x.shape
+    shape = (k, m) if columns else (m, k)
+    if out is None:
+        out = Mx4Tensor.create(*shape, device=dev)
+    elif out.shape != shape:
+        raise ValueError("out has the wrong shape")
+    _run(dev, "i8mp_mx4_quantize", x.data_ptr(), code, m, k, ldx, bool(columns), ctypes.byref(out.struct()))
+    return out
+
+
+def mx4_dequantize(t: Mx4Tensor, dtype: torch.dtype = torch.float16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """E2M1 value * 2^(scale - 127) [rows, k], as fp16, bfloat16 or fp32."""
+    if dtype not in _DTYPE_CODE:
+        raise ValueError("dtype must be torch.float16, torch.bfloat16 or torch.float32")
+    dev = _device_of(t.codes, t.scales, out)
+    if out is None:
+        out = torch.empty(t.shape, dtype=dtype, device=dev)
+    ldout = _rowmajor(out, "out", dtype)
+    if tuple(out.shape) != t.shape:
+        raise ValueError("out has the wrong shape")
+    _run(dev, "i8mp_mx4_dequantize", ctypes.byref(t.struct()), _DTYPE_CODE[dtype], out.data_ptr(), ldout)
+    return out
+
+
+def mx4_matmul(a: Mx4Tensor, b: Mx4Tensor, bias: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float16,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """a . b^T + bias of two microscaled matrices: out [a.rows, b.rows] in ``dtype`` (fp16, bfloat16 or fp32, the
+    bias too), sums in fp32.  ``workspace``: contiguous uint8, reused by the caller (default: allocated here)."""
+    if dtype not in _DTYPE_CODE:
+        raise ValueError("dtype must be torch.float16, torch.bfloat16 or torch.float32")
+    dev = _device_of(a.codes, a.scales, b.codes, b.scales, bias, out, workspace)
+    m, n, k = a.rows, b.rows, a.k
+    if b.k != k:
+        raise ValueError("a and b differ in k")
+    if bias is not None:
+        _vec(bias, "bias", dtype, n)
+    if out is None:
+        out = torch.empty((m, n), dtype=dtype, device=dev)
+    ldout = _rowmajor(out, "out", dtype)
+    if tuple(out.shape) != (m, n):
+        raise ValueError("out has the wrong shape")
+    ws = _space(lib().i8mp_mx4_matmul_workspace_bytes(m, n, k), workspace, dev)
+    _run(dev, "i8mp_mx4_matmul", ctypes.byref(a.struct()), ctypes.byref(b.struct()),
+         None if bias is None else bias.data_ptr(), _DTYPE_CODE[dtype], out.data_ptr(), ldout, *_run_of(ws))
+    return out
+
+
+def mx4_linear(x: torch.Tensor, w: Mx4Tensor, bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The linear with 4-bit weights and activations: mx4(x) . w^T + bias for x [m, k] of a 16-bit type, which out
+    [m, n] and the bias share.  No gradient is recorded: ``mx4_linear_backward`` computes both."""
+    dev = _device_of(x, w.codes, w.scales, bias, out, workspace)
+    ldx = _rowmajor(x, "x", x.dtype)
+    code = _half(x, "x")
+    m, k = x.shape
+    n = w.rows
+    if w.k != k:
+        raise ValueError("x and w differ in k")
+    if bias is not None:
+        _vec(bias, "bias", x.dtype, n)
+    if out is None:
+        out = x.new_empty((m, n))
+    ldout = _rowmajor(out, "out", x.dtype)
+    if tuple(out.shape) != (m, n):
+        raise ValueError("out has the wrong shape")
+    ws = _space(lib().i8mp_mx4_linear_workspace_bytes(m, n, k), workspace, dev)
+    _run(dev, "i8mp_mx4_linear", x.data_ptr(), code, m, ldx, ctypes.byref(w.struct()),
+         None if bias is None else bias.data_ptr(), out.data_ptr(), ldout, *_run_of(ws))
+    return out
+
+
+def mx4_linear_backward(grad_out: torch.Tensor, x: Optional[torch.Tensor], w: Optional[torch.Tensor],
+                        need_grad_x: bool = True, need_grad_w: bool = True, workspace: Optional[torch.Tensor] = None,
+                        out_x: Optional[torch.Tensor] = None, out_w: Optional[torch.Tensor] = None,
+                        ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Both gradients of x [m, k] . w^T for dL/dout = grad_out [m, n], w [n, k] the 16-bit weight kept for training:
+    (grad_x [m, k], grad_w [n, k]), products of operands quantized along what they sum over.  grad_x needs w, grad_w
+    needs x; all tensors share one 16-bit type."""
+    need_x, need_w = bool(need_grad_x), bool(need_grad_w)
+    dev = _device_of(grad_out, x, w, workspace, out_x, out_w)
+    dtype = grad_out.dtype
+    ldg = _rowmajor(grad_out, "grad_out", dtype)
+    code = _half(grad_out, "grad_out")
+    m, n = grad_out.shape
+    if (need_x and w is None) or (need_w and x is None):
+        raise ValueError("grad_x needs w, grad_w needs x")
+    if not (need_x or need_w):
+        return None, None
+    ldx = ldw = 0
+    if need_x:
+        ldw = _rowmajor(w, "w", dtype)
+    if need_w:
+        ldx = _rowmajor(x, "x", dtype)
+    k = w.shape[1] if need_x else x.shape[1]
+    if (need_x and tuple(w.shape) != (n, k)) or (need_w and tuple(x.shape) != (m, k)):
+        raise ValueError("grad_out, x and w must be [m, n], [m, k] and [n, k]")
+    ldgx = ldgw = 0
+    if need_x:
+        out_x = grad_out.new_empty((m, k)) if out_x is None else out_x
+        ldgx = _rowmajor(out_x, "out_x", dtype)
+        if tuple(out_x.shape) != (m, k):
+            raise ValueError("out_x has the wrong shape")
+    if need_w:
+        out_w = grad_out.new_empty((n, k)) if out_w is None else out_w
+        ldgw = _rowmajor(out_w, "out_w", dtype)
+        if tuple(out_w.shape) != (n, k):
+            raise ValueError("out_w has the wrong shape")
+    ws = _space(lib().i8mp_mx4_linear_backward_workspace_bytes(m, n, k), workspace, dev)
+    _run(dev, "i8mp_mx4_linear_backward", grad_out.data_ptr(), ldg, x.data_ptr() if need_w else None, ldx,
+         w.data_ptr() if need_x else None, ldw, code, m, n, k, out_x.data_ptr() if need_x else None, ldgx,
+         out_w.data_ptr() if need_w else None, ldgw, *_run_of(ws))
+    return out_x if need_x else None, out_w if need_w else None

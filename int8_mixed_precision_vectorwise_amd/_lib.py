@@ -47,6 +47,15 @@ EXPORTS = (
     "i8mp_fp4_cache_read",
     "i8mp_fp4_attention_workspace_bytes",
     "i8mp_fp4_cache_attention",
+    "i8mp_fp4_cache_append",
+    "i8mp_mx4_quantize",
+    "i8mp_mx4_dequantize",
+    "i8mp_mx4_matmul_workspace_bytes",
+    "i8mp_mx4_matmul",
+    "i8mp_mx4_linear_workspace_bytes",
+    "i8mp_mx4_linear",
+    "i8mp_mx4_linear_backward_workspace_bytes",
+    "i8mp_mx4_linear_backward",
 )
 
 
@@ -121,6 +130,45 @@ class Fp4AttentionStruct(Structure):
         ("scale", c_float),
         ("softcap", c_float),
         ("fill", c_int32),
+    ]
+
+
+class Fp4AppendStruct(Structure):
+    _fields_ = [
+        ("k", c_void_p),
+        ("ldk", c_int64),
+        ("hsk", c_int64),
+        ("v", c_void_p),
+        ("ldv", c_int64),
+        ("hsv", c_int64),
+        ("slots", c_void_p),
+        ("positions", c_void_p),
+        ("cos", c_void_p),
+        ("sin", c_void_p),
+        ("ldcos", c_int64),
+        ("ldsin", c_int64),
+        ("table_rows", c_int64),
+        ("q", c_void_p),
+        ("ldq", c_int64),
+        ("hsq", c_int64),
+        ("out", c_void_p),
+        ("ldo", c_int64),
+        ("hso", c_int64),
+        ("tokens", c_int64),
+        ("q_heads", c_int32),
+        ("rotary", c_int32),
+        ("interleaved", c_int32),
+    ]
+
+
+class Mx4Struct(Structure):
+    _fields_ = [
+        ("codes", c_void_p),
+        ("scales", c_void_p),
+        ("rows", c_int64),
+        ("k", c_int64),
+        ("ldc", c_int64),
+        ("lds", c_int64),
     ]
 
 
@@ -208,6 +256,26 @@ def _declare(lib):
     lib.i8mp_fp4_attention_workspace_bytes.restype = c_size_t
     lib.i8mp_fp4_cache_attention.argtypes = [cache, POINTER(Fp4AttentionStruct), c_void_p, c_size_t, c_void_p]
     lib.i8mp_fp4_cache_attention.restype = c_int32
+    lib.i8mp_fp4_cache_append.argtypes = [cache, POINTER(Fp4AppendStruct), c_void_p]
+    lib.i8mp_fp4_cache_append.restype = c_int32
+    mx4 = POINTER(Mx4Struct)
+    lib.i8mp_mx4_quantize.argtypes = [c_void_p, c_int32, c_int64, c_int64, c_int64, c_int32, mx4, c_void_p]
+    lib.i8mp_mx4_quantize.restype = c_int32
+    lib.i8mp_mx4_dequantize.argtypes = [mx4, c_int32, c_void_p, c_int64, c_void_p]
+    lib.i8mp_mx4_dequantize.restype = c_int32
+    for query in (lib.i8mp_mx4_matmul_workspace_bytes, lib.i8mp_mx4_linear_workspace_bytes,
+                  lib.i8mp_mx4_linear_backward_workspace_bytes):
+        query.argtypes = [c_int64, c_int64, c_int64]
+        query.restype = c_size_t
+    lib.i8mp_mx4_matmul.argtypes = [mx4, mx4, c_void_p, c_int32, c_void_p, c_int64, c_void_p, c_size_t, c_void_p]
+    lib.i8mp_mx4_matmul.restype = c_int32
+    lib.i8mp_mx4_linear.argtypes = [c_void_p, c_int32, c_int64, c_int64, mx4, c_void_p, c_void_p, c_int64, c_void_p,
+                                    c_size_t, c_void_p]
+    lib.i8mp_mx4_linear.restype = c_int32
+    lib.i8mp_mx4_linear_backward.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int32, c_int64,
+                                             c_int64, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_size_t,
+                                             c_void_p]
+    lib.i8mp_mx4_linear_backward.restype = c_int32
 
 
 def lib():

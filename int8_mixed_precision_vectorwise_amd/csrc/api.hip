@@ -10,6 +10,7 @@
 #include "backward.h"
 #include "fp4.h"
 #include "kvcache.h"
+#include "mx4.h"
 
 using namespace i8mp;
 
@@ -111,7 +112,7 @@ const char* i8mp_status_string(i8mp_status s) {
     }
 }
 
-int32_t i8mp_abi_version(void) { return (3 << 16) | 2; }
+int32_t i8mp_abi_version(void) { return (3 << 16) | 3; }
 
 size_t i8mp_quant_workspace_bytes(int64_t m, int64_t k) {
     if (m <= 0 || k < 1 || k > I8MP_MAX_K) return 0;
@@ -849,6 +850,211 @@ i8mp_status i8mp_fp4_cache_attention(const i8mp_fp4_cache* cache, const i8mp_fp4
     if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return I8MP_EWORKSPACE;
     if (i8mp_status s = check_device(); s != I8MP_OK) return s;
     return launched(launch_kv_attention(a, workspace, stream));
+}
+
+i8mp_status i8mp_fp4_cache_append(const i8mp_fp4_cache* cache, const i8mp_fp4_append* p, hipStream_t stream) {
+    KvAppendArgs a{};
+    KvMoveArgs& m = a.m;
+    if (!kv_cache(cache, &m.c) || !p || p->tokens < 0) return I8MP_EINVAL;
+    if (!kv_strides(p->ldk, p->hsk, cache, 8) || !kv_strides(p->ldv, p->hsv, cache, 8)) return I8MP_EINVAL;
+    if (p->rotary < 16 || p->rotary % 16 || p->rotary > cache->head_dim) return I8MP_EINVAL;
+    if (p->table_rows < 1 || p->ldcos < p->rotary / 2 || p->ldsin < p->rotary / 2) return I8MP_EINVAL;
+    if (p->q_heads < 0 || p->q_heads > 65535) return I8MP_EINVAL;
+    if (p->q_heads > 0 && (!kv_strides(p->ldq, p->hsq, cache, 8) || !kv_strides(p->ldo, p->hso, cache, 8))) return I8MP_EINVAL;
+    if (p->tokens == 0) return I8MP_OK;
+    if (!m.c.data || !p->k || !p->v || !p->slots || !p->positions || !p->cos || !p->sin) return I8MP_EINVAL;
+    if (!aligned16(m.c.data) || !aligned16(p->k) || !aligned16(p->v)) return I8MP_EINVAL;
+    if (p->q_heads > 0 && (!p->q || !p->out || !aligned16(p->q) || !aligned16(p->out))) return I8MP_EINVAL;
+    if (i8mp_status s = check_device(); s != I8MP_OK) return s;
+    m.slots = p->slots;
+    m.tokens = p->tokens;
+    m.k = const_cast<void*>(p->k);
+    m.ldk = p->ldk;
+    m.hsk = p->hsk;
+    m.v = const_cast<void*>(p->v);
+    m.ldv = p->ldv;
+    m.hsv = p->hsv;
+    if (p->q_heads > 0) {
+        a.q = static_cast<const half_bits*>(p->q);
+        a.ldq = p->ldq;
+        a.hsq = p->hsq;
+        a.out = static_cast<half_bits*>(p->out);
+        a.ldo = p->ldo;
+        a.hso = p->hso;
+        a.q_heads = p->q_heads;
+    }
+    a.positions = p->positions;
+    a.cos = p->cos;
+    a.sin = p->sin;
+    a.ldcos = p->ldcos;
+    a.ldsin = p->ldsin;
+    a.table_rows = p->table_rows;
+    a.rotary = p->rotary;
+    a.interleaved = p->interleaved != 0;
+    return launched(launch_kv_append(a, stream));
+}
+
+namespace {
+// the internal form of a quantized matrix, if its sizes are in range; `filled` also looks at the pointers
+bool mx4(const i8mp_mx4* p, Mx4* q) {
+    if (!p || p->rows < 0 || p->rows > INT32_MAX || p->k < 0 || p->ldc > I8MP_MAX_LD || p->lds > I8MP_MAX_LD) return false;
+    *q = Mx4{p->codes, p->ldc, p->scales, p->lds, p->rows, p->k};
+    return p->ldc % 16 == 0 && p->lds % 4 == 0 && p->ldc >= q->kp() / 2 && p->lds >= q->kp() / kMxBlock;
+}
+bool mx4_data(const Mx4& q) {
+    if (q.rows == 0 || q.k == 0) return true;
+    return q.codes && q.scales && aligned16(q.codes) && (reinterpret_cast<uintptr_t>(q.scales) & 3) == 0;
+}
+// a matrix in a workspace: its codes, then its scales, at `at`, which moves past them
+Mx4 mx4_at(char* base, size_t* at, int64_t rows, int64_t k) {
+    Mx4 q{nullptr, 0, nullptr, 0, rows, k};
+    q.ldc = q.kp() / 2;
+    q.lds = q.kp() / kMxBlock;
+    const size_t codes = align_up((size_t)rows * q.ldc);
+    if (base) {
+        q.codes = reinterpret_cast<uint8_t*>(base + *at);
+        q.scales = reinterpret_cast<uint8_t*>(base + *at + codes);
+    }
+    *at += codes + align_up((size_t)rows * q.lds);
+    return q;
+}
+bool mx4_sizes(int64_t m, int64_t n, int64_t k) {
+    const auto ok = [](int64_t v) { return v >= 0 && v <= INT32_MAX; };
+    return ok(m) && ok(n) && ok(k);
+}
+bool mx4_fits(int64_t k) { return Mx4{nullptr, 0, nullptr, 0, 0, k}.kp() / 2 <= I8MP_MAX_LD; }  // as a row's length
+
+MxQuantArgs mx4_quant(const void* x, int64_t ldx, int32_t dtype, bool columns, const Mx4& q) {
+    return MxQuantArgs{static_cast<const half_bits*>(x), ldx, dtype == I8MP_DTYPE_BF16, columns, q};
+}
+bool any_type(int32_t dtype) { return half_type(dtype) || dtype == I8MP_DTYPE_F32; }
+}  // namespace
+
+i8mp_status i8mp_mx4_quantize(const void* x, int32_t dtype, int64_t m, int64_t k, int64_t ldx, int32_t columns,
+                              const i8mp_mx4* out, hipStream_t stream) {
+    Mx4 q{};
+    if (!mx4(out, &q) || !half_type(dtype) || m < 0 || k < 0 || ldx < k) return I8MP_EINVAL;
+    if (q.rows != (columns ? k : m) || q.k != (columns ? m : k)) return I8MP_EINVAL;
+    if (m == 0 || k == 0) return I8MP_OK;
+    if (!x || !mx4_data(q)) return I8MP_EINVAL;
+    if (i8mp_status s = check_device(); s != I8MP_OK) return s;
+    return launched(launch_mx4_quantize(mx4_quant(x, ldx, dtype, columns != 0, q), stream));
+}
+
+i8mp_status i8mp_mx4_dequantize(const i8mp_mx4* a, int32_t out_dtype, void* out, int64_t ldout, hipStream_t stream) {
+    Mx4 q{};
+    if (!mx4(a, &q) || !any_type(out_dtype) || ldout < q.k) return I8MP_EINVAL;
+    if (q.rows == 0 || q.k == 0) return I8MP_OK;
+    if (!out || !mx4_data(q)) return I8MP_EINVAL;
+    if (i8mp_status s = check_device(); s != I8MP_OK) return s;
+    return launched(launch_mx4_dequantize(MxDequantArgs{q, out_dtype, out, ldout}, stream));
+}
+
+size_t i8mp_mx4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+    return mx4_sizes(m, n, k) ? mx4_gemm_workspace(m, n, k) : 0;
+}
+
+i8mp_status i8mp_mx4_matmul(const i8mp_mx4* a, const i8mp_mx4* b, const void* bias, int32_t out_dtype, void* out,
+                            int64_t ldout, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    MxGemmArgs g{};
+    if (!mx4(a, &g.a) || !mx4(b, &g.b) || g.a.k != g.b.k || !any_type(out_dtype)) return I8MP_EINVAL;
+    if (ldout < g.b.rows || bad_ld(ldout)) return I8MP_EINVAL;
+    if (g.a.rows == 0 || g.b.rows == 0) return I8MP_OK;
+    if (!out || !mx4_data(g.a) || !mx4_data(g.b)) return I8MP_EINVAL;
+    const size_t need = mx4_gemm_workspace(g.a.rows, g.b.rows, g.a.k);
+    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return I8MP_EWORKSPACE;
+    if (i8mp_status s = check_device(); s != I8MP_OK) return s;
+    g.bias = bias;
+    g.out_dtype = out_dtype;
+    g.out = out;
+    g.ldout = ldout;
+    g.part = static_cast<float*>(workspace);
+    return launched(launch_mx4_gemm(g, stream));
+}
+
+size_t i8mp_mx4_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+    if (!mx4_sizes(m, n, k)) return 0;
+    size_t at = 0;
+    mx4_at(nullptr, &at, m, k);
+    return at + mx4_gemm_workspace(m, n, k);
+}
+
+i8mp_status i8mp_mx4_linear(const void* x, int32_t dtype, int64_t m, int64_t ldx, const i8mp_mx4* w, const void* bias,
+                            void* out, int64_t ldout, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    MxGemmArgs g{};
+    if (!mx4(w, &g.b) || !half_type(dtype) || m < 0 || m > INT32_MAX || g.b.k > INT32_MAX) return I8MP_EINVAL;
+    const int64_t n = g.b.rows, k = g.b.k;
+    if (ldx < k || ldout < n || bad_ld(ldout)) return I8MP_EINVAL;
+    if (m == 0 || n == 0) return I8MP_OK;
+    if (!out || (k > 0 && !x) || !mx4_data(g.b)) return I8MP_EINVAL;
+    const size_t need = i8mp_mx4_linear_workspace_bytes(m, n, k);
+    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return I8MP_EWORKSPACE;
+    if (i8mp_status s = check_device(); s != I8MP_OK) return s;
+    size_t at = 0;
+    g.a = mx4_at(static_cast<char*>(workspace), &at, m, k);
+    g.bias = bias;
+    g.out_dtype = dtype;
+    g.out = out;
+    g.ldout = ldout;
+    g.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + at);
+    if (k > 0)
+        if (i8mp_status s = launched(launch_mx4_quantize(mx4_quant(x, ldx, dtype, false, g.a), stream)); s != I8MP_OK) return s;
+    return launched(launch_mx4_gemm(g, stream));
+}
+
+size_t i8mp_mx4_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+    if (!mx4_sizes(m, n, k)) return 0;
+    size_t at = 0;
+    mx4_at(nullptr, &at, m, n);
+    mx4_at(nullptr, &at, k, n);
+    mx4_at(nullptr, &at, n, m);
+    mx4_at(nullptr, &at, k, m);
+    const size_t x = mx4_gemm_workspace(m, k, n), w = mx4_gemm_workspace(n, k, m);
+    return at + (x > w ? x : w);
+}
+
+i8mp_status i8mp_mx4_linear_backward(const void* grad_out, int64_t ldg, const void* x, int64_t ldx, const void* w,
+                                     int64_t ldw, int32_t dtype, int64_t m, int64_t n, int64_t k, void* grad_x,
+                                     int64_t ldgx, void* grad_w, int64_t ldgw, void* workspace, size_t workspace_bytes,
+                                     hipStream_t stream) {
+    if (!mx4_sizes(m, n, k) || !mx4_fits(m) || !mx4_fits(n) || !half_type(dtype) || ldg < n) return I8MP_EINVAL;
+    const bool want_x = grad_x && m > 0 && k > 0, want_w = grad_w && n > 0 && k > 0;
+    if (grad_x && (ldw < k || ldgx < k || bad_ld(ldgx))) return I8MP_EINVAL;
+    if (grad_w && (ldx < k || ldgw < k || bad_ld(ldgw))) return I8MP_EINVAL;
+    if (!want_x && !want_w) return I8MP_OK;
+    if ((!grad_out && m > 0 && n > 0) || (want_x && n > 0 && !w) || (want_w && m > 0 && !x)) return I8MP_EINVAL;
+    const size_t need = i8mp_mx4_linear_backward_workspace_bytes(m, n, k);
+    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return I8MP_EWORKSPACE;
+    if (i8mp_status s = check_device(); s != I8MP_OK) return s;
+    char* const base = static_cast<char*>(workspace);
+    size_t at = 0;
+    const Mx4 g_rows = mx4_at(base, &at, m, n), w_cols = mx4_at(base, &at, k, n);
+    const Mx4 g_cols = mx4_at(base, &at, n, m), x_cols = mx4_at(base, &at, k, m);
+    MxGemmArgs g{};
+    g.out_dtype = dtype;
+    g.part = reinterpret_cast<float*>(base + at);
+    const auto quantize = [&](const void* p, int64_t ld, bool columns, const Mx4& q) {
+        return q.rows > 0 && q.k > 0 ? launch_mx4_quantize(mx4_quant(p, ld, dtype, columns, q), stream) : hipSuccess;
+    };
+    if (want_x) {
+        if (i8mp_status s = launched(quantize(grad_out, ldg, false, g_rows)); s != I8MP_OK) return s;
+        if (i8mp_status s = launched(quantize(w, ldw, true, w_cols)); s != I8MP_OK) return s;
+        g.a = g_rows;
+        g.b = w_cols;
+        g.out = grad_x;
+        g.ldout = ldgx;
+        if (i8mp_status s = launched(launch_mx4_gemm(g, stream)); s != I8MP_OK) return s;
+    }
+    if (want_w) {
+        if (i8mp_status s = launched(quantize(grad_out, ldg, true, g_cols)); s != I8MP_OK) return s;
+        if (i8mp_status s = launched(quantize(x, ldx, true, x_cols)); s != I8MP_OK) return s;
+        g.a = g_cols;
+        g.b = x_cols;
+        g.out = grad_w;
+        g.ldout = ldgw;
+        if (i8mp_status s = launched(launch_mx4_gemm(g, stream)); s != I8MP_OK) return s;
+    }
+    return I8MP_OK;
 }
 
 }  // extern "C"

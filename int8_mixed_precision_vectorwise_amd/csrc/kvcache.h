@@ -41,6 +41,22 @@ struct KvMoveArgs {
 hipError_t launch_kv_write(const KvMoveArgs& a, hipStream_t stream);
 hipError_t launch_kv_read(const KvMoveArgs& a, hipStream_t stream);
 
+// A write whose keys are rotated first, and queries with them.
+struct KvAppendArgs {
+    KvMoveArgs m;
+    const half_bits* q; int64_t ldq, hsq;   // nullable
+    half_bits* out; int64_t ldo, hso;       // rotated q; may be q itself
+    int32_t q_heads;
+    const int64_t* positions;               // [tokens], taken into [0, table_rows)
+    const float* cos;                       // [table_rows x rotary / 2], and sin
+    const float* sin;
+    int64_t ldcos, ldsin, table_rows;
+    int32_t rotary;                         // dims of a head that turn, a multiple of 16
+    bool interleaved;                       // pairs (2 i, 2 i + 1), else (i, i + rotary / 2)
+    uint32_t kv_blocks;                     // set by the launcher: workgroups that write, the others turn q
+};
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t stream);
+
 struct KvAttnArgs {
     KvCache c;
     const half_bits* q; int64_t ldq, hsq;

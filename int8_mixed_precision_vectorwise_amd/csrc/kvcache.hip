@@ -219,31 +219,19 @@ __device__ inline void store16(void* p, const u4& x) {
     else *static_cast<u4*>(p) = x;
 }
 
-template <bool kBf16, int NB, bool kPast>
-__global__ __launch_bounds__(kThreads) void kv_write_kernel(KvMoveArgs a) {
-    const Lane<NB> l = lane_of<NB>(a);
-    if (!l.live) return;  // the 8 lanes of a block leave together
-    int64_t slot[kQuad];
-    const bool whole = slots_of(a, l, slot);
-    const int dim = l.b * 64 + l.part * 8;
-    const half_bits* ks = static_cast<const half_bits*>(a.k) + l.tok0 * a.ldk + l.h * a.hsk + dim;
-    const half_bits* vs = static_cast<const half_bits*>(a.v) + l.tok0 * a.ldv + l.h * a.hsv + dim;
-    uint4 k[kQuad], v[kQuad];
-#pragma unroll
-    for (int i = 0; i < kQuad; ++i) {
-        const bool live = slot[i] >= 0;
-        k[i] = live ? load16<kPast>(ks + i * a.ldk) : make_uint4(0, 0, 0, 0);
-        v[i] = live ? load16<kPast>(vs + i * a.ldv) : make_uint4(0, 0, 0, 0);
-    }
+// quantizes and stores a lane's share of four tokens
+template <bool kBf16, int NB>
+__device__ inline void store_quad(const KvCache& c, const Lane<NB>& l, const int64_t (&slot)[kQuad], bool whole,
+                                  const uint4 (&k)[kQuad], const uint4 (&v)[kQuad]) {
     uint32_t kc[kQuad], vc[kQuad], ka[kQuad], va[kQuad];
 #pragma unroll
     for (int i = 0; i < kQuad; ++i) {
         kc[i] = quantize8<kBf16>(k[i], ka[i]);
         vc[i] = quantize8<kBf16>(v[i], va[i]);
     }
-    const int v_scales = a.c.page_size * 2 * NB;  // behind the K scales
+    const int v_scales = c.page_size * 2 * NB;  // behind the K scales
     if (whole) {
-        const Spot s = spot_of<NB>(a.c, slot[0], l);
+        const Spot s = spot_of<NB>(c, slot[0], l);
 #pragma unroll
         for (int i = 0; i < kQuad; ++i) *reinterpret_cast<uint32_t*>(s.k + i * 32 * NB) = kc[i];
         *reinterpret_cast<uint2*>(s.v) = v_words(vc[0], vc[1], vc[2], vc[3], false);
@@ -260,7 +248,7 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvMoveArgs a) {
 #pragma unroll
     for (int i = 0; i < kQuad; ++i) {
         if (slot[i] < 0) continue;
-        const Spot s = spot_of<NB>(a.c, slot[i], l);
+        const Spot s = spot_of<NB>(c, slot[i], l);
         *reinterpret_cast<uint32_t*>(s.k) = kc[i];
         *reinterpret_cast<uint16_t*>(s.v) = (uint16_t)vc[i];
         *reinterpret_cast<uint16_t*>(s.v + 8 * NB) = (uint16_t)(vc[i] >> 16);
@@ -269,6 +257,186 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(KvMoveArgs a) {
             *reinterpret_cast<uint16_t*>(s.s + v_scales) = (uint16_t)va[i];
         }
     }
+}
+
+template <bool kBf16, int NB, bool kPast>
+__global__ __launch_bounds__(kThreads) void kv_write_kernel(KvMoveArgs a) {
+    const Lane<NB> l = lane_of<NB>(a);
+    if (!l.live) return;  // the 8 lanes of a block leave together
+    int64_t slot[kQuad];
+    const bool whole = slots_of(a, l, slot);
+    const int dim = l.b * 64 + l.part * 8;
+    const half_bits* ks = static_cast<const half_bits*>(a.k) + l.tok0 * a.ldk + l.h * a.hsk + dim;
+    const half_bits* vs = static_cast<const half_bits*>(a.v) + l.tok0 * a.ldv + l.h * a.hsv + dim;
+    uint4 k[kQuad], v[kQuad];
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i) {
+        const bool live = slot[i] >= 0;
+        k[i] = live ? load16<kPast>(ks + i * a.ldk) : make_uint4(0, 0, 0, 0);
+        v[i] = live ? load16<kPast>(vs + i * a.ldv) : make_uint4(0, 0, 0, 0);
+    }
+    store_quad<kBf16, NB>(a.c, l, slot, whole, k, v);
+}
+
+// ---- rotation by position -------------------------------------------------------
+// Pair i of a head's first `rotary` dims turns by its token's angle i: (a cos - b sin,
+// b cos + a sin), rounded to fp32 from the exact value, then to the 16-bit type.  The
+// products of 11-bit and 24-bit numbers are exact in 64 bits and their sum rounds once
+// at 2^-53, so the rounding to fp32 is that of the exact value but where it lies within
+// 2^-29 of a border: the keys' codes, which a value next to a border of the 4-bit grid
+// decides, do not depend on how the sum was formed.
+typedef v4f v4f_any __attribute__((aligned(4)));
+
+template <bool kBf16>
+__device__ inline half_bits narrow(float x) {
+    if constexpr (kBf16) return __builtin_bit_cast(half_bits, (__bf16)x);
+    else return f2h(x);
+}
+
+// x cos + y sin
+template <bool kBf16>
+__device__ inline half_bits turn(uint32_t x, uint32_t y, float c, float s) {
+    float r = (float)__builtin_fma((double)wide<kBf16>(x), (double)c, (double)wide<kBf16>(y) * (double)s);
+    asm("" : "+v"(r));  // the compiler otherwise makes one rounding of the two
+    return narrow<kBf16>(r);
+}
+
+__device__ inline uint32_t half_of(const uint4& x, int e) {
+    const uint32_t w = e < 4 ? (e < 2 ? x.x : x.y) : (e < 6 ? x.z : x.w);
+    return (w >> (16 * (e & 1))) & 0xffffu;
+}
+
+__device__ inline void load8(const float* p, float (&x)[8]) {
+    const v4f a = *reinterpret_cast<const v4f_any*>(p), b = *reinterpret_cast<const v4f_any*>(p + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = a[e], x[4 + e] = b[e];
+}
+
+// 8 dims of a head whose pairs are the 8 of `other`; sign -1: these are the pairs' first
+template <bool kBf16>
+__device__ inline uint4 turn_halves(const uint4& own, const uint4& other, const float (&c)[8], const float (&s)[8], float sign) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = turn<kBf16>(half_of(own, 2 * i), half_of(other, 2 * i), c[2 * i], sign * s[2 * i]) |
+               (uint32_t)turn<kBf16>(half_of(own, 2 * i + 1), half_of(other, 2 * i + 1), c[2 * i + 1], sign * s[2 * i + 1]) << 16;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 8 dims that are four pairs
+template <bool kBf16>
+__device__ inline uint4 turn_pairs(const uint4& x, const v4f& c, const v4f& s) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = half_of(x, 2 * i), b = half_of(x, 2 * i + 1);
+        w[i] = turn<kBf16>(a, b, c[i], -s[i]) | (uint32_t)turn<kBf16>(b, a, c[i], s[i]) << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// the tables' row of a token
+__device__ inline int64_t row_of(const KvAppendArgs& a, int64_t token) {
+    const int64_t p = a.positions[token];
+    return p < 0 ? 0 : p < a.table_rows ? p : a.table_rows - 1;
+}
+
+constexpr int kTurnHeads = 4;  // heads of q that a lane turns by one token's angles
+
+// q: a lane has two 8-dim pieces of kTurnHeads heads of a token, those that turn into each other, so that q may
+// be turned in place.  Pieces of a head, `half` = rotary / 16 pairs first: (u, u + half), then those that do not
+// turn, two by two; where pairs are neighbours, (2 u, 2 u + 1).
+template <bool kBf16, int NB, bool kPast>
+__device__ inline void turn_queries(const KvAppendArgs& a, uint32_t block) {
+    constexpr int kUnits = 4 * NB;
+    const uint32_t groups = (uint32_t)(a.q_heads + kTurnHeads - 1) / kTurnHeads;  // heads g, g + groups, ...
+    const uint32_t i = block * kThreads + threadIdx.x, u = i % kUnits, rest = i / kUnits;
+    const uint32_t t = rest / groups, g = rest - t * groups;
+    if (t >= a.m.tokens) return;
+    const int half = a.rotary / 16;
+    int p0 = (int)u, p1 = p0 + half;
+    if (a.interleaved || p0 >= half) {
+        p0 = a.interleaved ? 2 * (int)u : 2 * half + 2 * ((int)u - half);
+        p1 = p0 + 1;
+    }
+    const int64_t row = row_of(a, t);
+    const float *cos = a.cos + row * a.ldcos, *sin = a.sin + row * a.ldsin;
+    const half_bits* from = a.q + (int64_t)t * a.ldq;
+    half_bits* to = a.out + (int64_t)t * a.ldo;
+    uint4 x[kTurnHeads][2];
+#pragma unroll
+    for (int j = 0; j < kTurnHeads; ++j) {
+        const int64_t h = g + (int64_t)j * groups;
+        if (h >= a.q_heads) break;
+        x[j][0] = load16<kPast>(from + h * a.hsq + p0 * 8);
+        x[j][1] = load16<kPast>(from + h * a.hsq + p1 * 8);
+    }
+    float c[8], s[8];
+    if (p0 * 8 < a.rotary) {  // the angles of pairs 8 u .. 8 u + 7
+        load8(cos + 8 * u, c);
+        load8(sin + 8 * u, s);
+    }
+#pragma unroll
+    for (int j = 0; j < kTurnHeads; ++j) {
+        const int64_t h = g + (int64_t)j * groups;
+        if (h >= a.q_heads) break;
+        uint4 y0 = x[j][0], y1 = x[j][1];
+        if (p0 * 8 < a.rotary) {
+            if (a.interleaved) {  // rotary is a multiple of 16: both pieces turn
+                y0 = turn_pairs<kBf16>(x[j][0], v4f{c[0], c[1], c[2], c[3]}, v4f{s[0], s[1], s[2], s[3]});
+                y1 = turn_pairs<kBf16>(x[j][1], v4f{c[4], c[5], c[6], c[7]}, v4f{s[4], s[5], s[6], s[7]});
+            } else {
+                y0 = turn_halves<kBf16>(x[j][0], x[j][1], c, s, -1.0f);
+                y1 = turn_halves<kBf16>(x[j][1], x[j][0], c, s, 1.0f);
+            }
+        }
+        store16<kPast>(to + h * a.hso + p0 * 8, __builtin_bit_cast(u4, y0));
+        store16<kPast>(to + h * a.hso + p1 * 8, __builtin_bit_cast(u4, y1));
+    }
+}
+
+template <bool kBf16, int NB, bool kPast>
+__global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendArgs a) {
+    if (blockIdx.x >= a.kv_blocks) {
+        turn_queries<kBf16, NB, kPast>(a, blockIdx.x - a.kv_blocks);
+        return;
+    }
+    const Lane<NB> l = lane_of<NB>(a.m);
+    if (!l.live) return;
+    int64_t slot[kQuad];
+    const bool whole = slots_of(a.m, l, slot);
+    const int dim = l.b * 64 + l.part * 8;
+    const half_bits* ks = static_cast<const half_bits*>(a.m.k) + l.tok0 * a.m.ldk + l.h * a.m.hsk;
+    const half_bits* vs = static_cast<const half_bits*>(a.m.v) + l.tok0 * a.m.ldv + l.h * a.m.hsv + dim;
+    const int half = a.rotary / 2;
+    const bool turns = dim < a.rotary, halves = turns && !a.interleaved, first = dim < half;
+    const int other = halves ? (first ? dim + half : dim - half) : dim;
+    uint4 k[kQuad], v[kQuad], o[kQuad];
+#pragma unroll
+    for (int i = 0; i < kQuad; ++i) {
+        const bool live = slot[i] >= 0;
+        k[i] = live ? load16<false>(ks + i * a.m.ldk + dim) : make_uint4(0, 0, 0, 0);
+        o[i] = live && halves ? load16<false>(ks + i * a.m.ldk + other) : make_uint4(0, 0, 0, 0);
+        v[i] = live ? load16<kPast>(vs + i * a.m.ldv) : make_uint4(0, 0, 0, 0);
+    }
+    if (turns) {
+#pragma unroll
+        for (int i = 0; i < kQuad; ++i) {
+            if (slot[i] < 0) continue;
+            const int64_t row = row_of(a, l.tok0 + i);
+            const float *cos = a.cos + row * a.ldcos, *sin = a.sin + row * a.ldsin;
+            if (a.interleaved) {
+                const v4f c = *reinterpret_cast<const v4f_any*>(cos + dim / 2), s = *reinterpret_cast<const v4f_any*>(sin + dim / 2);
+                k[i] = turn_pairs<kBf16>(k[i], c, s);
+            } else {
+                float c[8], s[8];
+                load8(cos + (first ? dim : dim - half), c);
+                load8(sin + (first ? dim : dim - half), s);
+                k[i] = turn_halves<kBf16>(k[i], o[i], c, s, first ? -1.0f : 1.0f);
+            }
+        }
+    }
+    store_quad<kBf16, NB>(a.m.c, l, slot, whole, k, v);
 }
 
 // one lane's 8 values of a token in the output's type
@@ -343,11 +511,13 @@ int64_t move_blocks(const KvMoveArgs& a, int64_t tokens) {
     return per >= kThreads ? quads * ceil_div(per, kThreads) : ceil_div(quads, kThreads / per);
 }
 
-// Tokens in launches of at most 2^22 workgroups (a grid holds fewer than 2^32 lanes).
+// Tokens in launches of at most 2^22 workgroups (a grid holds fewer than 2^32 lanes), and 2^22 more with `beside`
+// lanes a token.
 template <typename F>
-hipError_t in_pieces(const KvMoveArgs& args, int elem, F launch) {
+hipError_t in_pieces(const KvMoveArgs& args, int elem, int64_t beside, F launch) {
     const int64_t per = ceil_div((int64_t)args.c.heads * 8 * args.c.blocks, kThreads);
-    const int64_t most = ((int64_t)1 << 22) / per / (kSpan / kQuad + 1) * kSpan;
+    int64_t most = ((int64_t)1 << 22) / per / (kSpan / kQuad + 1) * kSpan;
+    if (most * beside > (int64_t)1 << 30) most = ((int64_t)1 << 30) / beside / kSpan * kSpan;
     for (int64_t t = 0; t < args.tokens; t += most) {
         KvMoveArgs a = args;
         a.tokens = args.tokens - t < most ? args.tokens - t : most;
@@ -367,9 +537,26 @@ bool past_cache(const KvMoveArgs& a, int elem) {
 template <bool kBf16, int NB>
 hipError_t write(const KvMoveArgs& args, hipStream_t stream) {
     const bool past = past_cache(args, 2);
-    return in_pieces(args, 2, [&](const KvMoveArgs& a, dim3 grid) {
+    return in_pieces(args, 2, 0, [&](const KvMoveArgs& a, dim3 grid) {
         if (past) hipLaunchKernelGGL((kv_write_kernel<kBf16, NB, true>), grid, dim3(kThreads), 0, stream, a);
         else hipLaunchKernelGGL((kv_write_kernel<kBf16, NB, false>), grid, dim3(kThreads), 0, stream, a);
+    });
+}
+
+template <bool kBf16, int NB>
+hipError_t append(const KvAppendArgs& args, hipStream_t stream) {
+    const int64_t groups = args.q ? ceil_div(args.q_heads, kTurnHeads) : 0;
+    const bool past = past_cache(args.m, 2);
+    return in_pieces(args.m, 2, groups * 4 * NB, [&](const KvMoveArgs& m, dim3 grid) {
+        KvAppendArgs a = args;
+        const int64_t t = m.slots - args.m.slots;
+        a.m = m;
+        a.positions += t;
+        if (a.q) a.q += t * a.ldq, a.out += t * a.ldo;
+        a.kv_blocks = grid.x;
+        grid.x += (unsigned)ceil_div(m.tokens * groups * 4 * NB, kThreads);
+        if (past) hipLaunchKernelGGL((kv_append_kernel<kBf16, NB, true>), grid, dim3(kThreads), 0, stream, a);
+        else hipLaunchKernelGGL((kv_append_kernel<kBf16, NB, false>), grid, dim3(kThreads), 0, stream, a);
     });
 }
 
@@ -377,7 +564,7 @@ template <bool kBf16, int NB, int kType>
 hipError_t read_as(const KvMoveArgs& args, hipStream_t stream) {
     constexpr int kElem = kType == I8MP_DTYPE_F32 ? 4 : 2;
     const bool past = past_cache(args, kElem);
-    return in_pieces(args, kElem, [&](const KvMoveArgs& a, dim3 grid) {
+    return in_pieces(args, kElem, 0, [&](const KvMoveArgs& a, dim3 grid) {
         if (past) hipLaunchKernelGGL((kv_read_kernel<kBf16, NB, kType, true>), grid, dim3(kThreads), 0, stream, a);
         else hipLaunchKernelGGL((kv_read_kernel<kBf16, NB, kType, false>), grid, dim3(kThreads), 0, stream, a);
     });
@@ -396,6 +583,12 @@ hipError_t launch_kv_write(const KvMoveArgs& a, hipStream_t stream) {
     if (a.c.bf16)
         return a.c.blocks == 1 ? write<true, 1>(a, stream) : a.c.blocks == 2 ? write<true, 2>(a, stream) : write<true, 4>(a, stream);
     return a.c.blocks == 1 ? write<false, 1>(a, stream) : a.c.blocks == 2 ? write<false, 2>(a, stream) : write<false, 4>(a, stream);
+}
+
+hipError_t launch_kv_append(const KvAppendArgs& a, hipStream_t stream) {
+    if (a.m.c.bf16)
+        return a.m.c.blocks == 1 ? append<true, 1>(a, stream) : a.m.c.blocks == 2 ? append<true, 2>(a, stream) : append<true, 4>(a, stream);
+    return a.m.c.blocks == 1 ? append<false, 1>(a, stream) : a.m.c.blocks == 2 ? append<false, 2>(a, stream) : append<false, 4>(a, stream);
 }
 
 hipError_t launch_kv_read(const KvMoveArgs& a, hipStream_t stream) {

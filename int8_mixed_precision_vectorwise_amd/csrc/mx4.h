@@ -1,0 +1,48 @@
+// Internal declarations of the microscaled 4-bit matrices: quantization by rows
+// and by columns, dequantization and the product (gfx950 only).
+#pragma once
+
+#include "common.h"
+
+namespace i8mp {
+
+constexpr int kMxBlock = 32;    // elements under one scale
+constexpr int kMxPad = 128;     // rows are padded with zeros to whole multiples: 64 bytes of codes, 4 scales
+
+// A [rows x k] matrix of E2M1 codes, two a byte, and one E8M0 scale a block.
+struct Mx4 {
+    uint8_t* codes; int64_t ldc;    // bytes; 16-byte aligned, ldc a multiple of 16
+    uint8_t* scales; int64_t lds;   // bytes; 4-byte aligned, lds a multiple of 4
+    int64_t rows, k;
+    __host__ __device__ int64_t kp() const { return (k + kMxPad - 1) / kMxPad * kMxPad; }
+};
+
+struct MxQuantArgs {
+    const half_bits* x;             // [m x k], or with `columns` [q.k x q.rows]: its transpose is quantized
+    int64_t ldx;
+    bool bf16;
+    bool columns;
+    Mx4 q;
+};
+
+struct MxDequantArgs {
+    Mx4 q;
+    int32_t out_dtype;
+    void* out; int64_t ldout;
+};
+
+struct MxGemmArgs {
+    Mx4 a, b;                       // out [a.rows x b.rows] = a . b^T + bias
+    const void* bias;               // nullable, [b.rows] of out's type
+    int32_t out_dtype;
+    void* out; int64_t ldout;
+    float* part;                    // workspace of mx4_gemm_workspace() bytes
+};
+
+hipError_t launch_mx4_quantize(const MxQuantArgs& a, hipStream_t stream);
+hipError_t launch_mx4_dequantize(const MxDequantArgs& a, hipStream_t stream);
+// workspace of a product of these sizes (0: none needed)
+size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k);
+hipError_t launch_mx4_gemm(const MxGemmArgs& g, hipStream_t stream);
+
+}  // namespace i8mp

@@ -1,0 +1,320 @@
+// Microscaled 4-bit matrices: quantization of 16-bit matrices by rows and by
+// columns, and dequantization.
+//
+// Elements are E2M1 in blocks of 32 along k under a power of two 2^E, held as the
+// byte E + 127:
+//   E = max(floor(log2 max |x|) - 2, -127): the block's largest value falls into
+//       [4, 8) times 2^E, of which E2M1 reaches 6;
+//   code = sign | E2M1 magnitude nearest to |x| / 2^E, ties to even, at most 6;
+//   a block that holds a NaN or an infinity has the byte 255 (no number) and codes 0.
+// Dividing by a power of two is exact, so every code is decided exactly: the
+// hardware's conversion (v_cvt_scalef32_pk_fp4_*) gives the definition's codes for
+// all 16-bit values, checked value by value.  Both passes stream: 2 bytes an
+// element in, 17/32 of a byte out.
+#include "common.h"
+#include "mx4.h"
+#include "quant_util.h"
+
+namespace i8mp {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+typedef _Float16 hh2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bb2 __attribute__((ext_vector_type(2)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+// at any element's address
+typedef v4u v4u_any __attribute__((aligned(2)));
+typedef uint32_t u32_any __attribute__((aligned(2)));
+
+// the scale's byte from the bits of the largest magnitude
+template <bool kBf16>
+__device__ inline uint32_t scale_byte(uint32_t top) {
+    // fp16's subnormal numbers are normal in fp32; bfloat16's get the least scale
+    const uint32_t bits = kBf16 ? top << 16 : __float_as_uint(h2f((half_bits)top));
+    const uint32_t e = bits >> 23;
+    return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+
+// 2^(byte - 127); 255 gives a NaN
+__device__ inline float scale_value(uint32_t byte) {
+    return __uint_as_float(byte == 0u ? 0x00400000u : byte == 255u ? 0x7fc00000u : byte << 23);
+}
+
+__device__ inline us2 mags(uint32_t w) { return __builtin_bit_cast(us2, w & 0x7fff7fffu); }
+
+// byte kSel of `old` := codes of a pair of 16-bit values
+template <bool kBf16, int kSel>
+__device__ inline uint32_t encode2(uint32_t old, uint32_t w, float scale) {
+    if constexpr (kBf16) return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(bb2, w), scale, kSel);
+    else return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, __builtin_bit_cast(hh2, w), scale, kSel);
+}
+template <bool kBf16>
+__device__ inline uint32_t encode8(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, float scale) {
+    uint32_t c = encode2<kBf16, 0>(0u, w0, scale);
+    c = encode2<kBf16, 1>(c, w1, scale);
+    c = encode2<kBf16, 2>(c, w2, scale);
+    return encode2<kBf16, 3>(c, w3, scale);
+}
+
+// ---- by rows ------------------------------------------------------------------
+// A lane has 8 neighbouring elements, four lanes a block.  A workgroup is
+// kThreads / lanes rows of `lanes` chunks at a time, and takes kRowSteps of them:
+// as many 16-byte loads in flight a lane.
+constexpr int kRowSteps = 4;
+
+template <bool kBf16, bool kAligned>
+__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(MxQuantArgs a, int lane_shift) {
+    const int lanes = 1 << lane_shift, rows = kThreads >> lane_shift;
+    const int64_t c = (int64_t)blockIdx.x * lanes + (threadIdx.x & (lanes - 1));  // chunk of 8 elements
+    const int64_t row0 = (int64_t)blockIdx.y * (rows * kRowSteps) + (threadIdx.x >> lane_shift);
+    if (c * 8 >= a.q.kp()) return;  // whole blocks leave: kp is a multiple of 128
+    const int64_t left = a.q.k - c * 8;
+    v4u x[kRowSteps];
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i) {
+        x[i] = v4u{0, 0, 0, 0};
+        const int64_t r = row0 + i * rows;
+        if (r >= a.q.rows) continue;
+        const half_bits* p = a.x + r * a.ldx + c * 8;
+        if (left >= 8) {
+            if constexpr (kAligned) x[i] = *reinterpret_cast<const v4u*>(p);
+            else x[i] = *reinterpret_cast<const v4u_any*>(p);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < left) x[i][e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i) {
+        const int64_t r = row0 + i * rows;
+        if (r >= a.q.rows) continue;
+        us2 m = __builtin_elementwise_max(__builtin_elementwise_max(mags(x[i][0]), mags(x[i][1])),
+                                          __builtin_elementwise_max(mags(x[i][2]), mags(x[i][3])));
+        uint32_t top = m.x > m.y ? m.x : m.y;
+        const auto up = [](uint32_t p, uint32_t q) { return p > q ? p : q; };
+        top = up(top, (uint32_t)dpp_i32<kDppQuadSwap1>((int32_t)top));
+        top = up(top, (uint32_t)dpp_i32<kDppQuadSwap2>((int32_t)top));
+        const uint32_t byte = scale_byte<kBf16>(top);
+        uint32_t codes = encode8<kBf16>(x[i][0], x[i][1], x[i][2], x[i][3], scale_value(byte));
+        if (byte == 255u) codes = 0;
+        *reinterpret_cast<uint32_t*>(a.q.codes + r * a.q.ldc + c * 4) = codes;
+        if ((threadIdx.x & 3) == 0) a.q.scales[r * a.q.lds + (c >> 2)] = (uint8_t)byte;
+    }
+}
+
+// ---- by columns ------------------------------------------------------------------
+// x [k x rows] read as it lies, its transpose quantized: a block is 32 rows of one
+// column.  A wave has 32 rows of 128 columns, a lane two columns: the block's
+// maximum needs no other lane, and 32 loads of 4 bytes are in flight a lane.  The
+// codes (16 bytes a column) meet in LDS, so that a column leaves as kWaves * 16
+// contiguous bytes.
+constexpr int kColCols = 128;
+
+template <bool kBf16, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void quantize_columns_kernel(MxQuantArgs a) {
+    constexpr int kPitch = kWaves * 16 + 16;
+    __shared__ __attribute__((aligned(16))) uint8_t codes[kColCols * kPitch];
+    __shared__ __attribute__((aligned(16))) uint8_t scales[kColCols * kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c0 = (int64_t)blockIdx.x * kColCols, c = c0 + 2 * lane;
+    const int64_t r0 = ((int64_t)blockIdx.y * kWaves + wave) * kMxBlock;
+    uint32_t x[kMxBlock];
+    const half_bits* p = a.x + r0 * a.ldx + c;
+    const bool two = c + 1 < a.q.rows, one = c < a.q.rows;
+#pragma unroll
+    for (int i = 0; i < kMxBlock; ++i) {
+        x[i] = 0;
+        if (r0 + i >= a.q.k) continue;
+        if (two) x[i] = *reinterpret_cast<const u32_any*>(p + i * a.ldx);
+        else if (one) x[i] = p[i * a.ldx];
+    }
+    us2 m = mags(x[0]);
+#pragma unroll
+    for (int i = 1; i < kMxBlock; ++i) m = __builtin_elementwise_max(m, mags(x[i]));
+    const uint32_t b0 = scale_byte<kBf16>(m.x), b1 = scale_byte<kBf16>(m.y);
+    const float s0 = scale_value(b0), s1 = scale_value(b1);
+    v4u k0, k1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t u = x[8 * i + 2 * j], v = x[8 * i + 2 * j + 1];
+            lo[j] = __builtin_amdgcn_perm(v, u, 0x05040100u);
+            hi[j] = __builtin_amdgcn_perm(v, u, 0x07060302u);
+        }
+        k0[i] = b0 == 255u ? 0u : encode8<kBf16>(lo[0], lo[1], lo[2], lo[3], s0);
+        k1[i] = b1 == 255u ? 0u : encode8<kBf16>(hi[0], hi[1], hi[2], hi[3], s1);
+    }
+    *reinterpret_cast<v4u*>(codes + 2 * lane * kPitch + wave * 16) = k0;
+    *reinterpret_cast<v4u*>(codes + (2 * lane + 1) * kPitch + wave * 16) = k1;
+    scales[2 * lane * kWaves + wave] = (uint8_t)b0;
+    scales[(2 * lane + 1) * kWaves + wave] = (uint8_t)b1;
+    __syncthreads();
+    const int64_t blocks = a.q.kp() / kMxBlock, first = (int64_t)blockIdx.y * kWaves;
+    for (int t = threadIdx.x; t < kColCols * kWaves; t += 64 * kWaves) {
+        const int col = t / kWaves, part = t % kWaves;
+        if (c0 + col < a.q.rows && first + part < blocks)
+            *reinterpret_cast<v4u*>(a.q.codes + (c0 + col) * a.q.ldc + (first + part) * 16) =
+                *reinterpret_cast<const v4u*>(codes + col * kPitch + part * 16);
+    }
+    for (int t = threadIdx.x; t < kColCols * kWaves / 4; t += 64 * kWaves) {
+        const int col = t / (kWaves / 4), part = t % (kWaves / 4) * 4;
+        if (c0 + col < a.q.rows && first + part < blocks)
+            *reinterpret_cast<uint32_t*>(a.q.scales + (c0 + col) * a.q.lds + first + part) =
+                *reinterpret_cast<const uint32_t*>(scales + col * kWaves + part);
+    }
+}
+
+// ---- back -----------------------------------------------------------------------
+
+template <int kType>
+__device__ inline void store_out(void* out, int64_t at, const float (&v)[8], int64_t left) {
+    if constexpr (kType == I8MP_DTYPE_F32) {
+        typedef v4f v4f_any __attribute__((aligned(4)));
+        float* p = static_cast<float*>(out) + at;
+        if (left >= 8) {
+            *reinterpret_cast<v4f_any*>(p) = v4f{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<v4f_any*>(p + 4) = v4f{v[4], v[5], v[6], v[7]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < left) p[e] = v[e];
+        }
+    } else {
+        half_bits h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (kType == I8MP_DTYPE_BF16) h[e] = __builtin_bit_cast(half_bits, (__bf16)v[e]);
+            else h[e] = f2h(v[e]);
+        }
+        half_bits* p = static_cast<half_bits*>(out) + at;
+        if (left >= 8) {
+            v4u w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = h[2 * e] | (uint32_t)h[2 * e + 1] << 16;
+            *reinterpret_cast<v4u_any*>(p) = w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < left) p[e] = h[e];
+        }
+    }
+}
+
+template <int kType>
+__global__ __launch_bounds__(kThreads) void dequantize_kernel(MxDequantArgs a, int lane_shift) {
+    const int lanes = 1 << lane_shift, rows = kThreads >> lane_shift;
+    const int64_t c = (int64_t)blockIdx.x * lanes + (threadIdx.x & (lanes - 1));
+    const int64_t row0 = (int64_t)blockIdx.y * (rows * kRowSteps) + (threadIdx.x >> lane_shift);
+    if (c * 8 >= a.q.k) return;
+    uint32_t codes[kRowSteps], byte[kRowSteps];
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i) {
+        const int64_t r = row0 + i * rows;
+        if (r >= a.q.rows) continue;
+        codes[i] = *reinterpret_cast<const uint32_t*>(a.q.codes + r * a.q.ldc + c * 4);
+        byte[i] = a.q.scales[r * a.q.lds + (c >> 2)];
+    }
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i) {
+        const int64_t r = row0 + i * rows;
+        if (r >= a.q.rows) continue;
+        const float s = scale_value(byte[i]);
+        float v[8];
+#define I8MP_PAIR(p)                                                                  \
+    do {                                                                              \
+        const f2 u = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[i], 1.0f, p);     \
+        v[2 * p] = u.x * s;                                                           \
+        v[2 * p + 1] = u.y * s;                                                       \
+    } while (0)
+        I8MP_PAIR(0);
+        I8MP_PAIR(1);
+        I8MP_PAIR(2);
+        I8MP_PAIR(3);
+#undef I8MP_PAIR
+        store_out<kType>(a.out, r * a.ldout + c * 8, v, a.q.k - c * 8);
+    }
+}
+
+// lanes of a workgroup along a row of `chunks`, as a shift: at least 16, since padded rows are whole 16s
+int row_lanes(int64_t chunks) {
+    int s = 4;
+    while (s < 8 && ((int64_t)1 << s) < chunks) ++s;
+    return s;
+}
+
+// Rows in launches whose grid holds them (a grid's second axis ends at 65535).
+template <typename F>
+hipError_t by_rows(int64_t rows, int64_t chunks, F launch) {
+    const int s = row_lanes(chunks);
+    const int64_t per = (int64_t)(kThreads >> s) * kRowSteps, most = per * 65535;
+    for (int64_t r = 0; r < rows; r += most) {
+        const int64_t n = rows - r < most ? rows - r : most;
+        launch(r, n, dim3((unsigned)ceil_div(chunks, (int64_t)1 << s), (unsigned)ceil_div(n, per)), s);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <bool kBf16>
+hipError_t quantize(const MxQuantArgs& args, hipStream_t stream) {
+    if (args.columns) {
+        const bool tall = args.q.k > kMxPad;
+        const int64_t most = (int64_t)65535 * (tall ? 256 : 128);  // rows of x a launch
+        for (int64_t r = 0; r < args.q.k; r += most) {
+            MxQuantArgs a = args;
+            a.x += r * a.ldx;
+            a.q.codes += r / 2;
+            a.q.scales += r / kMxBlock;
+            a.q.k = args.q.k - r < most ? args.q.k - r : most;
+            const unsigned cols = (unsigned)ceil_div(a.q.rows, kColCols);
+            if (tall)
+                hipLaunchKernelGGL((quantize_columns_kernel<kBf16, 8>), dim3(cols, (unsigned)ceil_div(a.q.k, 256)), dim3(512), 0, stream, a);
+            else
+                hipLaunchKernelGGL((quantize_columns_kernel<kBf16, 4>), dim3(cols, (unsigned)ceil_div(a.q.k, 128)), dim3(256), 0, stream, a);
+            if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
+    const bool aligned = args.ldx % 8 == 0 && reinterpret_cast<uintptr_t>(args.x) % 16 == 0;
+    return by_rows(args.q.rows, args.q.kp() / 8, [&](int64_t r, int64_t n, dim3 grid, int s) {
+        MxQuantArgs a = args;
+        a.x += r * a.ldx;
+        a.q.codes += r * a.q.ldc;
+        a.q.scales += r * a.q.lds;
+        a.q.rows = n;
+        if (aligned) hipLaunchKernelGGL((quantize_rows_kernel<kBf16, true>), grid, dim3(kThreads), 0, stream, a, s);
+        else hipLaunchKernelGGL((quantize_rows_kernel<kBf16, false>), grid, dim3(kThreads), 0, stream, a, s);
+    });
+}
+
+template <int kType>
+hipError_t dequantize(const MxDequantArgs& args, hipStream_t stream) {
+    return by_rows(args.q.rows, ceil_div(args.q.k, 8), [&](int64_t r, int64_t n, dim3 grid, int s) {
+        MxDequantArgs a = args;
+        a.q.codes += r * a.q.ldc;
+        a.q.scales += r * a.q.lds;
+        a.q.rows = n;
+        a.out = static_cast<uint8_t*>(a.out) + r * a.ldout * (kType == I8MP_DTYPE_F32 ? 4 : 2);
+        hipLaunchKernelGGL((dequantize_kernel<kType>), grid, dim3(kThreads), 0, stream, a, s);
+    });
+}
+
+}  // namespace
+
+hipError_t launch_mx4_quantize(const MxQuantArgs& a, hipStream_t stream) {
+    return a.bf16 ? quantize<true>(a, stream) : quantize<false>(a, stream);
+}
+
+hipError_t launch_mx4_dequantize(const MxDequantArgs& a, hipStream_t stream) {
+    return a.out_dtype == I8MP_DTYPE_F32   ? dequantize<I8MP_DTYPE_F32>(a, stream)
+           : a.out_dtype == I8MP_DTYPE_F16 ? dequantize<I8MP_DTYPE_F16>(a, stream)
+                                           : dequantize<I8MP_DTYPE_BF16>(a, stream);
+}
+
+}  // namespace i8mp
