@@ -37,6 +37,9 @@ struct MxGemmArgs {
     int32_t out_dtype;
     void* out; int64_t ldout;
     float* part;                    // workspace of mx4_gemm_workspace() bytes
+    // set by the launcher: the sums over k in so many parts of so many stages, each with an output of its own
+    int32_t parts, part_stages;
+    int64_t part_bytes;
 };
 
 hipError_t launch_mx4_quantize(const MxQuantArgs& a, hipStream_t stream);

@@ -5,17 +5,37 @@
 // 2^-24 of the sum of magnitudes; a scale byte of 255 gives NaN).
 //
 // A lane of the instruction holds 32 codes (16 bytes) of one row and that block's
-// scale; lane l has row l % 32 and block l / 32 of the step.  Which blocks of k
-// meet in a step does not matter as long as both operands agree, so a stage of 256
-// elements is taken as four steps in which lanes 0..31 have blocks 0, 1, 2, 3 and
-// lanes 32..63 blocks 4, 5, 6, 7: a lane's four scales are then one aligned word
-// of the row, the instruction picks the step's byte, and the matrices need no
-// other order in memory than rows.
+// scale; lane l has row l % 32 and block l / 32 of the step.  Which blocks of k meet
+// in a step does not matter as long as both operands agree: of 128 elements, lanes
+// 0..31 take blocks 0 and 1, lanes 32..63 blocks 2 and 3, in two steps.  A lane's two
+// scales are then neighbouring bytes, the instruction picks the step's, and matrices
+// lie in memory as plain rows.
 //
 // Workgroups of four waves, 2 x 2, each with 32 FM x 32 FN sums.  Stages of 256
-// elements (128 bytes of codes and 8 of scales a row) go from memory to LDS by
-// direct loads, two buffers in turn.  The weights are the instruction's first
-// operand: a lane then has four neighbouring columns of one output row.
+// elements go from memory to LDS by direct loads, two places in turn: 128 bytes of
+// codes a row are whole lines, which the L2 hands out at 134 GB/s a CU, lines halved
+// (stages of 128 elements) at 70.  Scales come for two stages at once, 16 bytes a row: a
+// load costs the vector memory path a cycle a row however few bytes it takes (with
+// every stage of 128 elements, 4 bytes a row, they cost as much there as the codes).
+// A stage is multiplied in quarters:
+//   1  the second half's operands are read from LDS; then all waves have read the stage
+//   2  its place fills with the stage after next; then all waves' share of the next is in
+//   3, 4  the next stage's first half is read, the rest of the loads go out
+// with reads and loads spread between the matrix instructions: a wave alone on its SIMD
+// that waits for the load path to take another load starves the matrix cores (all loads
+// in a row: 1.04 us for 128 elements of a 256 x 256 tile, spread 0.89, none 0.70).  The
+// weights are the instruction's first operand: a lane then has four neighbouring columns
+// of one output row.
+//
+// 256 x 256 tiles run 256 workgroups that take tiles in turn; a tile's first loads go
+// out before the results of the one before it leave.  At 8192 x 8192 x 16384 the matrix
+// cores are busy 59 % of the cycles at 1.76 GHz: the chip's power limit, which lets
+// matrix instructions alone run at 1.79 GHz (6.4 PFLOP/s), leaves little to gain by more
+// overlap.  The 16x16x128 instruction reaches 7.2 PFLOP/s alone, but its 64 accumulators
+// of four registers left the compiler no room (100 registers spilled).
+//
+// Measured (fp16 out, operands of random bits): 4096 x 22016 x 8192 390 us before the cut
+// below, 8192 x 8192 x 16384 506 us (4.3 PFLOP/s).
 #include "common.h"
 #include "mx4.h"
 
@@ -26,13 +46,12 @@ namespace {
 typedef int v8i __attribute__((ext_vector_type(8)));
 
 constexpr int kStageK = 256;             // elements of a stage
-constexpr int kRowBytes = kStageK / 2;   // its codes of a row
-constexpr int kXcds = 8;
-constexpr int kOut = (int)0x80000000;    // a buffer offset past every range: reads zeros
+constexpr int kRowBytes = kStageK / 2;   // its codes of a row: whole lines of the L2
+constexpr int kXcds = 8, kCUs = 256;
+constexpr int kOut = (int)0x80000000;    // makes a buffer offset leave every range: reads zeros
 
-__device__ inline __amdgpu_buffer_rsrc_t range_of(const void* base, int64_t bytes) {
-    bytes = bytes < 0 ? 0 : bytes > 0x7fffffffLL ? 0x7fffffffLL : bytes;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+__device__ inline __amdgpu_buffer_rsrc_t range_of(const void* base, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
 }
 
 // lane i's 16 or 4 bytes at `offset` land at lds + 16 i or 4 i (lds is the same in every lane)
@@ -66,181 +85,421 @@ __device__ inline void rows_done() {
 
 // Tile of a workgroup.  Workgroups go to the XCDs in turn; each XCD gets a run of
 // neighbouring tiles, in groups of 8 tile rows, so that its L2 serves them.
-__device__ inline void tile_of(int64_t id, int64_t count, int64_t tiles_m, int64_t tiles_n, int64_t& tm, int64_t& tn) {
-    constexpr int kGroup = 8;
-    const int64_t full = count / kXcds * kXcds;
-    const int64_t t = id < full ? id % kXcds * (full / kXcds) + id / kXcds : id;
-    const int64_t first = t / (kGroup * tiles_n) * kGroup, in = t % (kGroup * tiles_n);
-    const int64_t size = tiles_m - first < kGroup ? tiles_m - first : kGroup;
-    tm = first + in % size;
-    tn = in / size;
+__device__ inline void tile_of(uint32_t id, uint32_t count, uint32_t tiles_m, uint32_t tiles_n, int& tm, int& tn) {
+    constexpr uint32_t kGroup = 8;
+    const uint32_t full = count / kXcds * kXcds;
+    const uint32_t t = id < full ? id % kXcds * (full / kXcds) + id / kXcds : id;
+    const uint32_t group = t / (kGroup * tiles_n), first = group * kGroup, in = t - group * (kGroup * tiles_n);
+    const uint32_t size = tiles_m - first < kGroup ? tiles_m - first : kGroup;
+    // divided by vector instructions: back to scalars, which the buffers' descriptors must be
+    const uint32_t col = __builtin_amdgcn_readfirstlane(in / size);
+    tm = __builtin_amdgcn_readfirstlane(first + (in - col * size));
+    tn = col;
+}
+
+// until at most N of the wave's loads are under way, and its LDS reads are done
+template <int N>
+__device__ inline void wait_loads() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0070);
+}
+
+__device__ inline void meet() {
+    __builtin_amdgcn_sched_barrier(0);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 template <int FM, int FN>
 struct Tile {
     static constexpr int BM = 64 * FM, BN = 64 * FN;
-    static constexpr int kCodes = (BM + BN) * kRowBytes;   // a stage in LDS: codes of a, of b, then the scales
-    static constexpr int kStage = kCodes + (BM + BN) * 8;
-    static constexpr int kCopies = (BM + BN) / 32;         // copies of codes a wave and stage, 8 rows each
-    static constexpr int kScaleCopies = (BM + BN) / 128;   // of scales, 32 rows each
-    static_assert((BM + BN) % 128 == 0, "the waves' shares of the copies are equal");
+    static constexpr int kStage = (BM + BN) * kRowBytes;    // codes of a stage in LDS, a's first
+    static constexpr int kScales = (BM + BN) * 16;          // scales of two stages
+    static constexpr int kLoads = (BM + BN) / 32;           // a wave's loads of a stage's codes, 8 rows each
+    static constexpr int kScaleLoads = (BM / 64 + 3) / 4;   // and of a's or b's scales, 64 rows each
+    static_assert(BM >= BN, "b has no more rows than a");
+    // The next tile's first stages are on their way while a tile's results leave, where one workgroup fills a CU
+    static constexpr bool kAhead = FM * FN > 8;
+    static constexpr int kRowOut = 128;                     // bytes of an output row that a wave stages at a time, at most
+    static constexpr int kOutArea = 32 * (kRowOut + 16);    // 32 rows
+    static constexpr int kScaleAt = 2 * kStage;
+    static constexpr int kLds = kScaleAt + kScales + 2 * BN * 4 + (kAhead && 4 * kOutArea > kScales ? 4 * kOutArea : kScales);
 };
 
 template <int FM, int FN, int kType>
 __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx4_gemm_kernel(MxGemmArgs g) {
     using T = Tile<FM, FN>;
     constexpr int BM = T::BM, BN = T::BN;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * T::kStage + BN * 4];
-    float* const bias = reinterpret_cast<float*>(smem + 2 * T::kStage);
+    constexpr int kBiasAt = T::kScaleAt + (T::kAhead ? T::kScales : 2 * T::kScales);
+    constexpr int kScale2At = T::kAhead ? kBiasAt + 2 * BN * 4 : T::kScaleAt + T::kScales;
+    constexpr int kOutAt = T::kAhead ? kScale2At : 0;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLds];
+    static_assert(!T::kAhead || kScale2At + T::kScales <= T::kLds, "the second scales fit where results pass");
+    float* const bias = reinterpret_cast<float*>(smem + kBiasAt);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l32 = lane & 31, hi = lane >> 5;
     const int wm = (wave & 1) * 32 * FM, wn = (wave >> 1) * 32 * FN;
-    int64_t tm, tn;
-    tile_of(blockIdx.x, gridDim.x, (g.a.rows + BM - 1) / BM, (g.b.rows + BN - 1) / BN, tm, tn);
-    const int64_t m0 = tm * BM, n0 = tn * BN, kp = g.a.kp();
-    const int64_t rows_m = g.a.rows - m0 < BM ? g.a.rows - m0 : BM, rows_n = g.b.rows - n0 < BN ? g.b.rows - n0 : BN;
-    const __amdgpu_buffer_rsrc_t ca = range_of(g.a.codes + m0 * g.a.ldc, (rows_m - 1) * g.a.ldc + kp / 2);
-    const __amdgpu_buffer_rsrc_t cb = range_of(g.b.codes + n0 * g.b.ldc, (rows_n - 1) * g.b.ldc + kp / 2);
-    const __amdgpu_buffer_rsrc_t sa = range_of(g.a.scales + m0 * g.a.lds, (rows_m - 1) * g.a.lds + kp / kMxBlock);
-    const __amdgpu_buffer_rsrc_t sb = range_of(g.b.scales + n0 * g.b.lds, (rows_n - 1) * g.b.lds + kp / kMxBlock);
-    const int stages = (int)((kp + kStageK - 1) / kStageK);
-    const bool half = kp % kStageK != 0;   // the last stage has 128 elements
+    const int lda = (int)g.a.ldc, ldb = (int)g.b.ldc, lsa = (int)g.a.lds, lsb = (int)g.b.lds, all_m = (int)g.a.rows, all_n = (int)g.b.rows;
+    const int kp = (int)g.a.kp();
+    const uint32_t tiles_m = (uint32_t)((g.a.rows + BM - 1) / BM), tiles_n = (uint32_t)((g.b.rows + BN - 1) / BN);
+    const uint32_t tiles = tiles_m * tiles_n, units = tiles * (uint32_t)g.parts;
 
-    // Copies of codes: 8 rows of 128 bytes each, lane i the 16-byte chunk at place i % 8 of row i / 8.
-    // Place p of row r holds chunk p ^ (r / 2 % 8): the 16 lanes that LDS serves at once read one chunk of
-    // 16 neighbouring rows, which then lie in 16 different bank groups.
-    int place[2], chunk[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {   // copies of even and of odd index
-        chunk[q] = (lane & 7) ^ ((4 * q + (lane >> 4)) & 7);
-        place[q] = lane >> 3;
-    }
-    auto copy_codes = [&](int c, uint8_t* dst, int t, bool last) {   // copy c of a stage, a's first
-        const int ld = (int)(c < BM / 8 ? g.a.ldc : g.b.ldc), row = (c < BM / 8 ? c : c - BM / 8) * 8;
-        int off = (row + place[c & 1]) * ld + chunk[c & 1] * 16 + t * kRowBytes;
-        if (last && half && chunk[c & 1] >= 4) off = kOut;
-        copy16(c < BM / 8 ? ca : cb, dst + c * 1024, off);
+    // A load of codes: 8 rows of 128 bytes, lane i the 16-byte chunk at place i % 8 of row i / 8.  Place p of row r
+    // holds chunk p ^ (r / 2 % 8): the 16 lanes that LDS serves at once, which want one chunk of different rows, then
+    // find it in 16 different bank groups.
+    const int place = lane >> 3, chunk = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
+    const int va = place * lda + chunk * 16, vb = place * ldb + chunk * 16;
+    const int ya = lane * lsa, yb = lane * lsb;
+    const int past = chunk >= 4 ? kOut : 0;   // of a last stage of 128 elements
+
+    struct Unit {   // a tile, or a part of its sums
+        __amdgpu_buffer_rsrc_t ca, cb, sa, sb;
+        int m0, n0, rows_m, rows_n, part, stages;
+        bool cut;   // the last stage has 128 elements
     };
-    auto copy_scales = [&](int c, uint8_t* dst, int t, bool last) {  // 32 rows of two words
-        const int ld = (int)(c < BM / 32 ? g.a.lds : g.b.lds), row = (c < BM / 32 ? c : c - BM / 32) * 32;
-        int off = (row + (lane >> 1)) * ld + (lane & 1) * 4 + t * 8;
-        if (last && half && (lane & 1)) off = kOut;
-        copy4(c < BM / 32 ? sa : sb, dst + T::kCodes + c * 256, off);
+    auto open = [&](uint32_t id) {   // 256 rows of at most I8MP_MAX_LD bytes: offsets and ranges fit 32 bits
+        Unit u;
+        u.part = __builtin_amdgcn_readfirstlane(id / tiles);
+        tile_of(id - u.part * tiles, tiles, tiles_m, tiles_n, u.m0, u.n0);
+        u.m0 *= BM;
+        u.n0 *= BN;
+        u.rows_m = all_m - u.m0 < BM ? all_m - u.m0 : BM;
+        u.rows_n = all_n - u.n0 < BN ? all_n - u.n0 : BN;
+        const int from = u.part * g.part_stages * kStageK, left = kp - from;
+        u.stages = (left + kStageK - 1) / kStageK < g.part_stages ? (left + kStageK - 1) / kStageK : g.part_stages;
+        u.cut = left < u.stages * kStageK;
+        // k = 0: one stage, of zeros, from empty ranges
+        u.stages = kp > 0 ? u.stages : 1;
+        const int codes = from / 2, scales = from / kMxBlock;
+        u.ca = range_of(g.a.codes + (int64_t)u.m0 * lda + codes, kp > 0 ? (u.rows_m - 1) * lda + kp / 2 - codes : 0);
+        u.cb = range_of(g.b.codes + (int64_t)u.n0 * ldb + codes, kp > 0 ? (u.rows_n - 1) * ldb + kp / 2 - codes : 0);
+        u.sa = range_of(g.a.scales + (int64_t)u.m0 * lsa + scales, kp > 0 ? (u.rows_m - 1) * lsa + kp / kMxBlock - scales : 0);
+        u.sb = range_of(g.b.scales + (int64_t)u.n0 * lsb + scales, kp > 0 ? (u.rows_n - 1) * lsb + kp / kMxBlock - scales : 0);
+        return u;
     };
-    auto fill = [&](int t) {
-        uint8_t* dst = smem + (t & 1) * T::kStage;
-        const bool last = t == stages - 1;
-#pragma unroll
-        for (int i = 0; i < T::kCopies; ++i) copy_codes(i * 4 + wave, dst, t, last);
-#pragma unroll
-        for (int i = 0; i < T::kScaleCopies; ++i) copy_scales(i * 4 + wave, dst, t, last);
-    };
-
-    v16f acc[FM][FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-    for (int j = threadIdx.x; j < BN; j += 256) bias[j] = g.bias && j < rows_n ? widen(g.bias, n0 + j, g.out_dtype) : 0.0f;
-
-    if (stages > 0) fill(0);
-    for (int t = 0; t < stages; ++t) {
-        __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): this wave's copies of stage t
-        __syncthreads();
-        if (t + 1 < stages) fill(t + 1);
-        const uint8_t* src = smem + (t & 1) * T::kStage;
-        int sx[FM], sw[FN];
-#pragma unroll
-        for (int i = 0; i < FM; ++i) sx[i] = *reinterpret_cast<const int*>(src + T::kCodes + ((wm + 32 * i + l32) * 2 + hi) * 4);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) sw[j] = *reinterpret_cast<const int*>(src + T::kCodes + ((BM + wn + 32 * j + l32) * 2 + hi) * 4);
-#define I8MP_STEP(s)                                                                                                  \
-    do {                                                                                                              \
-        v4i x[FM], w[FN];                                                                                             \
-        const int at = ((4 * hi + s) ^ ((l32 >> 1) & 7)) * 16;                                                        \
-        _Pragma("unroll") for (int i = 0; i < FM; ++i)                                                                \
-            x[i] = *reinterpret_cast<const v4i*>(src + (wm + 32 * i + l32) * kRowBytes + at);                         \
-        _Pragma("unroll") for (int j = 0; j < FN; ++j)                                                                \
-            w[j] = *reinterpret_cast<const v4i*>(src + (BM + wn + 32 * j + l32) * kRowBytes + at);                    \
-        _Pragma("unroll") for (int i = 0; i < FM; ++i)                                                                \
-            _Pragma("unroll") for (int j = 0; j < FN; ++j)                                                            \
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(w[j]), operand(x[i]), acc[i][j], \
-                                                                           4, 4, s, sw[j], s, sx[i]);                 \
-    } while (0)
-        I8MP_STEP(0);
-        I8MP_STEP(1);
-        I8MP_STEP(2);
-        I8MP_STEP(3);
-#undef I8MP_STEP
-    }
-    __syncthreads();   // the stages are free, the bias is there
-
-    // Sums (i, j, r): row wm + 32 i + l32, column wn + 32 j + 8 (r / 4) + 4 hi + r % 4.  They pass through the
-    // wave's part of LDS, 32 rows at a time, and leave as 16-byte pieces of whole rows.
-    constexpr int kElem = kType == I8MP_DTYPE_F32 ? 4 : 2, kPitch = 32 * FN * kElem + 16;
-    static_assert(4 * 32 * kPitch <= 2 * T::kStage, "the waves' rows fit the stages");
-    uint8_t* const area = smem + wave * 32 * kPitch;
-    const bool whole = g.ldout * kElem % 16 == 0 && reinterpret_cast<uintptr_t>(g.out) % 16 == 0;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int col = 32 * j + 8 * q + 4 * hi;
-                const v4f b = *reinterpret_cast<const v4f*>(bias + wn + col);
-                float v[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = acc[i][j][4 * q + r] + b[r];
-                uint8_t* p = area + l32 * kPitch + col * kElem;
-                if constexpr (kType == I8MP_DTYPE_F32) *reinterpret_cast<v4f*>(p) = v4f{v[0], v[1], v[2], v[3]};
-                else *reinterpret_cast<uint2*>(p) = make_uint2(narrow2<kType>(v[0], v[1]), narrow2<kType>(v[2], v[3]));
-            }
-        rows_done();
-        constexpr int kPieces = 32 * FN * kElem / 16, kEach = 16 / kElem;
-#pragma unroll
-        for (int u = 0; u < kPieces / 2; ++u) {
-            const int p = u * 64 + lane, row = p / kPieces, col = p % kPieces * kEach;
-            const int64_t r = wm + 32 * i + row, c = wn + col;
-            if (r >= rows_m || c >= rows_n) continue;
-            const uint8_t* from = area + row * kPitch + col * kElem;
-            uint8_t* to = static_cast<uint8_t*>(g.out) + ((m0 + r) * g.ldout + n0 + c) * kElem;
-            if (whole && c + kEach <= rows_n) {
-                __builtin_nontemporal_store(*reinterpret_cast<const v4u*>(from), reinterpret_cast<v4u*>(to));
-            } else {
-#pragma unroll
-                for (int e = 0; e < kEach; ++e) {
-                    if (c + e >= rows_n) break;
-                    if constexpr (kElem == 4) reinterpret_cast<uint32_t*>(to)[e] = reinterpret_cast<const uint32_t*>(from)[e];
-                    else reinterpret_cast<uint16_t*>(to)[e] = reinterpret_cast<const uint16_t*>(from)[e];
-                }
-            }
+    // Loads for stages past the last are out of range: every wait counts the same loads.
+    auto copy = [&](const Unit& u, int i, int t) {   // load i of this wave for stage t
+        uint8_t* const dst = smem + (t & 1) * T::kStage;
+        const int at = (t < u.stages ? t * kRowBytes : kOut) + (u.cut && t == u.stages - 1 ? past : 0);
+        if (i < BM / 32) {
+            const int c = i * 4 + wave;
+            copy16(u.ca, dst + c * 1024, va + at + c * 8 * lda);
+        } else {
+            const int c = (i - BM / 32) * 4 + wave;
+            copy16(u.cb, dst + BM * kRowBytes + c * 1024, vb + at + c * 8 * ldb);
         }
-        rows_done();
+    };
+    auto scales_at = [&](int t) { return smem + (t >> 1 & 1 ? kScale2At : T::kScaleAt); };
+    // Scales of stages t and t + 1 (t even), of a or of b: those of a go out one stage before they are read, those of b
+    // two, so that every stage issues as many loads.  Bytes past a row's end are its neighbour's, or zeros.
+    // Where rows are few some loads are made twice: the same bytes again.
+    auto copy_scales = [&](const Unit& u, bool of_b, int t) {
+        const int at = t < u.stages ? t * 8 : kOut;
+#pragma unroll
+        for (int i = 0; i < T::kScaleLoads; ++i) {
+            const int c = (i * 4 + wave) % (BM / 64), d = (i * 4 + wave) % (BN / 64);
+            copy16(of_b ? u.sb : u.sa, scales_at(t) + (of_b ? BM / 64 + d : c) * 1024,
+                   (of_b ? yb + d * 64 * lsb : ya + c * 64 * lsa) + at);
+        }
+    };
+    auto begin = [&](const Unit& u) {   // the loads of a tile's first two stages
+        copy_scales(u, false, 0);
+        copy_scales(u, true, 0);
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i) copy(u, i, 0);
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i) copy(u, i, 1);
+    };
+
+    v4i x[2][2][FM], w[2][2][FN];   // operands: half of the stage, step
+    int sx[2][FM], sw[2][FN];
+    const int row_x = wm + l32, row_w = BM + wn + l32, swz = l32 >> 1 & 7;
+    auto read = [&](int p, int h, int t) {
+        const uint8_t* const src = smem + (t & 1) * T::kStage + ((4 * p + 2 * hi + h) ^ swz) * 16;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) x[p][h][i] = *reinterpret_cast<const v4i*>(src + (row_x + 32 * i) * kRowBytes);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) w[p][h][j] = *reinterpret_cast<const v4i*>(src + (row_w + 32 * j) * kRowBytes);
+    };
+    // A second half that is not there has codes of zero; the first half's scales do for it.
+    auto read_scales = [&](const Unit& u, int p, int t) {
+        const uint8_t* const src = scales_at(t) + (t & 1) * 8 + (p == 1 && !(u.cut && t == u.stages - 1) ? 4 : 0) + 2 * hi;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sx[p][i] = *reinterpret_cast<const uint16_t*>(src + (row_x + 32 * i) * 16);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) sw[p][j] = *reinterpret_cast<const uint16_t*>(src + (row_w + 32 * j) * 16);
+    };
+    v16f acc[FM][FN];
+#define I8MP_MULTIPLY(p, h)                                                                                          \
+    _Pragma("unroll") for (int i = 0; i < FM; ++i)                                                                   \
+        _Pragma("unroll") for (int j = 0; j < FN; ++j)                                                               \
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(w[p][h][j]), operand(x[p][h][i]),    \
+                                                                       acc[i][j], 4, 4, h, sw[p][j], h, sx[p][i])
+
+    begin(open(blockIdx.x));
+    uint32_t turn = 0;
+    for (uint32_t id = blockIdx.x; id < units; id += gridDim.x, turn ^= 1) {
+        const Unit u = open(id);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = v16f{};
+        float* const tile_bias = bias + turn * BN;
+        for (int j = threadIdx.x; j < BN; j += 256) tile_bias[j] = g.bias && j < u.rows_n ? widen(g.bias, (int64_t)u.n0 + j, g.out_dtype) : 0.0f;
+        wait_loads<T::kLoads>();   // stage 0 has landed; no results pass where the second scales go any more
+        meet();
+        copy_scales(u, true, 2);
+        read(0, 0, 0);
+        read_scales(u, 0, 0);
+        read(0, 1, 0);
+        constexpr int kEarly = T::kLoads / 2;
+        int t = 0;
+        do {
+            // first quarter: read the second half
+            read(1, 0, t);
+            read_scales(u, 1, t);
+            read(1, 1, t);
+            I8MP_MULTIPLY(0, 0);
+#pragma unroll
+            for (int i = 0; i < FM + FN; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): this wave has read stage t
+            meet();
+            // second quarter: its place is free for stage t + 2
+            copy_scales(u, t & 1, t & 1 ? t + 3 : t + 2);
+#pragma unroll
+            for (int i = 0; i < kEarly; ++i) copy(u, i, t + 2);
+            I8MP_MULTIPLY(0, 1);
+#pragma unroll
+            for (int i = 0; i < kEarly + T::kScaleLoads; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x8, FM * FN > 8 ? 2 : 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            wait_loads<kEarly + T::kScaleLoads>();   // stage t + 1 has landed
+            meet();
+            // second half: read the next stage's first
+            read(0, 0, t + 1);
+            read_scales(u, 0, t + 1);
+            read(0, 1, t + 1);
+#pragma unroll
+            for (int i = kEarly; i < T::kLoads; ++i) copy(u, i, t + 2);
+            I8MP_MULTIPLY(1, 0);
+            I8MP_MULTIPLY(1, 1);
+#pragma unroll
+            for (int i = 0; i < 3 * (FM + FN) / 2; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < T::kLoads - kEarly; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, FM * FN > 8 ? 2 : 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        } while (++t < u.stages);
+        wait_loads<0>();   // none lands in what follows
+        meet();            // the stages are free
+        if (T::kAhead && id + gridDim.x < units) begin(open(id + gridDim.x));
+
+        // Sums (i, j, r): row wm + 32 i + l32, column wn + 32 j + 8 (r / 4) + 4 hi + r % 4.  They pass through the wave's
+        // part of LDS, 32 rows of kCols at a time, and leave as 16-byte pieces of whole lines.
+        constexpr int kElem = kType == I8MP_DTYPE_F32 ? 4 : 2;
+        constexpr int kTiles = T::kRowOut / kElem / 32 < FN ? T::kRowOut / kElem / 32 : FN, kCols = 32 * kTiles;
+        constexpr int kPitch = kCols * kElem + 16, kPieces = kCols * kElem / 16, kEach = 16 / kElem;
+        uint8_t* const out = static_cast<uint8_t*>(g.out) + u.part * g.part_bytes;
+        uint8_t* const area = smem + kOutAt + wave * T::kOutArea;
+        const bool whole = g.ldout * kElem % 16 == 0 && reinterpret_cast<uintptr_t>(g.out) % 16 == 0;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j0 = 0; j0 < FN; j0 += kTiles) {
+                // so many sums at a time leave the accumulation registers
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (T::kAhead) {
+#pragma unroll
+                    for (int j = 0; j < kTiles; ++j) asm volatile("" : "+a"(acc[i][j0 + j]));
+                }
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int col = 32 * j + 8 * q + 4 * hi;
+                        const v4f b = *reinterpret_cast<const v4f*>(tile_bias + wn + 32 * j0 + col);
+                        float v[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) v[r] = acc[i][j0 + j][4 * q + r] + b[r];
+                        uint8_t* p = area + l32 * kPitch + col * kElem;
+                        if constexpr (kType == I8MP_DTYPE_F32) *reinterpret_cast<v4f*>(p) = v4f{v[0], v[1], v[2], v[3]};
+                        else *reinterpret_cast<uint2*>(p) = make_uint2(narrow2<kType>(v[0], v[1]), narrow2<kType>(v[2], v[3]));
+                    }
+                rows_done();
+#pragma unroll
+                for (int v = 0; v < kPieces / 2; ++v) {
+                    const int p = v * 64 + lane, row = p / kPieces, col = p % kPieces * kEach;
+                    const int r = wm + 32 * i + row, c = wn + 32 * j0 + col;
+                    if (r >= u.rows_m || c >= u.rows_n) continue;
+                    const uint8_t* from = area + row * kPitch + col * kElem;
+                    uint8_t* to = out + ((int64_t)(u.m0 + r) * g.ldout + u.n0 + c) * kElem;
+                    if (whole && c + kEach <= u.rows_n) {
+                        *reinterpret_cast<v4u*>(to) = *reinterpret_cast<const v4u*>(from);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e) {
+                            if (c + e >= u.rows_n) break;
+                            if constexpr (kElem == 4) reinterpret_cast<uint32_t*>(to)[e] = reinterpret_cast<const uint32_t*>(from)[e];
+                            else reinterpret_cast<uint16_t*>(to)[e] = reinterpret_cast<const uint16_t*>(from)[e];
+                        }
+                    }
+                }
+                rows_done();
+            }
+        if constexpr (!T::kAhead) break;   // as many workgroups as units
+    }
+#undef I8MP_MULTIPLY
+}
+
+// out = sum over parts + bias, parts in order; four columns a lane
+template <int kType>
+__global__ __launch_bounds__(256) void mx4_join_kernel(MxGemmArgs g, const float* part, int64_t ldp) {
+    const int64_t quads = ldp / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t r = i / quads, c = (i - r * quads) * 4;
+    if (r >= g.a.rows) return;
+    const float* p = part + r * ldp + c;
+    v4f v = *reinterpret_cast<const v4f*>(p);
+    for (int q = 1; q < g.parts; ++q) v += *reinterpret_cast<const v4f*>(p + q * g.part_bytes / 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (c + e >= g.b.rows) break;
+        const float x = g.bias ? v[e] + widen(g.bias, c + e, kType) : v[e];
+        const int64_t at = r * g.ldout + c + e;
+        if constexpr (kType == I8MP_DTYPE_F32) static_cast<float*>(g.out)[at] = x;
+        else static_cast<half_bits*>(g.out)[at] = (half_bits)narrow2<kType>(x, 0.0f);
     }
 }
 
-template <int FM, int FN>
-hipError_t launch(const MxGemmArgs& g, hipStream_t stream) {
-    using T = Tile<FM, FN>;
-    const dim3 grid((unsigned)(ceil_div(g.a.rows, T::BM) * ceil_div(g.b.rows, T::BN)));
-    if (g.out_dtype == I8MP_DTYPE_F32) hipLaunchKernelGGL((mx4_gemm_kernel<FM, FN, I8MP_DTYPE_F32>), grid, dim3(256), 0, stream, g);
-    else if (g.out_dtype == I8MP_DTYPE_F16) hipLaunchKernelGGL((mx4_gemm_kernel<FM, FN, I8MP_DTYPE_F16>), grid, dim3(256), 0, stream, g);
-    else hipLaunchKernelGGL((mx4_gemm_kernel<FM, FN, I8MP_DTYPE_BF16>), grid, dim3(256), 0, stream, g);
+template <int F, int kType>
+hipError_t launch_tiles(const MxGemmArgs& g, hipStream_t stream) {
+    using T = Tile<F, F>;
+    const int64_t units = ceil_div(g.a.rows, T::BM) * ceil_div(g.b.rows, T::BN) * g.parts;
+    const dim3 grid((unsigned)(T::kAhead && units > kCUs ? kCUs : units));
+    hipLaunchKernelGGL((mx4_gemm_kernel<F, F, kType>), grid, dim3(256), 0, stream, g);
     return hipGetLastError();
 }
+template <int F>
+hipError_t launch_type(const MxGemmArgs& g, hipStream_t stream) {
+    return g.out_dtype == I8MP_DTYPE_F32   ? launch_tiles<F, I8MP_DTYPE_F32>(g, stream)
+           : g.out_dtype == I8MP_DTYPE_F16 ? launch_tiles<F, I8MP_DTYPE_F16>(g, stream)
+                                           : launch_tiles<F, I8MP_DTYPE_BF16>(g, stream);
+}
+hipError_t launch_one(int f, const MxGemmArgs& g, hipStream_t stream) {
+    return f == 4 ? launch_type<4>(g, stream) : f == 2 ? launch_type<2>(g, stream) : launch_type<1>(g, stream);
+}
+
+// ---- which tiles -----------------------------------------------------------------
+// A cost model in us, fitted to timed products: a tile of 64 f costs a fixed time, and
+// a time a stage that depends on how many of them share a CU.
+//   f   rows    a CU holds   fixed   a stage, with 1 .. of them on a CU
+//   4   256     1            10      1.75
+//   2   128     2            5       0.65  1.45
+//   1   64      4            3.5     0.44  0.62  0.9  1.2
+constexpr int kShapes[3] = {4, 2, 1};
+double stage_us(int f, int64_t on_cu) {
+    static const double t4[] = {1.75}, t2[] = {0.65, 1.45}, t1[] = {0.44, 0.62, 0.9, 1.2};
+    return (f == 4 ? t4 : f == 2 ? t2 : t1)[on_cu - 1];
+}
+double tiles_us(int f, int64_t units, int64_t stages) {
+    const int64_t hold = f == 4 ? 1 : f == 2 ? 2 : 4;
+    const double fixed = f == 4 ? 10.0 : f == 2 ? 5.0 : 3.5;
+    const int64_t full = units / (kCUs * hold), rest = ceil_div(units - full * kCUs * hold, kCUs);
+    return full * (fixed + stages * stage_us(f, hold)) + (rest ? fixed + stages * stage_us(f, rest) : 0.0);
+}
+
+struct Cut {   // of a product's columns: one tile shape, sums in `parts` parts of `part_stages`
+    int f, parts;
+    int64_t part_stages;
+    double us;
+};
+// Sums are split over k where tiles alone leave CUs idle: the parts, in fp32, pass through the workspace, and a second
+// launch adds them.
+Cut best_cut(int64_t m, int64_t n, int64_t k) {
+    const int64_t stages = ceil_div(k, kStageK) > 0 ? ceil_div(k, kStageK) : 1;
+    Cut best{1, 1, stages, 1e300};
+    for (int f : kShapes) {
+        const int64_t tiles = ceil_div(m, 64 * f) * ceil_div(n, 64 * f);
+        for (int parts = 1; parts <= 16 && parts <= stages; ++parts) {
+            const int64_t per = ceil_div(stages, parts);
+            if (ceil_div(stages, per) != parts) continue;
+            if (parts > 1 && tiles * parts > 4 * kCUs) break;
+            double us = tiles_us(f, tiles * parts, per);
+            if (parts > 1) us += 4.0 + (double)m * n * 8 * parts / 4.0e6;   // written and read at 4 TB/s
+            if (us < best.us) best = Cut{f, parts, per, us};
+        }
+    }
+    return best;
+}
+// A product too large for one round may take whole rounds of 256 x 256 tiles for its first columns and another cut for
+// the rest, in a second launch.
+struct Plan {
+    int64_t n_main;   // 0: all columns by `rest`
+    Cut rest;
+};
+Plan plan(int64_t m, int64_t n, int64_t k) {
+    Plan p{0, best_cut(m, n, k)};
+    const int64_t rows = ceil_div(m, 256), rounds = rows * ceil_div(n, 256) / kCUs, cols = rounds * kCUs / rows;
+    const int64_t n_main = cols * 256, stages = ceil_div(k, kStageK);
+    if (cols > 0 && n_main < n) {
+        const Cut rest = best_cut(m, n - n_main, k);
+        if (tiles_us(4, rows * cols, stages) + 3.0 + rest.us < 0.98 * p.rest.us) p = Plan{n_main, rest};
+    }
+    return p;
+}
+int64_t part_row(int64_t n) { return round_up(n, 4); }
 
 }  // namespace
 
-size_t mx4_gemm_workspace(int64_t, int64_t, int64_t) { return 0; }
+size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k) {
+    if (m <= 0 || n <= 0) return 0;
+    const Plan p = plan(m, n, k);
+    return p.rest.parts > 1 ? (size_t)p.rest.parts * m * part_row(n - p.n_main) * 4 : 0;
+}
 
-hipError_t launch_mx4_gemm(const MxGemmArgs& g, hipStream_t stream) {
-    const auto tiles = [&](int64_t bm, int64_t bn) { return ceil_div(g.a.rows, bm) * ceil_div(g.b.rows, bn); };
-    if (tiles(256, 256) >= 200) return launch<4, 4>(g, stream);
-    if (tiles(128, 128) >= 200) return launch<2, 2>(g, stream);
-    return launch<1, 1>(g, stream);
+hipError_t launch_mx4_gemm(const MxGemmArgs& args, hipStream_t stream) {
+    const int64_t m = args.a.rows, n = args.b.rows, k = args.a.k, elem = args.out_dtype == I8MP_DTYPE_F32 ? 4 : 2;
+    const Plan p = plan(m, n, k);
+    MxGemmArgs g = args;
+    g.parts = 1;
+    g.part_stages = (int)ceil_div(k, kStageK);
+    g.part_bytes = 0;
+    if (p.n_main > 0) {
+        g.b.rows = p.n_main;
+        if (hipError_t e = launch_one(4, g, stream); e != hipSuccess) return e;
+        g.b.rows = n - p.n_main;
+        g.b.codes += p.n_main * g.b.ldc;
+        g.b.scales += p.n_main * g.b.lds;
+        g.out = static_cast<uint8_t*>(g.out) + p.n_main * elem;
+        if (g.bias) g.bias = static_cast<const uint8_t*>(g.bias) + p.n_main * elem;
+    }
+    if (p.rest.parts == 1) return launch_one(p.rest.f, g, stream);
+    const int64_t ldp = part_row(g.b.rows);
+    MxGemmArgs s = g;   // the parts
+    s.out = g.part;
+    s.out_dtype = I8MP_DTYPE_F32;
+    s.ldout = ldp;
+    s.bias = nullptr;
+    s.parts = g.parts = p.rest.parts;
+    s.part_stages = (int)p.rest.part_stages;
+    s.part_bytes = g.part_bytes = m * ldp * 4;
+    if (hipError_t e = launch_one(p.rest.f, s, stream); e != hipSuccess) return e;
+    const dim3 grid((unsigned)ceil_div(m * ldp / 4, 256));
+    if (g.out_dtype == I8MP_DTYPE_F32) hipLaunchKernelGGL((mx4_join_kernel<I8MP_DTYPE_F32>), grid, dim3(256), 0, stream, g, g.part, ldp);
+    else if (g.out_dtype == I8MP_DTYPE_F16) hipLaunchKernelGGL((mx4_join_kernel<I8MP_DTYPE_F16>), grid, dim3(256), 0, stream, g, g.part, ldp);
+    else hipLaunchKernelGGL((mx4_join_kernel<I8MP_DTYPE_BF16>), grid, dim3(256), 0, stream, g, g.part, ldp);
+    return hipGetLastError();
 }
 
 }  // namespace i8mp
