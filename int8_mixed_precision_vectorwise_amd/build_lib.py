@@ -21,7 +21,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libi8mp.so")
 
 SOURCES = ["api.hip", "quant.hip", "gemm.hip", "decode.hip", "dequant.hip", "backward.hip", "fp4.hip",
-           "kvcache.hip", "attention.hip", "attention_bf16.hip", "mx4.hip", "mx4_gemm.hip"]
+           "kvcache.hip", "attention.hip", "attention_bf16.hip", "mx4.hip", "mx4_gemm.hip", "mx4_decode.hip"]
 
 # -packed-fp32-ops: no v_pk_*_f32 generation.  Correctly rounded fp32 division:
 # the quantizer's 127/absmax must be the IEEE quotient.  No fast-math anywhere.

@@ -997,6 +997,11 @@ i8mp_status i8mp_mx4_linear(const void* x, int32_t dtype, int64_t m, int64_t ldx
     g.out = out;
     g.ldout = ldout;
     g.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + at);
+    if (mx4_decode_quantizes(m, k, x, ldx)) {
+        g.x = static_cast<const half_bits*>(x);
+        g.ldx = ldx;
+        return launched(launch_mx4_decode(g, stream));
+    }
     if (k > 0)
         if (i8mp_status s = launched(launch_mx4_quantize(mx4_quant(x, ldx, dtype, false, g.a), stream)); s != I8MP_OK) return s;
     return launched(launch_mx4_gemm(g, stream));

@@ -36,6 +36,7 @@ struct MxGemmArgs {
     const void* bias;               // nullable, [b.rows] of out's type
     int32_t out_dtype;
     void* out; int64_t ldout;
+    const half_bits* x; int64_t ldx;  // launch_mx4_decode: if given, a's 16-bit form, quantized on the way
     float* part;                    // workspace of mx4_gemm_workspace() bytes
     // set by the launcher: the sums over k in so many parts of so many stages, each with an output of its own
     int32_t parts, part_stages;
@@ -47,5 +48,11 @@ hipError_t launch_mx4_dequantize(const MxDequantArgs& a, hipStream_t stream);
 // workspace of a product of these sizes (0: none needed)
 size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k);
 hipError_t launch_mx4_gemm(const MxGemmArgs& g, hipStream_t stream);
+// The product of a few rows, where mx4_decode_fits: the weights streamed through the matrix cores.  x in place of a's
+// codes (and of out's type) where mx4_decode_quantizes.
+constexpr int kMxDecodeRows = 16;
+bool mx4_decode_fits(int64_t m, int64_t k);
+bool mx4_decode_quantizes(int64_t m, int64_t k, const void* x, int64_t ldx);
+hipError_t launch_mx4_decode(const MxGemmArgs& g, hipStream_t stream);
 
 }  // namespace i8mp

@@ -13,6 +13,7 @@
 // element in, 17/32 of a byte out.
 #include "common.h"
 #include "mx4.h"
+#include "mx4_util.h"
 #include "quant_util.h"
 
 namespace i8mp {
@@ -21,43 +22,9 @@ namespace {
 
 constexpr int kThreads = 256;
 
-typedef unsigned short us2 __attribute__((ext_vector_type(2)));
-typedef _Float16 hh2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bb2 __attribute__((ext_vector_type(2)));
-typedef float f2 __attribute__((ext_vector_type(2)));
 // at any element's address
 typedef v4u v4u_any __attribute__((aligned(2)));
 typedef uint32_t u32_any __attribute__((aligned(2)));
-
-// the scale's byte from the bits of the largest magnitude
-template <bool kBf16>
-__device__ inline uint32_t scale_byte(uint32_t top) {
-    // fp16's subnormal numbers are normal in fp32; bfloat16's get the least scale
-    const uint32_t bits = kBf16 ? top << 16 : __float_as_uint(h2f((half_bits)top));
-    const uint32_t e = bits >> 23;
-    return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
-}
-
-// 2^(byte - 127); 255 gives a NaN
-__device__ inline float scale_value(uint32_t byte) {
-    return __uint_as_float(byte == 0u ? 0x00400000u : byte == 255u ? 0x7fc00000u : byte << 23);
-}
-
-__device__ inline us2 mags(uint32_t w) { return __builtin_bit_cast(us2, w & 0x7fff7fffu); }
-
-// byte kSel of `old` := codes of a pair of 16-bit values
-template <bool kBf16, int kSel>
-__device__ inline uint32_t encode2(uint32_t old, uint32_t w, float scale) {
-    if constexpr (kBf16) return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(bb2, w), scale, kSel);
-    else return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, __builtin_bit_cast(hh2, w), scale, kSel);
-}
-template <bool kBf16>
-__device__ inline uint32_t encode8(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, float scale) {
-    uint32_t c = encode2<kBf16, 0>(0u, w0, scale);
-    c = encode2<kBf16, 1>(c, w1, scale);
-    c = encode2<kBf16, 2>(c, w2, scale);
-    return encode2<kBf16, 3>(c, w3, scale);
-}
 
 // ---- by rows ------------------------------------------------------------------
 // A lane has 8 neighbouring elements, four lanes a block.  A workgroup is

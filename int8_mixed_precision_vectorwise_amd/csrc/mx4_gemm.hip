@@ -38,42 +38,19 @@
 // below, 8192 x 8192 x 16384 506 us (4.3 PFLOP/s).
 #include "common.h"
 #include "mx4.h"
+#include "mx4_util.h"
 
 namespace i8mp {
 
 namespace {
 
-typedef int v8i __attribute__((ext_vector_type(8)));
-
 constexpr int kStageK = 256;             // elements of a stage
 constexpr int kRowBytes = kStageK / 2;   // its codes of a row: whole lines of the L2
 constexpr int kXcds = 8, kCUs = 256;
-constexpr int kOut = (int)0x80000000;    // makes a buffer offset leave every range: reads zeros
 
-__device__ inline __amdgpu_buffer_rsrc_t range_of(const void* base, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
-}
-
-// lane i's 16 or 4 bytes at `offset` land at lds + 16 i or 4 i (lds is the same in every lane)
+// lane i's 16 bytes at `offset` land at lds + 16 i (lds is the same in every lane)
 __device__ inline void copy16(__amdgpu_buffer_rsrc_t src, uint8_t* lds, int offset) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)lds, 16, offset, 0, 0, 0);
-}
-__device__ inline void copy4(__amdgpu_buffer_rsrc_t src, uint8_t* lds, int offset) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)lds, 4, offset, 0, 0, 0);
-}
-
-__device__ inline v8i operand(const v4i& x) { return __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1); }
-
-__device__ inline float widen(const void* p, int64_t i, int dtype) {
-    if (dtype == I8MP_DTYPE_F32) return static_cast<const float*>(p)[i];
-    const half_bits h = static_cast<const half_bits*>(p)[i];
-    return dtype == I8MP_DTYPE_BF16 ? __uint_as_float((uint32_t)h << 16) : h2f(h);
-}
-template <int kType>
-__device__ inline uint32_t narrow2(float x, float y) {
-    if constexpr (kType == I8MP_DTYPE_BF16)
-        return __builtin_bit_cast(half_bits, (__bf16)x) | (uint32_t)__builtin_bit_cast(half_bits, (__bf16)y) << 16;
-    else return f2h(x) | (uint32_t)f2h(y) << 16;
 }
 
 // accesses of LDS by the lanes of one wave stay on their side (LDS serves a wave in order)
@@ -463,12 +440,13 @@ int64_t part_row(int64_t n) { return round_up(n, 4); }
 }  // namespace
 
 size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k) {
-    if (m <= 0 || n <= 0) return 0;
+    if (m <= 0 || n <= 0 || mx4_decode_fits(m, k)) return 0;
     const Plan p = plan(m, n, k);
     return p.rest.parts > 1 ? (size_t)p.rest.parts * m * part_row(n - p.n_main) * 4 : 0;
 }
 
 hipError_t launch_mx4_gemm(const MxGemmArgs& args, hipStream_t stream) {
+    if (mx4_decode_fits(args.a.rows, args.a.k)) return launch_mx4_decode(args, stream);
     const int64_t m = args.a.rows, n = args.b.rows, k = args.a.k, elem = args.out_dtype == I8MP_DTYPE_F32 ? 4 : 2;
     const Plan p = plan(m, n, k);
     MxGemmArgs g = args;
