@@ -925,7 +925,13 @@ bool mx4_sizes(int64_t m, int64_t n, int64_t k) {
 bool mx4_fits(int64_t k) { return Mx4{nullptr, 0, nullptr, 0, 0, k}.kp() / 2 <= I8MP_MAX_LD; }  // as a row's length
 
 MxQuantArgs mx4_quant(const void* x, int64_t ldx, int32_t dtype, bool columns, const Mx4& q) {
-    return MxQuantArgs{static_cast<const half_bits*>(x), ldx, dtype == I8MP_DTYPE_BF16, columns, q};
+    MxQuantArgs a{};
+    a.x = static_cast<const half_bits*>(x);
+    a.ldx = ldx;
+    a.bf16 = dtype == I8MP_DTYPE_BF16;
+    a.columns = columns;
+    a.q = q;
+    return a;
 }
 bool any_type(int32_t dtype) { return half_type(dtype) || dtype == I8MP_DTYPE_F32; }
 }  // namespace
@@ -938,7 +944,8 @@ i8mp_status i8mp_mx4_quantize(const void* x, int32_t dtype, int64_t m, int64_t k
     if (m == 0 || k == 0) return I8MP_OK;
     if (!x || !mx4_data(q)) return I8MP_EINVAL;
     if (i8mp_status s = check_device(); s != I8MP_OK) return s;
-    return launched(launch_mx4_quantize(mx4_quant(x, ldx, dtype, columns != 0, q), stream));
+    const MxQuantArgs job = mx4_quant(x, ldx, dtype, columns != 0, q);
+    return launched(launch_mx4_quantize(&job, 1, stream));
 }
 
 i8mp_status i8mp_mx4_dequantize(const i8mp_mx4* a, int32_t out_dtype, void* out, int64_t ldout, hipStream_t stream) {
@@ -1002,8 +1009,8 @@ i8mp_status i8mp_mx4_linear(const void* x, int32_t dtype, int64_t m, int64_t ldx
         g.ldx = ldx;
         return launched(launch_mx4_decode(g, stream));
     }
-    if (k > 0)
-        if (i8mp_status s = launched(launch_mx4_quantize(mx4_quant(x, ldx, dtype, false, g.a), stream)); s != I8MP_OK) return s;
+    const MxQuantArgs job = mx4_quant(x, ldx, dtype, false, g.a);
+    if (i8mp_status s = launched(launch_mx4_quantize(&job, 1, stream)); s != I8MP_OK) return s;
     return launched(launch_mx4_gemm(g, stream));
 }
 
@@ -1038,12 +1045,18 @@ i8mp_status i8mp_mx4_linear_backward(const void* grad_out, int64_t ldg, const vo
     MxGemmArgs g{};
     g.out_dtype = dtype;
     g.part = reinterpret_cast<float*>(base + at);
-    const auto quantize = [&](const void* p, int64_t ld, bool columns, const Mx4& q) {
-        return q.rows > 0 && q.k > 0 ? launch_mx4_quantize(mx4_quant(p, ld, dtype, columns, q), stream) : hipSuccess;
-    };
+    MxQuantArgs jobs[kMxJobs];
+    int count = 0;
     if (want_x) {
-        if (i8mp_status s = launched(quantize(grad_out, ldg, false, g_rows)); s != I8MP_OK) return s;
-        if (i8mp_status s = launched(quantize(w, ldw, true, w_cols)); s != I8MP_OK) return s;
+        jobs[count++] = mx4_quant(grad_out, ldg, dtype, false, g_rows);
+        jobs[count++] = mx4_quant(w, ldw, dtype, true, w_cols);
+    }
+    if (want_w) {
+        jobs[count++] = mx4_quant(grad_out, ldg, dtype, true, g_cols);
+        jobs[count++] = mx4_quant(x, ldx, dtype, true, x_cols);
+    }
+    if (i8mp_status s = launched(launch_mx4_quantize(jobs, count, stream)); s != I8MP_OK) return s;
+    if (want_x) {
         g.a = g_rows;
         g.b = w_cols;
         g.out = grad_x;
@@ -1051,8 +1064,6 @@ i8mp_status i8mp_mx4_linear_backward(const void* grad_out, int64_t ldg, const vo
         if (i8mp_status s = launched(launch_mx4_gemm(g, stream)); s != I8MP_OK) return s;
     }
     if (want_w) {
-        if (i8mp_status s = launched(quantize(grad_out, ldg, true, g_cols)); s != I8MP_OK) return s;
-        if (i8mp_status s = launched(quantize(x, ldx, true, x_cols)); s != I8MP_OK) return s;
         g.a = g_cols;
         g.b = x_cols;
         g.out = grad_w;

@@ -23,6 +23,15 @@ struct MxQuantArgs {
     bool bf16;
     bool columns;
     Mx4 q;
+    // set by the launcher
+    bool aligned;                   // x can be read in whole words
+    int32_t lane_shift;             // by rows: lanes along a row
+    uint32_t block0, blocks_x;      // first workgroup, workgroups along a row of them
+};
+constexpr int kMxJobs = 4;
+struct MxQuantJobs {
+    MxQuantArgs job[kMxJobs];
+    int32_t count;
 };
 
 struct MxDequantArgs {
@@ -43,7 +52,8 @@ struct MxGemmArgs {
     int64_t part_bytes;
 };
 
-hipError_t launch_mx4_quantize(const MxQuantArgs& a, hipStream_t stream);
+// Up to kMxJobs matrices of one type, in one launch; empty ones are passed over.
+hipError_t launch_mx4_quantize(const MxQuantArgs* args, int count, hipStream_t stream);
 hipError_t launch_mx4_dequantize(const MxDequantArgs& a, hipStream_t stream);
 // workspace of a product of these sizes (0: none needed)
 size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k);

@@ -27,17 +27,17 @@ typedef v4u v4u_any __attribute__((aligned(2)));
 typedef uint32_t u32_any __attribute__((aligned(2)));
 
 // ---- by rows ------------------------------------------------------------------
-// A lane has 8 neighbouring elements, four lanes a block.  A workgroup is
-// kThreads / lanes rows of `lanes` chunks at a time, and takes kRowSteps of them:
-// as many 16-byte loads in flight a lane.
+// A lane has 8 neighbouring elements, four lanes a block, sixteen a word of scales.  A
+// workgroup is kThreads / lanes rows of `lanes` chunks at a time, and takes kRowSteps of
+// them: as many 16-byte loads in flight a lane.
 constexpr int kRowSteps = 4;
 
 template <bool kBf16, bool kAligned>
-__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(MxQuantArgs a, int lane_shift) {
-    const int lanes = 1 << lane_shift, rows = kThreads >> lane_shift;
-    const int64_t c = (int64_t)blockIdx.x * lanes + (threadIdx.x & (lanes - 1));  // chunk of 8 elements
-    const int64_t row0 = (int64_t)blockIdx.y * (rows * kRowSteps) + (threadIdx.x >> lane_shift);
-    if (c * 8 >= a.q.kp()) return;  // whole blocks leave: kp is a multiple of 128
+__device__ inline void quantize_rows(const MxQuantArgs& a, uint32_t bx, uint32_t by) {
+    const int lanes = 1 << a.lane_shift, rows = kThreads >> a.lane_shift;
+    const int64_t c = (int64_t)bx * lanes + (threadIdx.x & (lanes - 1));  // chunk of 8 elements
+    const int64_t row0 = (int64_t)by * (rows * kRowSteps) + (threadIdx.x >> a.lane_shift);
+    if (c * 8 >= a.q.kp()) return;  // whole words of scales leave: kp is a multiple of 128
     const int64_t left = a.q.k - c * 8;
     v4u x[kRowSteps];
 #pragma unroll
@@ -69,7 +69,10 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(MxQuantArgs a, 
         uint32_t codes = encode8<kBf16>(x[i][0], x[i][1], x[i][2], x[i][3], scale_value(byte));
         if (byte == 255u) codes = 0;
         *reinterpret_cast<uint32_t*>(a.q.codes + r * a.q.ldc + c * 4) = codes;
-        if ((threadIdx.x & 3) == 0) a.q.scales[r * a.q.lds + (c >> 2)] = (uint8_t)byte;
+        uint32_t word = byte << (8 * (threadIdx.x >> 2 & 3));   // four blocks' bytes meet
+        word |= (uint32_t)dpp_i32<kDppHalfMirror>((int32_t)word);
+        word |= (uint32_t)dpp_i32<kDppRowMirror>((int32_t)word);
+        if ((threadIdx.x & 15) == 0) *reinterpret_cast<uint32_t*>(a.q.scales + r * a.q.lds + (c >> 2)) = word;
     }
 }
 
@@ -77,27 +80,37 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(MxQuantArgs a, 
 // x [k x rows] read as it lies, its transpose quantized: a block is 32 rows of one
 // column.  A wave has 32 rows of 128 columns, a lane two columns: the block's
 // maximum needs no other lane, and 32 loads of 4 bytes are in flight a lane.  The
-// codes (16 bytes a column) meet in LDS, so that a column leaves as kWaves * 16
-// contiguous bytes.
-constexpr int kColCols = 128;
+// codes (16 bytes a column) meet in LDS, so that a column leaves as 64 contiguous
+// bytes.
+constexpr int kColCols = 128, kColRows = 32 * kThreads / 64, kColPitch = kColRows / 2 + 16;
 
-template <bool kBf16, int kWaves>
-__global__ __launch_bounds__(64 * kWaves) void quantize_columns_kernel(MxQuantArgs a) {
-    constexpr int kPitch = kWaves * 16 + 16;
-    __shared__ __attribute__((aligned(16))) uint8_t codes[kColCols * kPitch];
-    __shared__ __attribute__((aligned(16))) uint8_t scales[kColCols * kWaves];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c0 = (int64_t)blockIdx.x * kColCols, c = c0 + 2 * lane;
-    const int64_t r0 = ((int64_t)blockIdx.y * kWaves + wave) * kMxBlock;
+template <bool kBf16, bool kAligned>
+__device__ inline void quantize_columns(const MxQuantArgs& a, uint32_t bx, uint32_t by, uint8_t* codes, uint32_t* scales) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t c0 = (int64_t)bx * kColCols, c = c0 + 2 * lane;
+    const int64_t r0 = (int64_t)by * kColRows + wave * kMxBlock;
     uint32_t x[kMxBlock];
     const half_bits* p = a.x + r0 * a.ldx + c;
     const bool two = c + 1 < a.q.rows, one = c < a.q.rows;
+    if constexpr (kAligned) {   // rows past the last are out of range, and read as zeros
+        const int64_t there = a.q.k - r0 < kMxBlock ? a.q.k - r0 : kMxBlock;
+        const int ld = (int)a.ldx * 2, range = there > 0 ? ((int)there - 1) * ld + (int)(a.q.rows - c0 < kColCols ? a.q.rows - c0 : kColCols) * 2 : 0;
+        const __amdgpu_buffer_rsrc_t src = range_of(a.x + r0 * a.ldx + c0, __builtin_amdgcn_readfirstlane(range));
+        const int at = two ? lane * 4 : kOut;
 #pragma unroll
-    for (int i = 0; i < kMxBlock; ++i) {
-        x[i] = 0;
-        if (r0 + i >= a.q.k) continue;
-        if (two) x[i] = *reinterpret_cast<const u32_any*>(p + i * a.ldx);
-        else if (one) x[i] = p[i * a.ldx];
+        for (int i = 0; i < kMxBlock; ++i) x[i] = __builtin_amdgcn_raw_buffer_load_b32(src, at + i * ld, 0, 0);
+        if (one && !two) {
+#pragma unroll
+            for (int i = 0; i < kMxBlock; ++i) x[i] = r0 + i < a.q.k ? p[i * a.ldx] : 0;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kMxBlock; ++i) {
+            x[i] = 0;
+            if (r0 + i >= a.q.k) continue;
+            if (two) x[i] = *reinterpret_cast<const u32_any*>(p + i * a.ldx);
+            else if (one) x[i] = p[i * a.ldx];
+        }
     }
     us2 m = mags(x[0]);
 #pragma unroll
@@ -117,23 +130,41 @@ __global__ __launch_bounds__(64 * kWaves) void quantize_columns_kernel(MxQuantAr
         k0[i] = b0 == 255u ? 0u : encode8<kBf16>(lo[0], lo[1], lo[2], lo[3], s0);
         k1[i] = b1 == 255u ? 0u : encode8<kBf16>(hi[0], hi[1], hi[2], hi[3], s1);
     }
-    *reinterpret_cast<v4u*>(codes + 2 * lane * kPitch + wave * 16) = k0;
-    *reinterpret_cast<v4u*>(codes + (2 * lane + 1) * kPitch + wave * 16) = k1;
-    scales[2 * lane * kWaves + wave] = (uint8_t)b0;
-    scales[(2 * lane + 1) * kWaves + wave] = (uint8_t)b1;
+    constexpr int kWaves = kThreads / 64;
+    static_assert(kWaves == 4, "a word of scales a column");
+    *reinterpret_cast<v4u*>(codes + 2 * lane * kColPitch + wave * 16) = k0;
+    *reinterpret_cast<v4u*>(codes + (2 * lane + 1) * kColPitch + wave * 16) = k1;
+    reinterpret_cast<uint8_t*>(scales)[2 * lane * kWaves + wave] = (uint8_t)b0;
+    reinterpret_cast<uint8_t*>(scales)[(2 * lane + 1) * kWaves + wave] = (uint8_t)b1;
     __syncthreads();
-    const int64_t blocks = a.q.kp() / kMxBlock, first = (int64_t)blockIdx.y * kWaves;
-    for (int t = threadIdx.x; t < kColCols * kWaves; t += 64 * kWaves) {
+    const int64_t first = (int64_t)by * kWaves;   // all four blocks are there: kp is a multiple of 128
+#pragma unroll
+    for (int t = threadIdx.x; t < kColCols * kWaves; t += kThreads) {
         const int col = t / kWaves, part = t % kWaves;
-        if (c0 + col < a.q.rows && first + part < blocks)
+        if (c0 + col < a.q.rows)
             *reinterpret_cast<v4u*>(a.q.codes + (c0 + col) * a.q.ldc + (first + part) * 16) =
-                *reinterpret_cast<const v4u*>(codes + col * kPitch + part * 16);
+                *reinterpret_cast<const v4u*>(codes + col * kColPitch + part * 16);
     }
-    for (int t = threadIdx.x; t < kColCols * kWaves / 4; t += 64 * kWaves) {
-        const int col = t / (kWaves / 4), part = t % (kWaves / 4) * 4;
-        if (c0 + col < a.q.rows && first + part < blocks)
-            *reinterpret_cast<uint32_t*>(a.q.scales + (c0 + col) * a.q.lds + first + part) =
-                *reinterpret_cast<const uint32_t*>(scales + col * kWaves + part);
+    if (threadIdx.x < kColCols && c0 + threadIdx.x < a.q.rows)
+        *reinterpret_cast<uint32_t*>(a.q.scales + (c0 + threadIdx.x) * a.q.lds + first) = scales[threadIdx.x];
+}
+
+// Up to kMxJobs matrices in one launch: each has its run of workgroups.
+template <bool kBf16>
+__global__ __launch_bounds__(kThreads) void quantize_kernel(MxQuantJobs jobs) {
+    __shared__ __attribute__((aligned(16))) uint8_t codes[kColCols * kColPitch];
+    __shared__ uint32_t scales[kColCols];
+    int j = 0;
+#pragma unroll
+    for (int i = 1; i < kMxJobs; ++i) j += i < jobs.count && blockIdx.x >= jobs.job[i].block0;
+    const MxQuantArgs& a = jobs.job[j];
+    const uint32_t id = blockIdx.x - a.block0, by = id / a.blocks_x, bx = id - by * a.blocks_x;
+    if (a.columns) {
+        if (a.aligned) quantize_columns<kBf16, true>(a, bx, by, codes, scales);
+        else quantize_columns<kBf16, false>(a, bx, by, codes, scales);
+    } else {
+        if (a.aligned) quantize_rows<kBf16, true>(a, bx, by);
+        else quantize_rows<kBf16, false>(a, bx, by);
     }
 }
 
@@ -228,36 +259,54 @@ hipError_t by_rows(int64_t rows, int64_t chunks, F launch) {
     return hipSuccess;
 }
 
-template <bool kBf16>
-hipError_t quantize(const MxQuantArgs& args, hipStream_t stream) {
-    if (args.columns) {
-        const bool tall = args.q.k > kMxPad;
-        const int64_t most = (int64_t)65535 * (tall ? 256 : 128);  // rows of x a launch
-        for (int64_t r = 0; r < args.q.k; r += most) {
-            MxQuantArgs a = args;
-            a.x += r * a.ldx;
-            a.q.codes += r / 2;
-            a.q.scales += r / kMxBlock;
-            a.q.k = args.q.k - r < most ? args.q.k - r : most;
-            const unsigned cols = (unsigned)ceil_div(a.q.rows, kColCols);
-            if (tall)
-                hipLaunchKernelGGL((quantize_columns_kernel<kBf16, 8>), dim3(cols, (unsigned)ceil_div(a.q.k, 256)), dim3(512), 0, stream, a);
-            else
-                hipLaunchKernelGGL((quantize_columns_kernel<kBf16, 4>), dim3(cols, (unsigned)ceil_div(a.q.k, 128)), dim3(256), 0, stream, a);
-            if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-        }
-        return hipSuccess;
+constexpr int64_t kMaxBlocks = 1 << 22;   // of a launch: a grid holds fewer than 2^32 lanes
+
+// the workgroups of a matrix
+int64_t set_blocks(MxQuantArgs& a) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.x);
+    int64_t x, y;
+    if (a.columns) {
+        a.aligned = a.ldx % 2 == 0 && at % 4 == 0 && a.ldx <= (int64_t)1 << 24;   // 32 rows stay below 2^31 bytes
+        x = ceil_div(a.q.rows, kColCols);
+        y = ceil_div(a.q.k, kColRows);
+    } else {
+        a.aligned = a.ldx % 8 == 0 && at % 16 == 0;
+        a.lane_shift = row_lanes(a.q.kp() / 8);
+        x = ceil_div(a.q.kp() / 8, (int64_t)1 << a.lane_shift);
+        y = ceil_div(a.q.rows, (int64_t)(kThreads >> a.lane_shift) * kRowSteps);
     }
-    const bool aligned = args.ldx % 8 == 0 && reinterpret_cast<uintptr_t>(args.x) % 16 == 0;
-    return by_rows(args.q.rows, args.q.kp() / 8, [&](int64_t r, int64_t n, dim3 grid, int s) {
-        MxQuantArgs a = args;
+    a.blocks_x = (uint32_t)x;
+    return x * y;
+}
+
+hipError_t launch_jobs(const MxQuantJobs& jobs, int64_t blocks, bool bf16, hipStream_t stream) {
+    if (bf16) hipLaunchKernelGGL((quantize_kernel<true>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, jobs);
+    else hipLaunchKernelGGL((quantize_kernel<false>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, jobs);
+    return hipGetLastError();
+}
+
+// One matrix of more workgroups than a launch takes: rows of it at a time.
+hipError_t in_pieces(const MxQuantArgs& args, hipStream_t stream) {
+    const int64_t all = args.columns ? args.q.k : args.q.rows;
+    MxQuantArgs a = args;
+    int64_t most = all;
+    while (set_blocks(a) > kMaxBlocks) {
+        most = round_up(most / 2, kMxPad);
+        (args.columns ? a.q.k : a.q.rows) = most;
+    }
+    for (int64_t r = 0; r < all; r += most) {
+        a = args;
         a.x += r * a.ldx;
-        a.q.codes += r * a.q.ldc;
-        a.q.scales += r * a.q.lds;
-        a.q.rows = n;
-        if (aligned) hipLaunchKernelGGL((quantize_rows_kernel<kBf16, true>), grid, dim3(kThreads), 0, stream, a, s);
-        else hipLaunchKernelGGL((quantize_rows_kernel<kBf16, false>), grid, dim3(kThreads), 0, stream, a, s);
-    });
+        (args.columns ? a.q.k : a.q.rows) = all - r < most ? all - r : most;
+        a.q.codes += args.columns ? r / 2 : r * a.q.ldc;
+        a.q.scales += args.columns ? r / kMxBlock : r * a.q.lds;
+        MxQuantJobs jobs{};
+        jobs.job[0] = a;
+        jobs.count = 1;
+        const int64_t blocks = set_blocks(jobs.job[0]);
+        if (hipError_t e = launch_jobs(jobs, blocks, args.bf16, stream); e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 template <int kType>
@@ -274,8 +323,23 @@ hipError_t dequantize(const MxDequantArgs& args, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_mx4_quantize(const MxQuantArgs& a, hipStream_t stream) {
-    return a.bf16 ? quantize<true>(a, stream) : quantize<false>(a, stream);
+hipError_t launch_mx4_quantize(const MxQuantArgs* args, int count, hipStream_t stream) {
+    MxQuantJobs jobs{};
+    int64_t blocks = 0;
+    for (int i = 0; i < count; ++i) {
+        if (args[i].q.rows == 0 || args[i].q.k == 0) continue;
+        MxQuantArgs& a = jobs.job[jobs.count];
+        a = args[i];
+        const int64_t more = set_blocks(a);
+        if (more > kMaxBlocks / kMxJobs) {
+            if (hipError_t e = in_pieces(args[i], stream); e != hipSuccess) return e;
+            continue;
+        }
+        a.block0 = (uint32_t)blocks;
+        blocks += more;
+        ++jobs.count;
+    }
+    return jobs.count > 0 ? launch_jobs(jobs, blocks, args[0].bf16, stream) : hipSuccess;
 }
 
 hipError_t launch_mx4_dequantize(const MxDequantArgs& a, hipStream_t stream) {
