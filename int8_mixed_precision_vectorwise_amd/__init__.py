@@ -99,13 +99,16 @@ def _rowmajor(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
     """Leading dimension of a row-major 2-D tensor with unit column stride."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
-    if t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1 and rows > 0:
         raise ValueError(f"{name} must have unit column stride")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if rows > 1 and ld < cols:
         raise ValueError(f"{name} must not have rows that overlap (an expanded tensor: make it contiguous)")
-    return max(t.stride(0), t.shape[1], 1)
+    return max(ld, cols, 1)
 
 
 def _vec(t: torch.Tensor, name: str, dtype: torch.dtype, n: int) -> None:
@@ -867,10 +870,12 @@ def fp4_cache_append(cache: Fp4Cache, q: Optional[torch.Tensor], k: torch.Tensor
             raise ValueError("q and k differ in tokens")
         heads = q.shape[1]
         if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        ldo, hso = _heads(out, "out", cache.dtype, heads, c.head_dim)
-        if out.shape[0] != n:
-            raise ValueError("out has the wrong shape")
+            out = q.new_empty(q.shape)
+            ldo, hso = heads * c.head_dim, c.head_dim
+        else:
+            ldo, hso = _heads(out, "out", cache.dtype, heads, c.head_dim)
+            if out.shape[0] != n:
+                raise ValueError("out has the wrong shape")
     elif out is not None:
         raise ValueError("out without q")
     call = Fp4AppendStruct(k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv, slots.data_ptr(), positions.data_ptr(),
@@ -906,14 +911,15 @@ class Mx4Tensor:
 
     def struct(self) -> Mx4Struct:
         """The C form, after checking that the fields go together (the library checks ranges and alignment)."""
-        codes, scales, kp = self.codes, self.scales, (self.k + 127) // 128 * 128
+        codes, scales, k = self.codes, self.scales, self.k
+        kp = -(-k // 128) * 128
         ldc, lds = _rowmajor(codes, "codes", torch.uint8), _rowmajor(scales, "scales", torch.uint8)
-        rows = codes.shape[0]
-        if scales.shape[0] != rows or codes.shape[1] < kp // 2 or scales.shape[1] < kp // 32:
-            raise ValueError(f"codes and scales must hold [{rows}, {kp // 2}] and [{rows}, {kp // 32}] bytes for k = {self.k}")
-        # the stride of a single row, or of empty ones, is never taken
-        return Mx4Struct(codes.data_ptr(), scales.data_ptr(), rows, self.k, ldc if rows > 1 and kp else kp // 2,
-                         lds if rows > 1 and kp else kp // 32)
+        (rows, width), (held, scale_width) = codes.shape, scales.shape
+        if held != rows or width < kp // 2 or scale_width < kp // 32:
+            raise ValueError(f"codes and scales must hold [{rows}, {kp // 2}] and [{rows}, {kp // 32}] bytes for k = {k}")
+        if rows <= 1 or kp == 0:        # a stride that is never taken: any that the library accepts
+            ldc, lds = kp // 2, kp // 32
+        return Mx4Struct(codes.data_ptr(), scales.data_ptr(), rows, k, ldc, lds)
 
 
 def _half(t: torch.Tensor, name: str) -> int:
@@ -924,12 +930,12 @@ def _half(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _space(need: int, workspace: Optional[torch.Tensor], dev: torch.device) -> Optional[torch.Tensor]:
+def _space(need: int, workspace: Optional[torch.Tensor], like: torch.Tensor) -> Optional[torch.Tensor]:
     """A call's workspace: the caller's, or one of ``need`` bytes (none for 0)."""
     if workspace is not None:
         _bytes(workspace, "workspace")
         return workspace
-    return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    return like.new_empty(need, dtype=torch.uint8) if need else None
 
 
 def _run_of(ws: Optional[torch.Tensor]) -> Tuple[Optional[int], int]:
@@ -943,12 +949,18 @@ def mx4_quantize(x: torch.Tensor, columns: bool = False, out: Optional[Mx4Tensor
     ldx = _rowmajor(x, "x", x.dtype)
     code = _half(x, "x")
     m, k = x.shape
-    shape = (k, m) if columns else (m, k)
+    rows, length = (k, m) if columns else (m, k)
     if out is None:
-        out = Mx4Tensor.create(*shape, device=dev)
-    elif out.shape != shape:
+        kp = -(-length // 128) * 128
+        codes = x.new_empty((rows, kp // 2), dtype=torch.uint8)
+        scales = x.new_empty((rows, kp // 32), dtype=torch.uint8)
+        out = Mx4Tensor(codes, scales, length)
+        c = Mx4Struct(codes.data_ptr(), scales.data_ptr(), rows, length, kp // 2, kp // 32)
+    elif out.shape != (rows, length):
         raise ValueError("out has the wrong shape")
-    _run(dev, "i8mp_mx4_quantize", x.data_ptr(), code, m, k, ldx, bool(columns), ctypes.byref(out.struct()))
+    else:
+        c = out.struct()
+    _run(dev, "i8mp_mx4_quantize", x.data_ptr(), code, m, k, ldx, bool(columns), ctypes.byref(c))
     return out
 
 
@@ -958,10 +970,12 @@ def mx4_dequantize(t: Mx4Tensor, dtype: torch.dtype = torch.float16, out: Option
         raise ValueError("dtype must be torch.float16, torch.bfloat16 or torch.float32")
     dev = _device_of(t.codes, t.scales, out)
     if out is None:
-        out = torch.empty(t.shape, dtype=dtype, device=dev)
-    ldout = _rowmajor(out, "out", dtype)
-    if tuple(out.shape) != t.shape:
-        raise ValueError("out has the wrong shape")
+        out = t.codes.new_empty((t.codes.shape[0], t.k), dtype=dtype)
+        ldout = t.k
+    else:
+        ldout = _rowmajor(out, "out", dtype)
+        if tuple(out.shape) != t.shape:
+            raise ValueError("out has the wrong shape")
     _run(dev, "i8mp_mx4_dequantize", ctypes.byref(t.struct()), _DTYPE_CODE[dtype], out.data_ptr(), ldout)
     return out
 
@@ -979,11 +993,13 @@ def mx4_matmul(a: Mx4Tensor, b: Mx4Tensor, bias: Optional[torch.Tensor] = None, 
     if bias is not None:
         _vec(bias, "bias", dtype, n)
     if out is None:
-        out = torch.empty((m, n), dtype=dtype, device=dev)
-    ldout = _rowmajor(out, "out", dtype)
-    if tuple(out.shape) != (m, n):
-        raise ValueError("out has the wrong shape")
-    ws = _space(lib().i8mp_mx4_matmul_workspace_bytes(m, n, k), workspace, dev)
+        out = a.codes.new_empty((m, n), dtype=dtype)
+        ldout = n
+    else:
+        ldout = _rowmajor(out, "out", dtype)
+        if tuple(out.shape) != (m, n):
+            raise ValueError("out has the wrong shape")
+    ws = _space(lib().i8mp_mx4_matmul_workspace_bytes(m, n, k), workspace, a.codes)
     _run(dev, "i8mp_mx4_matmul", ctypes.byref(a.struct()), ctypes.byref(b.struct()),
          None if bias is None else bias.data_ptr(), _DTYPE_CODE[dtype], out.data_ptr(), ldout, *_run_of(ws))
     return out
@@ -1004,10 +1020,12 @@ def mx4_linear(x: torch.Tensor, w: Mx4Tensor, bias: Optional[torch.Tensor] = Non
         _vec(bias, "bias", x.dtype, n)
     if out is None:
         out = x.new_empty((m, n))
-    ldout = _rowmajor(out, "out", x.dtype)
-    if tuple(out.shape) != (m, n):
-        raise ValueError("out has the wrong shape")
-    ws = _space(lib().i8mp_mx4_linear_workspace_bytes(m, n, k), workspace, dev)
+        ldout = n
+    else:
+        ldout = _rowmajor(out, "out", x.dtype)
+        if tuple(out.shape) != (m, n):
+            raise ValueError("out has the wrong shape")
+    ws = _space(lib().i8mp_mx4_linear_workspace_bytes(m, n, k), workspace, x)
     _run(dev, "i8mp_mx4_linear", x.data_ptr(), code, m, ldx, ctypes.byref(w.struct()),
          None if bias is None else bias.data_ptr(), out.data_ptr(), ldout, *_run_of(ws))
     return out
@@ -1040,16 +1058,20 @@ def mx4_linear_backward(grad_out: torch.Tensor, x: Optional[torch.Tensor], w: Op
         raise ValueError("grad_out, x and w must be [m, n], [m, k] and [n, k]")
     ldgx = ldgw = 0
     if need_x:
-        out_x = grad_out.new_empty((m, k)) if out_x is None else out_x
-        ldgx = _rowmajor(out_x, "out_x", dtype)
-        if tuple(out_x.shape) != (m, k):
-            raise ValueError("out_x has the wrong shape")
+        if out_x is None:
+            out_x, ldgx = grad_out.new_empty((m, k)), k
+        else:
+            ldgx = _rowmajor(out_x, "out_x", dtype)
+            if tuple(out_x.shape) != (m, k):
+                raise ValueError("out_x has the wrong shape")
     if need_w:
-        out_w = grad_out.new_empty((n, k)) if out_w is None else out_w
-        ldgw = _rowmajor(out_w, "out_w", dtype)
-        if tuple(out_w.shape) != (n, k):
-            raise ValueError("out_w has the wrong shape")
-    ws = _space(lib().i8mp_mx4_linear_backward_workspace_bytes(m, n, k), workspace, dev)
+        if out_w is None:
+            out_w, ldgw = grad_out.new_empty((n, k)), k
+        else:
+            ldgw = _rowmajor(out_w, "out_w", dtype)
+            if tuple(out_w.shape) != (n, k):
+                raise ValueError("out_w has the wrong shape")
+    ws = _space(lib().i8mp_mx4_linear_backward_workspace_bytes(m, n, k), workspace, grad_out)
     _run(dev, "i8mp_mx4_linear_backward", grad_out.data_ptr(), ldg, x.data_ptr() if need_w else None, ldx,
          w.data_ptr() if need_x else None, ldw, code, m, n, k, out_x.data_ptr() if need_x else None, ldgx,
          out_w.data_ptr() if need_w else None, ldgw, *_run_of(ws))
