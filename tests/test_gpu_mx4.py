@@ -185,6 +185,71 @@ def test_matmul_exact_sums(case):
         assert torch.equal(got.cpu(), torch.from_numpy((want + bias).astype(np.float32)).to(DTYPE[kind])), kind
 
 
+# several tiles a workgroup, whole rounds and another cut for the last columns, sums split over k with every tile shape
+LARGE = [(4352, 16640, 300), (4173, 22011, 1000), (8192, 2049, 1500), (1500, 1600, 5000), (40, 200, 20000), (100, 300, 9001),
+         (512, 512, 60000), (128, 5120, 13824), (700, 1200, 9000), (300, 300, 30000), (17, 70001, 140), (70001, 17, 300)]
+
+
+@pytest.mark.parametrize("case", LARGE, ids=lambda c: "%dx%dx%d" % c)
+def test_matmul_exact_sums_large(case):
+    """As above, against torch's fp32 product on the GPU, exact for such sums too."""
+    m, n, k = case
+    gen = torch.Generator(device="cuda").manual_seed(m + n + k)
+    kp = -(-k // 128) * 128
+    lut = torch.tensor(np.concatenate([mx4.GRID, -mx4.GRID]), dtype=torch.float32, device="cuda")
+    keep = torch.arange(kp, device="cuda") < k
+
+    def drawn_here(rows, low, high):
+        codes = torch.randint(0, 16, (rows, kp), generator=gen, device="cuda", dtype=torch.uint8) * keep
+        # mostly small numbers where sums are long: they stay below 2^22 quarters
+        if k > 5000:
+            codes = torch.where(torch.rand(codes.shape, generator=gen, device="cuda") < 0.98, codes & 9, codes)
+        scales = torch.randint(low, high, (rows, kp // 32), generator=gen, device="cuda", dtype=torch.uint8)
+        value = lut[codes.int()] * torch.exp2(scales.float() - 127).repeat_interleave(32, 1)
+        return i8.Mx4Tensor(codes[:, 0::2] | codes[:, 1::2] << 4, scales, k), value
+
+    qa, a = drawn_here(m, 127, 129)
+    qb, b = drawn_here(n, 126, 128)
+    bias = torch.randint(-8, 9, (n,), generator=gen, device="cuda").float()
+    say(f"mx4_matmul large {case}")
+    want = a @ b.t()
+    # what has passed through a sum on the way, in quarters of the least product, stays whole in fp32
+    assert float((a.abs().max() * b.abs().max())) * k < 2 ** 24 or float((a.abs() @ b.abs().t()).max()) < 2 ** 22
+    got = i8.mx4_matmul(qa, qb, dtype=torch.float32)
+    assert torch.equal(got, want)
+    out = torch.full((m, n + 5), 7.0, dtype=torch.float16, device="cuda")
+    i8.mx4_matmul(qa, qb, bias.half(), out=out[:, 1:1 + n])
+    assert torch.equal(out[:, 1:1 + n], (want + bias).half())
+    assert bool((out[:, :1] == 7).all()) and bool((out[:, 1 + n:] == 7).all())
+    assert torch.equal(i8.mx4_matmul(qa, qb, bias.bfloat16(), torch.bfloat16), (want + bias).bfloat16())
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 60, 600), (4, 90, 1152), (16, 40, 128), (40, 300, 600), (200, 260, 384), (800, 900, 640)])
+def test_a_neighbours_scales_are_not_read_as_a_rows_own(m, n, k):
+    """Rows that end in the middle of a stage of 256, beside rows that begin with a block that is no number."""
+    rng = np.random.default_rng([93, m, k])
+    a, b = drawn(rng, m, k), drawn(rng, n, k)
+    a[1][1::2, 0] = 255
+    b[1][2::3, 0] = 255
+    say(f"mx4_matmul neighbours {m} {n} {k}")
+    got = wide(i8.mx4_matmul(held(*a, k), held(*b, k), dtype=torch.float32))
+    with np.errstate(invalid="ignore"):
+        want = mx4.values(*a) @ mx4.values(*b).T
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.nan_to_num(got), np.nan_to_num(want))
+
+
+def test_large_outputs_of_dequantize():
+    """Outputs past half the last-level cache are stored another way."""
+    say("mx4_dequantize large")
+    for m, k, t in ((6000, 11300, torch.float16), (6000, 5700, torch.float32), (5000, 13500, torch.bfloat16)):
+        x = torch.randn((m, k), device="cuda", dtype=torch.float32).to(torch.float16)
+        q = i8.mx4_quantize(x)
+        got = i8.mx4_dequantize(q, t)
+        rows = torch.tensor([0, 1, 777, m // 2, m - 1])
+        assert np.array_equal(wide(got[rows.cuda()]), mx4.rounded(wide(x[rows.cuda()])))
+        assert bool((got.float().abs().sum(1) > 0).all())
+
+
 @pytest.mark.parametrize("case", [(1, 300, 5120), (5, 64, 1000), (40, 200, 4096), (130, 260, 2500), (300, 2000, 640)],
                          ids=lambda c: "%dx%dx%d" % c)
 @pytest.mark.parametrize("kind", ["f16", "bf16", "f32"])

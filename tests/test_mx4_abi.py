@@ -92,6 +92,7 @@ def test_matmul_workspace(L):
             assert run(a, b, None, 0, A16, n, ODD, w, None) == EWORKSPACE
         if NO_GPU:
             assert run(a, b, None, 0, A16, n, A16, w, None) == EDEVICE
+    assert seen >= 2
 
 
 def test_linear_validation(L):
