@@ -46,28 +46,29 @@ __host__ __device__ inline int w_bytes(int64_t rows, int64_t k) {
     return (int)((rows * ((k + kStretch - 1) / kStretch) * (kStretch / kMxBlock) + 15) / 16 * 16);
 }
 
-template <bool kBf16>
-__device__ inline void quantize_x(const MxGemmArgs& g, int blocks, uint8_t* lds) {
-    const int m = (int)g.a.rows, k = (int)g.a.k;
-    for (int id = threadIdx.x; id < m * blocks; id += kThreads) {
-        const int row = id / blocks, block = id - row * blocks;
-        v4u v[4] = {};
-        if (block * kMxBlock < k) {   // k is a multiple of 32
-            const v4u* p = reinterpret_cast<const v4u*>(g.x + row * g.ldx + block * kMxBlock);
+// block `id` of x's m rows of `blocks`
+__device__ inline void load_x(const MxGemmArgs& g, int blocks, int id, v4u (&v)[4]) {
+    const int row = id / blocks, block = id - row * blocks;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = p[e];
-        }
-        us2 top = mags(v[0][0]);
+    for (int e = 0; e < 4; ++e) v[e] = v4u{0, 0, 0, 0};
+    if (row < (int)g.a.rows && block * kMxBlock < (int)g.a.k) {   // k is a multiple of 32
+        const v4u* p = reinterpret_cast<const v4u*>(g.x + row * g.ldx + block * kMxBlock);
 #pragma unroll
-        for (int e = 1; e < 16; ++e) top = __builtin_elementwise_max(top, mags(v[e >> 2][e & 3]));
-        const uint32_t byte = scale_byte<kBf16>(top.x > top.y ? top.x : top.y);
-        const float scale = scale_value(byte);
-        v4u codes;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) codes[e] = byte == 255u ? 0u : encode8<kBf16>(v[e][0], v[e][1], v[e][2], v[e][3], scale);
-        *reinterpret_cast<v4u*>(lds + id * 16) = codes;
-        lds[m * blocks * 16 + id] = (uint8_t)byte;
+        for (int e = 0; e < 4; ++e) v[e] = p[e];
     }
+}
+template <bool kBf16>
+__device__ inline void quantize_x(const v4u (&v)[4], int id, int all, uint8_t* lds) {
+    us2 top = mags(v[0][0]);
+#pragma unroll
+    for (int e = 1; e < 16; ++e) top = __builtin_elementwise_max(top, mags(v[e >> 2][e & 3]));
+    const uint32_t byte = scale_byte<kBf16>(top.x > top.y ? top.x : top.y);
+    const float scale = scale_value(byte);
+    v4u codes;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) codes[e] = byte == 255u ? 0u : encode8<kBf16>(v[e][0], v[e][1], v[e][2], v[e][3], scale);
+    *reinterpret_cast<v4u*>(lds + id * 16) = codes;
+    lds[all * 16 + id] = (uint8_t)byte;
 }
 
 // R tiles of 16 rows of w.  kIn: x is quantized (0), fp16 (1) or bfloat16 (2).
@@ -133,12 +134,28 @@ __global__ __launch_bounds__(kThreads, 4) void mx4_decode_kernel(MxGemmArgs g, i
     Stretch b[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) fetch(b[i], wave + i * kWaves);
-    // w's scales, whole rows at once: by stretches they took as long as a third of the codes.  Past a row's end zeros.
-    for (int id = threadIdx.x; id < rows * (row_scales / 4); id += kThreads) {
-        const int row = id / (row_scales / 4), at = (id - row * (row_scales / 4)) * 4;
-        reinterpret_cast<uint32_t*>(lds)[id] = __builtin_amdgcn_raw_buffer_load_b32(scales, at < kp / kMxBlock ? row * lsw + at : kOut, 0, 0);
+    const int x_blocks = m * row_scales, words = rows * (row_scales / 4);
+    v4u v[4];
+    if constexpr (kIn != 0) load_x(g, row_scales, threadIdx.x, v);
+    // w's scales, whole rows; past a row's end zeros
+    constexpr int kWords = 4;   // a thread's at a time
+    for (int base = threadIdx.x; base < words; base += kWords * kThreads) {
+        uint32_t word[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            const int id = base + i * kThreads, row = id / (row_scales / 4), at = (id - row * (row_scales / 4)) * 4;
+            word[i] = __builtin_amdgcn_raw_buffer_load_b32(scales, id < words && at < kp / kMxBlock ? row * lsw + at : kOut, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            if (base + i * kThreads < words) reinterpret_cast<uint32_t*>(lds)[base + i * kThreads] = word[i];
     }
-    if constexpr (kIn != 0) quantize_x<kIn == 2>(g, row_scales, lds + x_at);
+    if constexpr (kIn != 0) {
+        for (int id = threadIdx.x; id < x_blocks; id += kThreads) {
+            if (id >= kThreads) load_x(g, row_scales, id, v);
+            quantize_x<kIn == 2>(v, id, x_blocks, lds + x_at);
+        }
+    }
     __syncthreads();
     for (int t = wave; t < stretches; t += kAhead * kWaves) {
 #pragma unroll
