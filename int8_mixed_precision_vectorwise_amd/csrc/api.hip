@@ -1056,21 +1056,16 @@ i8mp_status i8mp_mx4_linear_backward(const void* grad_out, int64_t ldg, const vo
         jobs[count++] = mx4_quant(x, ldx, dtype, true, x_cols);
     }
     if (i8mp_status s = launched(launch_mx4_quantize(jobs, count, stream)); s != I8MP_OK) return s;
-    if (want_x) {
-        g.a = g_rows;
-        g.b = w_cols;
-        g.out = grad_x;
-        g.ldout = ldgx;
-        if (i8mp_status s = launched(launch_mx4_gemm(g, stream)); s != I8MP_OK) return s;
-    }
-    if (want_w) {
-        g.a = g_cols;
-        g.b = x_cols;
-        g.out = grad_w;
-        g.ldout = ldgw;
-        if (i8mp_status s = launched(launch_mx4_gemm(g, stream)); s != I8MP_OK) return s;
-    }
-    return I8MP_OK;
+    MxGemmArgs gw = g;
+    g.a = g_rows;
+    g.b = w_cols;
+    g.out = grad_x;
+    g.ldout = ldgx;
+    gw.a = g_cols;
+    gw.b = x_cols;
+    gw.out = grad_w;
+    gw.ldout = ldgw;
+    return launched(want_x && want_w ? launch_mx4_gemm_pair(g, gw, stream) : launch_mx4_gemm(want_x ? g : gw, stream));
 }
 
 }  // extern "C"

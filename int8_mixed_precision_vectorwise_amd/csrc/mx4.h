@@ -24,7 +24,7 @@ struct MxQuantArgs {
     bool columns;
     Mx4 q;
     // set by the launcher
-    bool aligned;                   // x can be read in whole words
+    bool aligned, few;              // x can be read in whole words; a lane takes one row
     int32_t lane_shift;             // by rows: lanes along a row
     uint32_t block0, blocks_x;      // first workgroup, workgroups along a row of them
 };
@@ -58,6 +58,8 @@ hipError_t launch_mx4_dequantize(const MxDequantArgs& a, hipStream_t stream);
 // workspace of a product of these sizes (0: none needed)
 size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k);
 hipError_t launch_mx4_gemm(const MxGemmArgs& g, hipStream_t stream);
+// Two products whose outputs are of one 16-bit type.
+hipError_t launch_mx4_gemm_pair(const MxGemmArgs& a, const MxGemmArgs& b, hipStream_t stream);
 // The product of a few rows, where mx4_decode_fits: the weights streamed through the matrix cores.  x in place of a's
 // codes (and of out's type) where mx4_decode_quantizes.
 constexpr int kMxDecodeRows = 16;

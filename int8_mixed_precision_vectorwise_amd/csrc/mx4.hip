@@ -32,16 +32,16 @@ typedef uint32_t u32_any __attribute__((aligned(2)));
 // them: as many 16-byte loads in flight a lane.
 constexpr int kRowSteps = 4;
 
-template <bool kBf16, bool kAligned>
+template <bool kBf16, bool kAligned, int kSteps>
 __device__ inline void quantize_rows(const MxQuantArgs& a, uint32_t bx, uint32_t by) {
     const int lanes = 1 << a.lane_shift, rows = kThreads >> a.lane_shift;
     const int64_t c = (int64_t)bx * lanes + (threadIdx.x & (lanes - 1));  // chunk of 8 elements
-    const int64_t row0 = (int64_t)by * (rows * kRowSteps) + (threadIdx.x >> a.lane_shift);
+    const int64_t row0 = (int64_t)by * (rows * kSteps) + (threadIdx.x >> a.lane_shift);
     if (c * 8 >= a.q.kp()) return;  // whole words of scales leave: kp is a multiple of 128
     const int64_t left = a.q.k - c * 8;
-    v4u x[kRowSteps];
+    v4u x[kSteps];
 #pragma unroll
-    for (int i = 0; i < kRowSteps; ++i) {
+    for (int i = 0; i < kSteps; ++i) {
         x[i] = v4u{0, 0, 0, 0};
         const int64_t r = row0 + i * rows;
         if (r >= a.q.rows) continue;
@@ -56,7 +56,7 @@ __device__ inline void quantize_rows(const MxQuantArgs& a, uint32_t bx, uint32_t
         }
     }
 #pragma unroll
-    for (int i = 0; i < kRowSteps; ++i) {
+    for (int i = 0; i < kSteps; ++i) {
         const int64_t r = row0 + i * rows;
         if (r >= a.q.rows) continue;
         us2 m = __builtin_elementwise_max(__builtin_elementwise_max(mags(x[i][0]), mags(x[i][1])),
@@ -163,8 +163,9 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(MxQuantJobs jobs) {
         if (a.aligned) quantize_columns<kBf16, true>(a, bx, by, codes, scales);
         else quantize_columns<kBf16, false>(a, bx, by, codes, scales);
     } else {
-        if (a.aligned) quantize_rows<kBf16, true>(a, bx, by);
-        else quantize_rows<kBf16, false>(a, bx, by);
+        if (!a.aligned) quantize_rows<kBf16, false, kRowSteps>(a, bx, by);
+        else if (a.few) quantize_rows<kBf16, true, 1>(a, bx, by);
+        else quantize_rows<kBf16, true, kRowSteps>(a, bx, by);
     }
 }
 
@@ -285,7 +286,10 @@ int64_t set_blocks(MxQuantArgs& a) {
         a.aligned = a.ldx % 8 == 0 && at % 16 == 0;
         a.lane_shift = row_lanes(a.q.kp() / 8);
         x = ceil_div(a.q.kp() / 8, (int64_t)1 << a.lane_shift);
-        y = ceil_div(a.q.rows, (int64_t)(kThreads >> a.lane_shift) * kRowSteps);
+        // too few rows to fill the chip with kRowSteps a lane: one each
+        const int64_t rows = kThreads >> a.lane_shift;
+        a.few = a.aligned && x * ceil_div(a.q.rows, rows * kRowSteps) < 256;
+        y = ceil_div(a.q.rows, a.few ? rows : rows * kRowSteps);
     }
     a.blocks_x = (uint32_t)x;
     return x * y;
