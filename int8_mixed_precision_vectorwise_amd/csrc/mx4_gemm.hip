@@ -104,11 +104,12 @@ struct Tile {
     static constexpr int kLds = kScaleAt + kScales + 2 * BN * 4 + (kAhead && 4 * kOutArea > kScales ? 4 * kOutArea : kScales);
 };
 
-// kPair: the workgroups from units0 on belong to a second product
+// kPair: the workgroups from split on belong to a second product
 template <int FM, int FN, int kType, bool kPair>
-__global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx4_gemm_kernel(MxGemmArgs first, MxGemmArgs second, uint32_t units0) {
-    const MxGemmArgs& g = kPair && blockIdx.x >= units0 ? second : first;
-    const uint32_t block = kPair && blockIdx.x >= units0 ? blockIdx.x - units0 : blockIdx.x;
+__global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx4_gemm_kernel(MxGemmArgs first, MxGemmArgs second, uint32_t split) {
+    const bool later = kPair && blockIdx.x >= split;
+    const MxGemmArgs& g = later ? second : first;
+    const uint32_t block = later ? blockIdx.x - split : blockIdx.x, stride = !kPair ? gridDim.x : later ? gridDim.x - split : split;
     using T = Tile<FM, FN>;
     constexpr int BM = T::BM, BN = T::BN;
     constexpr int kBiasAt = T::kScaleAt + (T::kAhead ? T::kScales : 2 * T::kScales);
@@ -124,6 +125,7 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx4_gemm_kernel(MxGe
     const int kp = (int)g.a.kp();
     const uint32_t tiles_m = (uint32_t)((g.a.rows + BM - 1) / BM), tiles_n = (uint32_t)((g.b.rows + BN - 1) / BN);
     const uint32_t tiles = tiles_m * tiles_n, units = tiles * (uint32_t)g.parts;
+    if (kPair && block >= units) return;   // its product has fewer tiles than workgroups
 
     // A load of codes: 8 rows of 128 bytes, lane i the 16-byte chunk at place i % 8 of row i / 8.  Place p of row r
     // holds chunk p ^ (r / 2 % 8): the 16 lanes that LDS serves at once, which want one chunk of different rows, then
@@ -219,7 +221,7 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx4_gemm_kernel(MxGe
 
     begin(open(block));
     uint32_t turn = 0;
-    for (uint32_t id = block; id < units; id += gridDim.x, turn ^= 1) {
+    for (uint32_t id = block; id < units; id += stride, turn ^= 1) {
         const Unit u = open(id);
 #pragma unroll
         for (int i = 0; i < FM; ++i)
@@ -284,7 +286,7 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx4_gemm_kernel(MxGe
         } while (++t < u.stages);
         wait_loads<0>();   // none lands in what follows
         meet();            // the stages are free
-        if (T::kAhead && id + gridDim.x < units) begin(open(id + gridDim.x));
+        if (T::kAhead && id + stride < units) begin(open(id + stride));
 
         // Sums (i, j, r): row wm + 32 i + l32, column wn + 32 j + 8 (r / 4) + 4 hi + r % 4.  They pass through the wave's
         // part of LDS, 32 rows of kCols at a time, and leave as 16-byte pieces of whole lines.
@@ -427,14 +429,17 @@ Cut best_cut(int64_t m, int64_t n, int64_t k) {
 struct Plan {
     int64_t n_main;   // 0: all columns by `rest`
     Cut rest;
+    double us;
 };
 Plan plan(int64_t m, int64_t n, int64_t k) {
-    Plan p{0, best_cut(m, n, k)};
+    const Cut whole = best_cut(m, n, k);
+    Plan p{0, whole, whole.us};
     const int64_t rows = ceil_div(m, 256), rounds = rows * ceil_div(n, 256) / kCUs, cols = rounds * kCUs / rows;
     const int64_t n_main = cols * 256, stages = ceil_div(k, kStageK);
     if (cols > 0 && n_main < n) {
         const Cut rest = best_cut(m, n - n_main, k);
-        if (tiles_us(4, rows * cols, stages) + 3.0 + rest.us < 0.98 * p.rest.us) p = Plan{n_main, rest};
+        const double us = tiles_us(4, rows * cols, stages) + 3.0 + rest.us;
+        if (us < 0.98 * whole.us) p = Plan{n_main, rest, us};
     }
     return p;
 }
@@ -448,32 +453,45 @@ size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k) {
     return p.rest.parts > 1 ? (size_t)p.rest.parts * m * part_row(n - p.n_main) * 4 : 0;
 }
 
-// Two products of one type in one launch, where each is one cut of 64 x 64 tiles: small ones leave most of the chip to
-// each other.  The one with the longer sums starts first.  Gradients of 512 x 4096 x 1024: 9.9 and 7.4 us apart.
-template <int kType>
-hipError_t launch_pair(const MxGemmArgs& x, const MxGemmArgs& y, hipStream_t stream) {
-    const auto units = [](const MxGemmArgs& g) { return (uint32_t)(ceil_div(g.a.rows, 64) * ceil_div(g.b.rows, 64)); };
-    hipLaunchKernelGGL((mx4_gemm_kernel<1, 1, kType, true>), dim3(units(x) + units(y)), dim3(256), 0, stream, x, y, units(x));
+// Two products of one type in one launch, where one alone leaves workgroups idle or both are small:
+// - each one cut of 64 x 64 tiles: all tiles, those of the longer sums first.  Gradients of 512 x 4096 x 1024: 12.5 us, one
+//   after the other 17.3.
+// - by 256 x 256 tiles, where the model finds a share of the workgroups for each that beats two launches.  Gradients
+//   of 2048 x 4096 x 4096 (128 tiles of 16 stages, 256 of 8): 50.9 us, one after the other 54.4.
+template <int F, int kType>
+hipError_t launch_pair(const MxGemmArgs& x, const MxGemmArgs& y, int64_t split, int64_t all, hipStream_t stream) {
+    hipLaunchKernelGGL((mx4_gemm_kernel<F, F, kType, true>), dim3((unsigned)all), dim3(256), 0, stream, x, y, (uint32_t)split);
     return hipGetLastError();
 }
 
 hipError_t launch_mx4_gemm_pair(const MxGemmArgs& a, const MxGemmArgs& b, hipStream_t stream) {
-    const auto simple = [](const MxGemmArgs& g) {
-        if (mx4_decode_fits(g.a.rows, g.a.k)) return false;
-        const Plan p = plan(g.a.rows, g.b.rows, g.a.k);
-        return p.n_main == 0 && p.rest.f == 1 && p.rest.parts == 1;
-    };
-    if (!simple(a) || !simple(b)) {
-        if (hipError_t e = launch_mx4_gemm(a, stream); e != hipSuccess) return e;
-        return launch_mx4_gemm(b, stream);
-    }
     MxGemmArgs x = a.a.k >= b.a.k ? a : b, y = a.a.k >= b.a.k ? b : a;
     for (MxGemmArgs* g : {&x, &y}) {
         g->parts = 1;
         g->part_stages = (int)ceil_div(g->a.k, kStageK);
         g->part_bytes = 0;
     }
-    return x.out_dtype == I8MP_DTYPE_BF16 ? launch_pair<I8MP_DTYPE_BF16>(x, y, stream) : launch_pair<I8MP_DTYPE_F16>(x, y, stream);
+    const auto tiles = [](const MxGemmArgs& g, int f) { return ceil_div(g.a.rows, 64 * f) * ceil_div(g.b.rows, 64 * f); };
+    const bool bf16 = x.out_dtype == I8MP_DTYPE_BF16;
+    if (!mx4_decode_fits(x.a.rows, x.a.k) && !mx4_decode_fits(y.a.rows, y.a.k)) {
+        const Plan px = plan(x.a.rows, x.b.rows, x.a.k), py = plan(y.a.rows, y.b.rows, y.a.k);
+        const auto small = [](const Plan& p) { return p.n_main == 0 && p.rest.f == 1 && p.rest.parts == 1; };
+        if (small(px) && small(py)) {
+            const int64_t tx = tiles(x, 1), all = tx + tiles(y, 1);
+            return bf16 ? launch_pair<1, I8MP_DTYPE_BF16>(x, y, tx, all, stream) : launch_pair<1, I8MP_DTYPE_F16>(x, y, tx, all, stream);
+        }
+        // whole XCDs' turns each: a workgroup's tiles stay on its XCD
+        const int64_t tx = tiles(x, 4), ty = tiles(y, 4);
+        int64_t split = 0;
+        double best = 0.98 * (px.us + 3.0 + py.us);
+        for (int64_t s = kXcds; s < kCUs; s += kXcds) {
+            const double ux = tiles_us(4, ceil_div(tx, s) * kCUs, x.part_stages), uy = tiles_us(4, ceil_div(ty, kCUs - s) * kCUs, y.part_stages);
+            if ((ux > uy ? ux : uy) < best) best = ux > uy ? ux : uy, split = s;
+        }
+        if (split > 0) return bf16 ? launch_pair<4, I8MP_DTYPE_BF16>(x, y, split, kCUs, stream) : launch_pair<4, I8MP_DTYPE_F16>(x, y, split, kCUs, stream);
+    }
+    if (hipError_t e = launch_mx4_gemm(a, stream); e != hipSuccess) return e;
+    return launch_mx4_gemm(b, stream);
 }
 
 hipError_t launch_mx4_gemm(const MxGemmArgs& args, hipStream_t stream) {
