@@ -337,6 +337,27 @@ def test_linear_backward(case, kind):
     assert i8.mx4_linear_backward(tg, tx, tw, False, False) == (None, None)
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("case", [(2560, 2816, 2816), (2047, 4100, 4090), (600, 4099, 1030), (4096, 300, 5000)],
+                         ids=lambda c: "%dx%dx%d" % c)
+def test_linear_backward_at_size(case, kind):
+    """Both products in one launch, of large and of small tiles, into columns of wider matrices."""
+    m, n, k = case
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    g, x, w = (torch.randn(s, generator=gen, device="cuda").to(DTYPE[kind]) for s in ((m, n), (m, k), (n, k)))
+    say(f"mx4_linear_backward at size {case} {kind}")
+    bx, bw = (torch.full((r, k + 8), 7.0, dtype=DTYPE[kind], device="cuda") for r in (m, n))
+    gx, gw = i8.mx4_linear_backward(g, x, w, out_x=bx[:, :k], out_w=bw[:, :k])
+    assert gx.data_ptr() == bx.data_ptr() and gw.data_ptr() == bw.data_ptr()
+    assert bool((bx[:, k:] == 7).all()) and bool((bw[:, k:] == 7).all())
+    back = lambda t, columns: i8.mx4_dequantize(i8.mx4_quantize(t, columns), torch.float32).double()
+    for got, a, b in ((gx, back(g, False), back(w, True)), (gw, back(g, True), back(x, True))):
+        want, size = a @ b.t(), a.abs() @ b.abs().t()
+        kp = -(-a.shape[1] // 128) * 128
+        tol = (kp / 64 + 64) * 2.0 ** -23 * size + torch.finfo(DTYPE[kind]).eps / 2 * want.abs() + STEP[kind]
+        assert bool(((got.double() - want).abs() <= tol).all())
+
+
 def test_gradients_are_differences_of_the_linear():
     """Where every operand is on the 4-bit grid, the linear is linear and its gradients are its differences."""
     rng = np.random.default_rng(88)
