@@ -576,10 +576,11 @@ i8mp_status i8mp_fp4_cache_append(const i8mp_fp4_cache* cache /* host */, const 
  * 128: codes [rows x ldc bytes], two a byte, element 2 j in the low nibble of byte j,
  * and scales [rows x lds bytes].  i8mp_mx4_quantize writes the padding; who fills a
  * matrix by other means writes codes of 0 and any scale but 255 there. */
+#define I8MP_MX4_MAX_ROWS 67108864 /* more rows than this would leave the range of a launch's grid: I8MP_EINVAL */
 typedef struct i8mp_mx4 {
     uint8_t* codes;   /* device, 16-byte aligned                          */
     uint8_t* scales;  /* device, 4-byte aligned                           */
-    int64_t rows;     /* >= 0, < 2^31                                     */
+    int64_t rows;     /* >= 0, <= I8MP_MX4_MAX_ROWS                       */
     int64_t k;        /* >= 0                                             */
     int64_t ldc;      /* bytes: >= kp / 2, a multiple of 16, <= I8MP_MAX_LD */
     int64_t lds;      /* bytes: >= kp / 32, a multiple of 4, <= I8MP_MAX_LD */

@@ -897,7 +897,7 @@ i8mp_status i8mp_fp4_cache_append(const i8mp_fp4_cache* cache, const i8mp_fp4_ap
 namespace {
 // the internal form of a quantized matrix, if its sizes are in range; `filled` also looks at the pointers
 bool mx4(const i8mp_mx4* p, Mx4* q) {
-    if (!p || p->rows < 0 || p->rows > INT32_MAX || p->k < 0 || p->ldc > I8MP_MAX_LD || p->lds > I8MP_MAX_LD) return false;
+    if (!p || p->rows < 0 || p->rows > I8MP_MX4_MAX_ROWS || p->k < 0 || p->ldc > I8MP_MAX_LD || p->lds > I8MP_MAX_LD) return false;
     *q = Mx4{p->codes, p->ldc, p->scales, p->lds, p->rows, p->k};
     return p->ldc % 16 == 0 && p->lds % 4 == 0 && p->ldc >= q->kp() / 2 && p->lds >= q->kp() / kMxBlock;
 }
@@ -919,7 +919,7 @@ Mx4 mx4_at(char* base, size_t* at, int64_t rows, int64_t k) {
     return q;
 }
 bool mx4_sizes(int64_t m, int64_t n, int64_t k) {
-    const auto ok = [](int64_t v) { return v >= 0 && v <= INT32_MAX; };
+    const auto ok = [](int64_t v) { return v >= 0 && v <= I8MP_MX4_MAX_ROWS; };
     return ok(m) && ok(n) && ok(k);
 }
 bool mx4_fits(int64_t k) { return Mx4{nullptr, 0, nullptr, 0, 0, k}.kp() / 2 <= I8MP_MAX_LD; }  // as a row's length
@@ -989,7 +989,7 @@ size_t i8mp_mx4_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
 i8mp_status i8mp_mx4_linear(const void* x, int32_t dtype, int64_t m, int64_t ldx, const i8mp_mx4* w, const void* bias,
                             void* out, int64_t ldout, void* workspace, size_t workspace_bytes, hipStream_t stream) {
     MxGemmArgs g{};
-    if (!mx4(w, &g.b) || !half_type(dtype) || m < 0 || m > INT32_MAX || g.b.k > INT32_MAX) return I8MP_EINVAL;
+    if (!mx4(w, &g.b) || !half_type(dtype) || m < 0 || m > I8MP_MX4_MAX_ROWS) return I8MP_EINVAL;
     const int64_t n = g.b.rows, k = g.b.k;
     if (ldx < k || ldout < n || bad_ld(ldout)) return I8MP_EINVAL;
     if (m == 0 || n == 0) return I8MP_OK;

@@ -177,3 +177,14 @@ def test_python_binding_refusals():
             bad.struct()
     with pytest.raises(TypeError):
         i8.Mx4Tensor(w.codes.to(torch.int8), w.scales, 64).struct()
+
+
+def test_rows_that_a_grid_cannot_hold(L):
+    most = 1 << 26
+    assert L.i8mp_mx4_quantize(A16, 0, most + 1, 200, 200, 0, mx(rows=most + 1), None) == EINVAL
+    assert L.i8mp_mx4_matmul(mx(rows=most + 1), mx(), None, 0, A16, 5, A16, BIG, None) == EINVAL
+    assert L.i8mp_mx4_linear(A16, 0, most + 1, 200, mx(), None, A16, 5, A16, BIG, None) == EINVAL
+    assert L.i8mp_mx4_linear_workspace_bytes(most + 1, 5, 200) == 0 < L.i8mp_mx4_linear_workspace_bytes(most, 5, 200)
+    if NO_GPU:
+        assert L.i8mp_mx4_quantize(A16, 0, most, 200, 200, 0, mx(rows=most), None) == EDEVICE
+        assert L.i8mp_mx4_matmul(mx(rows=most), mx(), None, 0, A16, 5, A16, BIG, None) == EDEVICE
