@@ -607,7 +607,8 @@ i8mp_status i8mp_mx4_matmul(const i8mp_mx4* a /* host */, const i8mp_mx4* b /* h
 
 /* The linear with 4-bit weights and activations: out [m x n] = mx4(x) . w^T + bias, x
  * [m x k] quantized by rows on the way; x, bias and out of one 16-bit type.  The same
- * numbers, up to the order of the sums, as i8mp_mx4_quantize and i8mp_mx4_matmul. */
+ * numbers, up to the order of the sums, as i8mp_mx4_quantize and i8mp_mx4_matmul.  The
+ * query gives 0 where up to four rows are quantized within the product. */
 size_t i8mp_mx4_linear_workspace_bytes(int64_t m, int64_t n, int64_t k);
 i8mp_status i8mp_mx4_linear(const void* x, int32_t dtype, int64_t m, int64_t ldx, const i8mp_mx4* w /* host */,
                             const void* bias, void* out, int64_t ldout, void* workspace, size_t workspace_bytes,

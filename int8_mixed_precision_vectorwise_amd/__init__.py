@@ -832,14 +832,6 @@ def fp4_cache_attention(q: torch.Tensor, cache: Fp4Cache, table: torch.Tensor, l
     return out if lse is None else (out, lse)
 
 
-def _turning(t: torch.Tensor, name: str) -> int:
-    """Leading dimension of an angle table [rows, rotary / 2], fp32."""
-    ld = _rowmajor(t, name, torch.float32)
-    if t.shape[0] == 0:
-        raise ValueError(f"{name} has no rows")
-    return ld
-
-
 def fp4_cache_append(cache: Fp4Cache, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
                      positions: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor, interleaved: bool = False,
                      out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
@@ -860,9 +852,12 @@ def fp4_cache_append(cache: Fp4Cache, q: Optional[torch.Tensor], k: torch.Tensor
         raise ValueError("k and v differ in tokens")
     _vec(slots, "slots", torch.int64, n)
     _vec(positions, "positions", torch.int64, n)
-    ldcos, ldsin = _turning(cos, "cos"), _turning(sin, "sin")
-    if cos.shape != sin.shape:
+    ldcos, ldsin = _rowmajor(cos, "cos", torch.float32), _rowmajor(sin, "sin", torch.float32)
+    rows, half = cos.shape
+    if sin.shape != cos.shape:
         raise ValueError("cos and sin differ in shape")
+    if rows == 0:
+        raise ValueError("cos and sin have no rows")
     ldq = hsq = ldo = hso = heads = 0
     if q is not None:
         ldq, hsq = _heads(q, "q", cache.dtype, None, c.head_dim)
@@ -879,9 +874,9 @@ def fp4_cache_append(cache: Fp4Cache, q: Optional[torch.Tensor], k: torch.Tensor
     elif out is not None:
         raise ValueError("out without q")
     call = Fp4AppendStruct(k.data_ptr(), ldk, hsk, v.data_ptr(), ldv, hsv, slots.data_ptr(), positions.data_ptr(),
-                           cos.data_ptr(), sin.data_ptr(), ldcos, ldsin, cos.shape[0],
+                           cos.data_ptr(), sin.data_ptr(), ldcos, ldsin, rows,
                            q.data_ptr() if heads else None, ldq, hsq, out.data_ptr() if heads else None, ldo, hso, n, heads,
-                           2 * cos.shape[1], bool(interleaved))
+                           2 * half, bool(interleaved))
     _run(dev, "i8mp_fp4_cache_append", ctypes.byref(c), ctypes.byref(call))
     return out
 
@@ -912,13 +907,14 @@ class Mx4Tensor:
     def struct(self) -> Mx4Struct:
         """The C form, after checking that the fields go together (the library checks ranges and alignment)."""
         codes, scales, k = self.codes, self.scales, self.k
-        kp = -(-k // 128) * 128
         ldc, lds = _rowmajor(codes, "codes", torch.uint8), _rowmajor(scales, "scales", torch.uint8)
-        (rows, width), (held, scale_width) = codes.shape, scales.shape
-        if held != rows or width < kp // 2 or scale_width < kp // 32:
-            raise ValueError(f"codes and scales must hold [{rows}, {kp // 2}] and [{rows}, {kp // 32}] bytes for k = {k}")
-        if rows <= 1 or kp == 0:        # a stride that is never taken: any that the library accepts
-            ldc, lds = kp // 2, kp // 32
+        rows, width = codes.shape
+        held, scale_width = scales.shape
+        units = -(-k // 128)
+        if held != rows or width < units * 64 or scale_width < units * 4:
+            raise ValueError(f"codes and scales must hold [{rows}, {units * 64}] and [{rows}, {units * 4}] bytes for k = {k}")
+        if rows <= 1 or units == 0:     # a stride that is never taken: any that the library accepts
+            ldc, lds = units * 64, units * 4
         return Mx4Struct(codes.data_ptr(), scales.data_ptr(), rows, k, ldc, lds)
 
 

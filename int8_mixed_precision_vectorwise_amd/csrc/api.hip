@@ -980,7 +980,7 @@ i8mp_status i8mp_mx4_matmul(const i8mp_mx4* a, const i8mp_mx4* b, const void* bi
 }
 
 size_t i8mp_mx4_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    if (!mx4_sizes(m, n, k)) return 0;
+    if (!mx4_sizes(m, n, k) || mx4_decode_quantizes(m, k)) return 0;
     size_t at = 0;
     mx4_at(nullptr, &at, m, k);
     return at + mx4_gemm_workspace(m, n, k);
@@ -997,18 +997,20 @@ i8mp_status i8mp_mx4_linear(const void* x, int32_t dtype, int64_t m, int64_t ldx
     const size_t need = i8mp_mx4_linear_workspace_bytes(m, n, k);
     if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return I8MP_EWORKSPACE;
     if (i8mp_status s = check_device(); s != I8MP_OK) return s;
-    size_t at = 0;
-    g.a = mx4_at(static_cast<char*>(workspace), &at, m, k);
     g.bias = bias;
     g.out_dtype = dtype;
     g.out = out;
     g.ldout = ldout;
-    g.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + at);
-    if (mx4_decode_quantizes(m, k, x, ldx)) {
+    if (mx4_decode_quantizes(m, k)) {
+        g.a.rows = m;
+        g.a.k = k;
         g.x = static_cast<const half_bits*>(x);
         g.ldx = ldx;
         return launched(launch_mx4_decode(g, stream));
     }
+    size_t at = 0;
+    g.a = mx4_at(static_cast<char*>(workspace), &at, m, k);
+    g.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + at);
     const MxQuantArgs job = mx4_quant(x, ldx, dtype, false, g.a);
     if (i8mp_status s = launched(launch_mx4_quantize(&job, 1, stream)); s != I8MP_OK) return s;
     return launched(launch_mx4_gemm(g, stream));

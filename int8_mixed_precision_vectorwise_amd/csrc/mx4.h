@@ -24,8 +24,9 @@ struct MxQuantArgs {
     bool columns;
     Mx4 q;
     // set by the launcher
-    bool aligned, few;              // x can be read in whole words; a lane takes one row
-    int32_t lane_shift;             // by rows: lanes along a row
+    bool aligned;                   // by columns: x can be read in whole words
+    bool few;                       // by rows: a lane takes one row
+    int32_t lane_shift;             // and lanes along a row
     uint32_t block0, blocks_x;      // first workgroup, workgroups along a row of them
 };
 constexpr int kMxJobs = 4;
@@ -64,7 +65,7 @@ hipError_t launch_mx4_gemm_pair(const MxGemmArgs& a, const MxGemmArgs& b, hipStr
 // codes (and of out's type) where mx4_decode_quantizes.
 constexpr int kMxDecodeRows = 16;
 bool mx4_decode_fits(int64_t m, int64_t k);
-bool mx4_decode_quantizes(int64_t m, int64_t k, const void* x, int64_t ldx);
+bool mx4_decode_quantizes(int64_t m, int64_t k);
 hipError_t launch_mx4_decode(const MxGemmArgs& g, hipStream_t stream);
 
 }  // namespace i8mp

@@ -15,7 +15,7 @@
 // every CU gets as many workgroups of equal work.  Lanes whose row is not there take the
 // last row that is: their sums are not stored.
 //
-// Up to four rows of 16-bit x are quantized here (kIn), once a workgroup into LDS, while
+// Up to four rows of 16-bit x, of any alignment, are quantized here (kIn), once a workgroup into LDS, while
 // the first weights are on their way: a thread's 32 elements are one block.  That saves a
 // launch; with more rows every workgroup would read and convert too much of x.
 #include "common.h"
@@ -46,15 +46,22 @@ __host__ __device__ inline int w_bytes(int64_t rows, int64_t k) {
     return (int)((rows * ((k + kStretch - 1) / kStretch) * (kStretch / kMxBlock) + 15) / 16 * 16);
 }
 
+typedef v4u v4u_any __attribute__((aligned(2)));   // at any element's address
+
 // block `id` of x's m rows of `blocks`
 __device__ inline void load_x(const MxGemmArgs& g, int blocks, int id, v4u (&v)[4]) {
-    const int row = id / blocks, block = id - row * blocks;
+    const int row = id / blocks, block = id - row * blocks, left = (int)g.a.k - block * kMxBlock;
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = v4u{0, 0, 0, 0};
-    if (row < (int)g.a.rows && block * kMxBlock < (int)g.a.k) {   // k is a multiple of 32
-        const v4u* p = reinterpret_cast<const v4u*>(g.x + row * g.ldx + block * kMxBlock);
+    if (row >= (int)g.a.rows || left <= 0) return;
+    const half_bits* p = g.x + row * g.ldx + block * kMxBlock;
+    if (left >= kMxBlock) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = p[e];
+        for (int e = 0; e < 4; ++e) v[e] = reinterpret_cast<const v4u_any*>(p)[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < kMxBlock; ++e)
+            if (e < left) v[e >> 3][e >> 1 & 3] |= (uint32_t)p[e] << (16 * (e & 1));
     }
 }
 template <bool kBf16>
@@ -223,10 +230,7 @@ hipError_t launch_rows(const MxGemmArgs& g, hipStream_t stream) {
 
 bool mx4_decode_fits(int64_t m, int64_t k) { return m <= kMxDecodeRows && rows_fit(k, 0) >= 4; }
 
-bool mx4_decode_quantizes(int64_t m, int64_t k, const void* x, int64_t ldx) {
-    return m <= 4 && k > 0 && k % kMxBlock == 0 && ldx % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
-           k <= (1 << 20) && rows_fit(k, x_bytes(m, k)) >= 4;
-}
+bool mx4_decode_quantizes(int64_t m, int64_t k) { return m <= 4 && k > 0 && k <= (1 << 20) && rows_fit(k, x_bytes(m, k)) >= 4; }
 
 hipError_t launch_mx4_decode(const MxGemmArgs& g, hipStream_t stream) {
     if (g.x) return g.out_dtype == I8MP_DTYPE_BF16 ? launch_rows<2>(g, stream) : launch_rows<1>(g, stream);

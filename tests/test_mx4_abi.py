@@ -188,3 +188,11 @@ def test_rows_that_a_grid_cannot_hold(L):
     if NO_GPU:
         assert L.i8mp_mx4_quantize(A16, 0, most, 200, 200, 0, mx(rows=most), None) == EDEVICE
         assert L.i8mp_mx4_matmul(mx(rows=most), mx(), None, 0, A16, 5, A16, BIG, None) == EDEVICE
+
+
+def test_few_rows_need_no_workspace(L):
+    for k in (1, 200, 5120, 13824):
+        assert L.i8mp_mx4_linear_workspace_bytes(4, 7, k) == 0 < L.i8mp_mx4_linear_workspace_bytes(5, 7, k)
+    assert L.i8mp_mx4_linear_workspace_bytes(1, 7, 1 << 21) > 0          # more than LDS holds
+    if NO_GPU:
+        assert L.i8mp_mx4_linear(A16 + 2, 0, 4, 203, mx(rows=7), None, A16, 7, None, 0, None) == EDEVICE
