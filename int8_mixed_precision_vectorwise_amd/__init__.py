@@ -82,17 +82,17 @@ def _stream(device: torch.device):
 
 
 def _device_of(*tensors) -> torch.device:
-    dev = None
+    first = index = None
     for t in tensors:
         if t is not None:
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
+            if first is None:
+                first, index = t, t.get_device()
+            elif t.get_device() != index or (index < 0 and t.device != first.device):
                 raise ValueError("all tensors must be on one device, got "
                                  f"{sorted({str(x.device) for x in tensors if x is not None})}")
-    if dev is None or dev.type != "cuda":
-        raise ValueError(f"tensors must be on a GPU (got {dev}); there is no CPU path")
-    return dev
+    if first is None or not first.is_cuda:
+        raise ValueError(f"tensors must be on a GPU (got {None if first is None else first.device}); there is no CPU path")
+    return first.device
 
 
 def _rowmajor(t: torch.Tensor, name: str, dtype: torch.dtype) -> int:
