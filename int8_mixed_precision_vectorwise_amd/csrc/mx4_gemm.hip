@@ -34,8 +34,11 @@
 // overlap.  The 16x16x128 instruction reaches 7.2 PFLOP/s alone, but its 64 accumulators
 // of four registers left the compiler no room (100 registers spilled).
 //
-// Measured (fp16 out, operands of random bits): 4096 x 22016 x 8192 390 us before the cut
-// below, 8192 x 8192 x 16384 506 us (4.3 PFLOP/s).
+// Measured (fp16 out, operands of random bits): 4096 x 22016 x 8192 383 us in two launches
+// (3.9 PFLOP/s), 8192 x 8192 x 16384 506 (4.3 PFLOP/s), 512 x 4096 x 1024 7.7, bound by the
+// launch and the latency of four stages.
+#include <cmath>
+
 #include "common.h"
 #include "mx4.h"
 #include "mx4_util.h"
@@ -387,18 +390,26 @@ hipError_t launch_one(int f, const MxGemmArgs& g, hipStream_t stream) {
 // a time a stage that depends on how many of them share a CU.
 //   f   rows    a CU holds   fixed   a stage, with 1 .. of them on a CU
 //   4   256     1            10      1.75
-//   2   128     2            5       0.65  1.45
+//   2   128     2            5       0.65  1.35
 //   1   64      4            3.5     0.44  0.62  0.9  1.2
+// Between one and two of 128 rows a CU the waiting ones help early: 1.08 with 352 on 256 CUs, 1.11 with 384.
+// us with each shape alone, unsplit:  256 rows   128 rows   64 rows
+//    512 x  8192 x  8192                  50.7       26.1      39.4
+//    512 x 13824 x  5120                  40.7       31.5      44.4
+//    300 x 11008 x  4096                  31.7       20.2      21.6
+//    256 x 13824 x  5120                  36.9       19.0      25.0
+//   4096 x  4096 x  4096                  39.9       47.5      76.5
+// Tiles of 256 x 128, one a CU, gain 8 to 14 % where they come to just one a CU, and nothing elsewhere: not kept.
 constexpr int kShapes[3] = {4, 2, 1};
-double stage_us(int f, int64_t on_cu) {
-    static const double t4[] = {1.75}, t2[] = {0.65, 1.45}, t1[] = {0.44, 0.62, 0.9, 1.2};
-    return (f == 4 ? t4 : f == 2 ? t2 : t1)[on_cu - 1];
+double stage_us(int f, double on_cu) {
+    static const double t1[] = {0.44, 0.62, 0.9, 1.2};
+    return f == 4 ? 1.75 : f == 2 ? 0.65 + (on_cu > 1.0 ? 0.7 * std::sqrt(on_cu - 1.0) : 0.0) : t1[(int)std::ceil(on_cu) - 1];
 }
 double tiles_us(int f, int64_t units, int64_t stages) {
     const int64_t hold = f == 4 ? 1 : f == 2 ? 2 : 4;
     const double fixed = f == 4 ? 10.0 : f == 2 ? 5.0 : 3.5;
-    const int64_t full = units / (kCUs * hold), rest = ceil_div(units - full * kCUs * hold, kCUs);
-    return full * (fixed + stages * stage_us(f, hold)) + (rest ? fixed + stages * stage_us(f, rest) : 0.0);
+    const int64_t full = units / (kCUs * hold), rest = units - full * kCUs * hold;
+    return full * (fixed + stages * stage_us(f, hold)) + (rest ? fixed + stages * stage_us(f, (double)rest / kCUs) : 0.0);
 }
 
 struct Cut {   // of a product's columns: one tile shape, sums in `parts` parts of `part_stages`
