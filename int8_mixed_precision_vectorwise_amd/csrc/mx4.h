@@ -24,10 +24,10 @@ struct MxQuantArgs {
     bool columns;
     Mx4 q;
     // set by the launcher
-    bool aligned;                   // by columns: x can be read in whole words
+    bool aligned, runs;             // by columns: x can be read in whole words; each XCD gets a run of workgroups
     bool few;                       // by rows: a lane takes one row
     int32_t lane_shift;             // and lanes along a row
-    uint32_t block0, blocks_x;      // first workgroup, workgroups along a row of them
+    uint32_t block0, blocks_x, blocks_y;  // first workgroup, workgroups along a row of them and rows
 };
 constexpr int kMxJobs = 4;
 struct MxQuantJobs {
