@@ -575,7 +575,8 @@ i8mp_status i8mp_fp4_cache_append(const i8mp_fp4_cache* cache /* host */, const 
  * A [rows x k] matrix is held by rows, padded with zeros to kp = k rounded up to
  * 128: codes [rows x ldc bytes], two a byte, element 2 j in the low nibble of byte j,
  * and scales [rows x lds bytes].  i8mp_mx4_quantize writes the padding; who fills a
- * matrix by other means writes codes of 0 and any scale but 255 there. */
+ * matrix by other means writes codes of 0 and any scale but 255 there.  Outputs and the
+ * workspace share no memory with inputs. */
 #define I8MP_MX4_MAX_ROWS 67108864 /* more rows than this would leave the range of a launch's grid: I8MP_EINVAL */
 typedef struct i8mp_mx4 {
     uint8_t* codes;   /* device, 16-byte aligned                          */

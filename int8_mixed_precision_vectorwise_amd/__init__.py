@@ -884,7 +884,8 @@ def fp4_cache_append(cache: Fp4Cache, q: Optional[torch.Tensor], k: torch.Tensor
 @dataclass
 class Mx4Tensor:
     """A microscaled 4-bit matrix [rows, k] in the layout of include/i8mp.h: packed E2M1 ``codes`` uint8
-    [rows, kp / 2] and E8M0 ``scales`` uint8 [rows, kp / 32], kp = k rounded up to 128 (``create`` allocates them)."""
+    [rows, kp / 2] and E8M0 ``scales`` uint8 [rows, kp / 32], kp = k rounded up to 128 (``create`` allocates them).
+    An ``out`` of the calls that take one shares no memory with their inputs."""
 
     codes: torch.Tensor
     scales: torch.Tensor

@@ -18,6 +18,9 @@
 // Up to four rows of 16-bit x, of any alignment, are quantized here (kIn), once a workgroup into LDS, while
 // the first weights are on their way: a thread's 32 elements are one block.  That saves a
 // launch; with more rows every workgroup would read and convert too much of x.
+//
+// Measured (us, weights from memory): 13824 x 5120 by one row 10.8 (3.5 TB/s of codes and
+// scales), by 16 rows quantized before 12.6; 22016 x 8192 23.3 (4.1 TB/s) and 27.5.
 #include "common.h"
 #include "mx4.h"
 #include "mx4_util.h"
