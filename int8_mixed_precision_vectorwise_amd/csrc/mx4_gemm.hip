@@ -300,9 +300,14 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx4_gemm_kernel(MxGe
         uint8_t* const area = smem + kOutAt + wave * T::kOutArea;
         const bool whole = g.ldout * kElem % 16 == 0 && reinterpret_cast<uintptr_t>(g.out) % 16 == 0;
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+        for (int j0 = 0; j0 < FN; j0 += kTiles) {
+            v4f b[kTiles][4];
 #pragma unroll
-            for (int j0 = 0; j0 < FN; j0 += kTiles) {
+            for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) b[j][q] = *reinterpret_cast<const v4f*>(tile_bias + wn + 32 * (j0 + j) + 8 * q + 4 * hi);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
                 // so many sums at a time leave the accumulation registers
                 __builtin_amdgcn_sched_barrier(0);
                 if constexpr (T::kAhead) {
@@ -314,10 +319,9 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx4_gemm_kernel(MxGe
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int col = 32 * j + 8 * q + 4 * hi;
-                        const v4f b = *reinterpret_cast<const v4f*>(tile_bias + wn + 32 * j0 + col);
                         float v[4];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) v[r] = acc[i][j0 + j][4 * q + r] + b[r];
+                        for (int r = 0; r < 4; ++r) v[r] = acc[i][j0 + j][4 * q + r] + b[j][q][r];
                         uint8_t* p = area + l32 * kPitch + col * kElem;
                         if constexpr (kType == I8MP_DTYPE_F32) *reinterpret_cast<v4f*>(p) = v4f{v[0], v[1], v[2], v[3]};
                         else *reinterpret_cast<uint2*>(p) = make_uint2(narrow2<kType>(v[0], v[1]), narrow2<kType>(v[2], v[3]));
@@ -343,6 +347,7 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx4_gemm_kernel(MxGe
                 }
                 rows_done();
             }
+        }
         if constexpr (!T::kAhead) break;   // as many workgroups as units
     }
 #undef I8MP_MULTIPLY
