@@ -299,6 +299,11 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx4_gemm_kernel(MxGe
         uint8_t* const out = static_cast<uint8_t*>(g.out) + u.part * g.part_bytes;
         uint8_t* const area = smem + kOutAt + wave * T::kOutArea;
         const bool whole = g.ldout * kElem % 16 == 0 && reinterpret_cast<uintptr_t>(g.out) % 16 == 0;
+        const bool all = whole && u.rows_m == BM && u.rows_n == BN;
+        const int64_t pitch = g.ldout * kElem;
+        const int row0 = wm + lane / kPieces, col0 = wn + lane % kPieces * kEach;   // of the lane's first piece
+        uint8_t* const first_to = out + (u.m0 + row0) * pitch + (u.n0 + col0) * (int64_t)kElem;
+        const uint8_t* const from = area + lane / kPieces * kPitch + lane % kPieces * 16;
 #pragma unroll
         for (int j0 = 0; j0 < FN; j0 += kTiles) {
             v4f b[kTiles][4];
@@ -329,19 +334,23 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx4_gemm_kernel(MxGe
                 rows_done();
 #pragma unroll
                 for (int v = 0; v < kPieces / 2; ++v) {
-                    const int p = v * 64 + lane, row = p / kPieces, col = p % kPieces * kEach;
-                    const int r = wm + 32 * i + row, c = wn + 32 * j0 + col;
+                    constexpr int kRows = 64 / kPieces;   // of 64 lanes
+                    const v4u* const piece = reinterpret_cast<const v4u*>(from + v * kRows * kPitch);
+                    uint8_t* const to = first_to + (32 * i + v * kRows) * pitch + 32 * j0 * kElem;
+                    if (all) {
+                        *reinterpret_cast<v4u*>(to) = *piece;
+                        continue;
+                    }
+                    const int r = row0 + 32 * i + v * kRows, c = col0 + 32 * j0;
                     if (r >= u.rows_m || c >= u.rows_n) continue;
-                    const uint8_t* from = area + row * kPitch + col * kElem;
-                    uint8_t* to = out + ((int64_t)(u.m0 + r) * g.ldout + u.n0 + c) * kElem;
                     if (whole && c + kEach <= u.rows_n) {
-                        *reinterpret_cast<v4u*>(to) = *reinterpret_cast<const v4u*>(from);
+                        *reinterpret_cast<v4u*>(to) = *piece;
                     } else {
 #pragma unroll
                         for (int e = 0; e < kEach; ++e) {
                             if (c + e >= u.rows_n) break;
-                            if constexpr (kElem == 4) reinterpret_cast<uint32_t*>(to)[e] = reinterpret_cast<const uint32_t*>(from)[e];
-                            else reinterpret_cast<uint16_t*>(to)[e] = reinterpret_cast<const uint16_t*>(from)[e];
+                            if constexpr (kElem == 4) reinterpret_cast<uint32_t*>(to)[e] = reinterpret_cast<const uint32_t*>(piece)[e];
+                            else reinterpret_cast<uint16_t*>(to)[e] = reinterpret_cast<const uint16_t*>(piece)[e];
                         }
                     }
                 }
