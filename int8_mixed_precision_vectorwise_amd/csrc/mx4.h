@@ -51,6 +51,7 @@ struct MxGemmArgs {
     // set by the launcher: the sums over k in so many parts of so many stages, each with an output of its own
     int32_t parts, part_stages;
     int64_t part_bytes;
+    bool past;                      // out passes the last-level cache by
 };
 
 // Up to kMxJobs matrices of one type, in one launch; empty ones are passed over.

@@ -51,6 +51,18 @@ constexpr int kStageK = 256;             // elements of a stage
 constexpr int kRowBytes = kStageK / 2;   // its codes of a row: whole lines of the L2
 constexpr int kXcds = 8, kCUs = 256;
 
+// Whole tiles' results are stored through the L2: what is left in it is written back before a launch ends, which costs 1.6
+// to 2.5 us, and the next launch finds them in the last-level cache either way.  us of a product, and with a scaling of
+// its output after it, stored through / left in L2 / past the last-level cache:
+//   2048 x 4096 x  512 (16 MiB)    7.9 / 9.5 / 8.8      18.3 / 20.1 / 19.0
+//   4096 x 4096 x 2048 (32 MiB)    23.9 / 26.0 / 24.1   34.9 / 36.5 / 37.4
+//   8192 x 8192 x  512 (128 MiB)   42.4 / 45.6 / 47.6   82.2 / 83.0 / 89.1
+//   4096 x 22016 x 8192 (172 MiB)  366 / 367 / 360      443 / 438 / 451
+//   5000 x 22016 x 1000 (210 MiB)  99 / 109 / 103       191 / 188 / 186
+//   6607 x 22016 x 384 (277 MiB)   107 / 98 / 95        212 / 211 / 202
+constexpr int kThrough = 16, kPast = 2;          // the stores' cache policies
+constexpr int64_t kPastBytes = 256 << 20;        // the last-level cache: larger outputs pass it by
+
 // lane i's 16 bytes at `offset` land at lds + 16 i (lds is the same in every lane)
 __device__ inline void copy16(__amdgpu_buffer_rsrc_t src, uint8_t* lds, int offset) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)lds, 16, offset, 0, 0, 0);
@@ -302,6 +314,8 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx4_gemm_kernel(MxGe
         const bool all = whole && u.rows_m == BM && u.rows_n == BN;
         const int64_t pitch = g.ldout * kElem;
         const int row0 = wm + lane / kPieces, col0 = wn + lane % kPieces * kEach;   // of the lane's first piece
+        const int at0 = row0 * (int)pitch + col0 * kElem;
+        const __amdgpu_buffer_rsrc_t tile_to = range_of(out + u.m0 * pitch + u.n0 * (int64_t)kElem, (BM - 1) * (int)pitch + BN * kElem);
         uint8_t* const first_to = out + (u.m0 + row0) * pitch + (u.n0 + col0) * (int64_t)kElem;
         const uint8_t* const from = area + lane / kPieces * kPitch + lane % kPieces * 16;
 #pragma unroll
@@ -338,7 +352,9 @@ __global__ __launch_bounds__(256, FM * FN > 8 ? 1 : 2) void mx4_gemm_kernel(MxGe
                     const v4u* const piece = reinterpret_cast<const v4u*>(from + v * kRows * kPitch);
                     uint8_t* const to = first_to + (32 * i + v * kRows) * pitch + 32 * j0 * kElem;
                     if (all) {
-                        *reinterpret_cast<v4u*>(to) = *piece;
+                        const int step = (32 * i + v * kRows) * (int)pitch + 32 * j0 * kElem;
+                        if (g.past) __builtin_amdgcn_raw_buffer_store_b128(*piece, tile_to, at0, step, kPast);
+                        else __builtin_amdgcn_raw_buffer_store_b128(*piece, tile_to, at0, step, kThrough);
                         continue;
                     }
                     const int r = row0 + 32 * i + v * kRows, c = col0 + 32 * j0;
@@ -495,6 +511,7 @@ hipError_t launch_mx4_gemm_pair(const MxGemmArgs& a, const MxGemmArgs& b, hipStr
         g->parts = 1;
         g->part_stages = (int)ceil_div(g->a.k, kStageK);
         g->part_bytes = 0;
+        g->past = g->a.rows * g->b.rows * 2 > kPastBytes;
     }
     const auto tiles = [](const MxGemmArgs& g, int f) { return ceil_div(g.a.rows, 64 * f) * ceil_div(g.b.rows, 64 * f); };
     const bool bf16 = x.out_dtype == I8MP_DTYPE_BF16;
@@ -527,6 +544,7 @@ hipError_t launch_mx4_gemm(const MxGemmArgs& args, hipStream_t stream) {
     g.parts = 1;
     g.part_stages = (int)ceil_div(k, kStageK);
     g.part_bytes = 0;
+    g.past = m * n * elem > kPastBytes;
     if (p.n_main > 0) {
         g.b.rows = p.n_main;
         if (hipError_t e = launch_one(4, g, stream); e != hipSuccess) return e;
@@ -546,6 +564,7 @@ hipError_t launch_mx4_gemm(const MxGemmArgs& args, hipStream_t stream) {
     s.parts = g.parts = p.rest.parts;
     s.part_stages = (int)p.rest.part_stages;
     s.part_bytes = g.part_bytes = m * ldp * 4;
+    s.past = false;
     if (hipError_t e = launch_one(p.rest.f, s, stream); e != hipSuccess) return e;
     const dim3 grid((unsigned)ceil_div(m * ldp / 4, 256));
     if (g.out_dtype == I8MP_DTYPE_F32) hipLaunchKernelGGL((mx4_join_kernel<I8MP_DTYPE_F32>), grid, dim3(256), 0, stream, g, g.part, ldp);
