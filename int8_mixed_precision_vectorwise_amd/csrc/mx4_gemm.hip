@@ -416,30 +416,33 @@ hipError_t launch_one(int f, const MxGemmArgs& g, hipStream_t stream) {
 }
 
 // ---- which tiles -----------------------------------------------------------------
-// A cost model in us, fitted to timed products: a tile of 64 f costs a fixed time, and
-// a time a stage that depends on how many of them share a CU.
+// A cost model in us, fitted to timed products: a launch starts in 2; a tile of 64 f costs a
+// fixed time, and a time a stage that depends on how many of them share a CU.
 //   f   rows    a CU holds   fixed   a stage, with 1 .. of them on a CU
-//   4   256     1            10      1.75
-//   2   128     2            5       0.65  1.35
-//   1   64      4            3.5     0.44  0.62  0.9  1.2
+//   4   256     1            7       1.75
+//   2   128     2            3       0.65  1.35
+//   1   64      4            1.8     0.44  0.62  0.9  1.2
 // Between one and two of 128 rows a CU the waiting ones help early: 1.08 with 352 on 256 CUs, 1.11 with 384.
 // us with each shape alone, unsplit:  256 rows   128 rows   64 rows
 //    512 x  8192 x  8192                  50.7       26.1      39.4
-//    512 x 13824 x  5120                  40.7       31.5      44.4
-//    300 x 11008 x  4096                  31.7       20.2      21.6
-//    256 x 13824 x  5120                  36.9       19.0      25.0
-//   4096 x  4096 x  4096                  39.9       47.5      76.5
+//    646 x  4096 x  5120                  33.9       15.7      20.1
+//     64 x 13824 x  5120                  32.9       16.3      12.7
+//   3663 x 22016 x  1435                   110        108       160
+//   4096 x  4096 x  2048                  22.9       26.9      42.1
+//   5673 x  5120 x 11008                   164        217       351
 // Tiles of 256 x 128, one a CU, gain 8 to 14 % where they come to just one a CU, and nothing elsewhere: not kept.
 constexpr int kShapes[3] = {4, 2, 1};
+constexpr double kStart = 2.0;
 double stage_us(int f, double on_cu) {
     static const double t1[] = {0.44, 0.62, 0.9, 1.2};
     return f == 4 ? 1.75 : f == 2 ? 0.65 + (on_cu > 1.0 ? 0.7 * std::sqrt(on_cu - 1.0) : 0.0) : t1[(int)std::ceil(on_cu) - 1];
 }
-double tiles_us(int f, int64_t units, int64_t stages) {
+double fixed_us(int f) { return f == 4 ? 7.0 : f == 2 ? 3.0 : 1.8; }
+double tiles_us(int f, int64_t units, double stages) {
     const int64_t hold = f == 4 ? 1 : f == 2 ? 2 : 4;
-    const double fixed = f == 4 ? 10.0 : f == 2 ? 5.0 : 3.5;
     const int64_t full = units / (kCUs * hold), rest = units - full * kCUs * hold;
-    return full * (fixed + stages * stage_us(f, hold)) + (rest ? fixed + stages * stage_us(f, (double)rest / kCUs) : 0.0);
+    return kStart + full * (fixed_us(f) + stages * stage_us(f, hold)) +
+           (rest ? fixed_us(f) + stages * stage_us(f, (double)rest / kCUs) : 0.0);
 }
 
 struct Cut {   // of a product's columns: one tile shape, sums in `parts` parts of `part_stages`
@@ -458,8 +461,9 @@ Cut best_cut(int64_t m, int64_t n, int64_t k) {
             const int64_t per = ceil_div(stages, parts);
             if (ceil_div(stages, per) != parts) continue;
             if (parts > 1 && tiles * parts > 4 * kCUs) break;
-            double us = tiles_us(f, tiles * parts, per);
-            if (parts > 1) us += 4.0 + (double)m * n * 8 * parts / 4.0e6;   // written and read at 4 TB/s
+            double us = tiles_us(f, tiles * parts, (double)per);
+            // a second launch, on the host too, and the parts through the last-level cache at 10 TB/s
+            if (parts > 1) us += 5.0 + 0.2 * parts + (double)m * n * 8 * parts / 1.0e7;
             if (us < best.us) best = Cut{f, parts, per, us};
         }
     }
@@ -479,7 +483,7 @@ Plan plan(int64_t m, int64_t n, int64_t k) {
     const int64_t n_main = cols * 256, stages = ceil_div(k, kStageK);
     if (cols > 0 && n_main < n) {
         const Cut rest = best_cut(m, n - n_main, k);
-        const double us = tiles_us(4, rows * cols, stages) + 3.0 + rest.us;
+        const double us = tiles_us(4, rows * cols, (double)stages) + 1.0 + rest.us;
         if (us < 0.98 * whole.us) p = Plan{n_main, rest, us};
     }
     return p;
@@ -494,11 +498,11 @@ size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k) {
     return p.rest.parts > 1 ? (size_t)p.rest.parts * m * part_row(n - p.n_main) * 4 : 0;
 }
 
-// Two products of one type in one launch, where one alone leaves workgroups idle or both are small:
-// - each one cut of 64 x 64 tiles: all tiles, those of the longer sums first.  Gradients of 512 x 4096 x 1024: 12.5 us, one
+// Two products of one type in one launch, where the model finds that to beat one after the other:
+// - by 64 x 64 tiles, all of them, those of the longer sums first.  Gradients of 512 x 4096 x 1024: 12.5 us, one
 //   after the other 17.3.
-// - by 256 x 256 tiles, where the model finds a share of the workgroups for each that beats two launches.  Gradients
-//   of 2048 x 4096 x 4096 (128 tiles of 16 stages, 256 of 8): 50.9 us, one after the other 54.4.
+// - by 256 x 256 tiles, a share of the workgroups each.  Gradients of 2048 x 4096 x 4096 (128 tiles of 16 stages, 256
+//   of 8): 50.9 us, one after the other 54.4.
 template <int F, int kType>
 hipError_t launch_pair(const MxGemmArgs& x, const MxGemmArgs& y, int64_t split, int64_t all, hipStream_t stream) {
     hipLaunchKernelGGL((mx4_gemm_kernel<F, F, kType, true>), dim3((unsigned)all), dim3(256), 0, stream, x, y, (uint32_t)split);
@@ -517,20 +521,21 @@ hipError_t launch_mx4_gemm_pair(const MxGemmArgs& a, const MxGemmArgs& b, hipStr
     const bool bf16 = x.out_dtype == I8MP_DTYPE_BF16;
     if (!mx4_decode_fits(x.a.rows, x.a.k) && !mx4_decode_fits(y.a.rows, y.a.k)) {
         const Plan px = plan(x.a.rows, x.b.rows, x.a.k), py = plan(y.a.rows, y.b.rows, y.a.k);
-        const auto small = [](const Plan& p) { return p.n_main == 0 && p.rest.f == 1 && p.rest.parts == 1; };
-        if (small(px) && small(py)) {
-            const int64_t tx = tiles(x, 1), all = tx + tiles(y, 1);
-            return bf16 ? launch_pair<1, I8MP_DTYPE_BF16>(x, y, tx, all, stream) : launch_pair<1, I8MP_DTYPE_F16>(x, y, tx, all, stream);
-        }
+        double best = 0.98 * (px.us + 1.0 + py.us);
+        const int64_t sx = tiles(x, 1), all = sx + tiles(y, 1);
+        const double mean = ((double)sx * x.part_stages + (double)(all - sx) * y.part_stages) / all;
+        const double longest = kStart + fixed_us(1) + x.part_stages * stage_us(1, 2.0), together = tiles_us(1, all, mean);
+        const bool small = (longest > together ? longest : together) < best;
+        if (small) best = longest > together ? longest : together;
         // whole XCDs' turns each: a workgroup's tiles stay on its XCD
         const int64_t tx = tiles(x, 4), ty = tiles(y, 4);
         int64_t split = 0;
-        double best = 0.98 * (px.us + 3.0 + py.us);
         for (int64_t s = kXcds; s < kCUs; s += kXcds) {
             const double ux = tiles_us(4, ceil_div(tx, s) * kCUs, x.part_stages), uy = tiles_us(4, ceil_div(ty, kCUs - s) * kCUs, y.part_stages);
             if ((ux > uy ? ux : uy) < best) best = ux > uy ? ux : uy, split = s;
         }
         if (split > 0) return bf16 ? launch_pair<4, I8MP_DTYPE_BF16>(x, y, split, kCUs, stream) : launch_pair<4, I8MP_DTYPE_F16>(x, y, split, kCUs, stream);
+        if (small) return bf16 ? launch_pair<1, I8MP_DTYPE_BF16>(x, y, sx, all, stream) : launch_pair<1, I8MP_DTYPE_F16>(x, y, sx, all, stream);
     }
     if (hipError_t e = launch_mx4_gemm(a, stream); e != hipSuccess) return e;
     return launch_mx4_gemm(b, stream);
