@@ -34,9 +34,12 @@
 // overlap.  The 16x16x128 instruction reaches 7.2 PFLOP/s alone, but its 64 accumulators
 // of four registers left the compiler no room (100 registers spilled).
 //
-// Measured (fp16 out, operands of random bits): 4096 x 22016 x 8192 383 us in two launches
-// (3.9 PFLOP/s), 8192 x 8192 x 16384 506 (4.3 PFLOP/s), 512 x 4096 x 1024 7.7, bound by the
-// launch and the latency of four stages.
+// A tile's results pass through LDS: the bias of its columns waits in registers (read from
+// LDS beside them it cost 2 us a tile), whole tiles leave by one address and fixed steps.
+//
+// Measured (fp16 out, operands of random numbers, us): 4096 x 22016 x 8192 376 in two
+// launches (3.9 PFLOP/s), 8192 x 8192 x 16384 505 (4.4), 8192 x 8192 x 512 42, 512 x 4096 x
+// 1024 5.7, bound by the launch and the latency of four stages.
 #include <cmath>
 
 #include "common.h"
@@ -499,10 +502,10 @@ size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k) {
 }
 
 // Two products of one type in one launch, where the model finds that to beat one after the other:
-// - by 64 x 64 tiles, all of them, those of the longer sums first.  Gradients of 512 x 4096 x 1024: 12.5 us, one
-//   after the other 17.3.
+// - by 64 x 64 tiles, all of them, those of the longer sums first.  Gradients of 512 x 4096 x 1024: 12.4 us, one
+//   after the other 16.8.
 // - by 256 x 256 tiles, a share of the workgroups each.  Gradients of 2048 x 4096 x 4096 (128 tiles of 16 stages, 256
-//   of 8): 50.9 us, one after the other 54.4.
+//   of 8): 46.9 us, one after the other 52.3.
 template <int F, int kType>
 hipError_t launch_pair(const MxGemmArgs& x, const MxGemmArgs& y, int64_t split, int64_t all, hipStream_t stream) {
     hipLaunchKernelGGL((mx4_gemm_kernel<F, F, kType, true>), dim3((unsigned)all), dim3(256), 0, stream, x, y, (uint32_t)split);
