@@ -1049,12 +1049,15 @@ i8mp_status i8mp_mx4_linear_backward(const void* grad_out, int64_t ldg, const vo
     g.part = reinterpret_cast<float*>(base + at);
     MxQuantArgs jobs[kMxJobs];
     int count = 0;
+    const bool both = want_x && want_w && mx4_quantize_both(m, n);
     if (want_x) {
-        jobs[count++] = mx4_quant(grad_out, ldg, dtype, false, g_rows);
+        if (!both) jobs[count++] = mx4_quant(grad_out, ldg, dtype, false, g_rows);
         jobs[count++] = mx4_quant(w, ldw, dtype, true, w_cols);
     }
     if (want_w) {
-        jobs[count++] = mx4_quant(grad_out, ldg, dtype, true, g_cols);
+        jobs[count] = mx4_quant(grad_out, ldg, dtype, true, g_cols);
+        if (both) jobs[count].rows = g_rows;
+        ++count;
         jobs[count++] = mx4_quant(x, ldx, dtype, true, x_cols);
     }
     if (i8mp_status s = launched(launch_mx4_quantize(jobs, count, stream)); s != I8MP_OK) return s;

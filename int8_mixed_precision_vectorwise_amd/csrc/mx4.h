@@ -23,6 +23,7 @@ struct MxQuantArgs {
     bool bf16;
     bool columns;
     Mx4 q;
+    Mx4 rows;                       // with `columns`, where its codes are given: x quantized by rows beside it
     // set by the launcher
     bool aligned, runs;             // by columns: x can be read in whole words; each XCD gets a run of workgroups
     bool few;                       // by rows: a lane takes one row
@@ -56,6 +57,8 @@ struct MxGemmArgs {
 
 // Up to kMxJobs matrices of one type, in one launch; empty ones are passed over.
 hipError_t launch_mx4_quantize(const MxQuantArgs* args, int count, hipStream_t stream);
+// whether a matrix that is wanted by rows and by columns is better quantized by one job (MxQuantArgs::rows) than by two
+bool mx4_quantize_both(int64_t rows, int64_t cols);
 hipError_t launch_mx4_dequantize(const MxDequantArgs& a, hipStream_t stream);
 // workspace of a product of these sizes (0: none needed)
 size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k);

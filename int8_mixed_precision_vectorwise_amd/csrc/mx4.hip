@@ -85,8 +85,49 @@ __device__ inline void quantize_rows(const MxQuantArgs& a, uint32_t bx, uint32_t
 // bytes.
 constexpr int kColCols = 128, kColRows = 32 * kThreads / 64, kColPitch = kColRows / 2 + 16;
 
-template <bool kBf16, bool kAligned>
-__device__ inline void quantize_columns(const MxQuantArgs& a, uint32_t bx, uint32_t by, uint8_t* codes, uint32_t* scales) {
+// Every lane's dword, the bytes of four rows in turn, becomes one row's bytes of the quad's four lanes
+__device__ inline uint32_t transpose4(uint32_t d) {
+    const bool upper = threadIdx.x & 2, odd = threadIdx.x & 1;
+    d = __builtin_amdgcn_perm((uint32_t)dpp_i32<kDppQuadSwap2>((int32_t)d), d, upper ? 0x03020706u : 0x05040100u);
+    return __builtin_amdgcn_perm((uint32_t)dpp_i32<kDppQuadSwap1>((int32_t)d), d, odd ? 0x03070105u : 0x06020400u);
+}
+
+// The same 32 rows of two columns a lane, quantized by rows: a block is a row of 16 lanes.  Two rows' maxima share a
+// register; a lane has one byte of codes a row, and quads of lanes exchange them into words.
+template <bool kBf16>
+__device__ inline void quantize_beside(const MxQuantArgs& a, const uint32_t (&x)[kMxBlock], int64_t c0, int64_t r0, uint8_t* scales) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t kept[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < kMxBlock; i += 4) {
+        uint32_t codes = 0;
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            const uint32_t u = x[i + j], v = x[i + j + 1];
+            us2 m = __builtin_elementwise_max(mags(__builtin_amdgcn_perm(v, u, 0x05040100u)), mags(__builtin_amdgcn_perm(v, u, 0x07060302u)));
+            const auto with = [&](uint32_t other) { m = __builtin_elementwise_max(m, __builtin_bit_cast(us2, other)); };
+            with((uint32_t)dpp_i32<kDppQuadSwap1>(__builtin_bit_cast(int32_t, m)));
+            with((uint32_t)dpp_i32<kDppQuadSwap2>(__builtin_bit_cast(int32_t, m)));
+            with((uint32_t)dpp_i32<kDppHalfMirror>(__builtin_bit_cast(int32_t, m)));
+            with((uint32_t)dpp_i32<kDppRowMirror>(__builtin_bit_cast(int32_t, m)));
+            const uint32_t b0 = scale_byte<kBf16>(m.x), b1 = scale_byte<kBf16>(m.y);
+            const uint32_t both = (b0 == 255u ? 0u : encode2<kBf16, 0>(0u, u, scale_value(b0))) |
+                                  (b1 == 255u ? 0u : encode2<kBf16, 0>(0u, v, scale_value(b1)) << 8);
+            codes |= both << (8 * j);
+            if ((lane & 15) == ((i + j) & 15)) kept[(i + j) >> 4] = b0;
+            if ((lane & 15) == ((i + j + 1) & 15)) kept[(i + j) >> 4] = b1;
+        }
+        codes = transpose4(codes);
+        const int64_t r = r0 + i + (lane & 3);
+        if (r < a.rows.rows) *reinterpret_cast<uint32_t*>(a.rows.codes + r * a.rows.ldc + c0 / 2 + (lane & ~3)) = codes;
+        __builtin_amdgcn_sched_barrier(0);   // four rows in registers at a time
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) scales[(wave * kMxBlock + 16 * h + (lane & 15)) * 4 + (lane >> 4)] = (uint8_t)kept[h];
+}
+
+template <bool kBf16, bool kAligned, bool kBeside>
+__device__ inline void quantize_columns(const MxQuantArgs& a, uint32_t bx, uint32_t by, uint8_t* codes, uint32_t* scales, uint32_t* row_scales) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t c0 = (int64_t)bx * kColCols, c = c0 + 2 * lane;
     const int64_t r0 = (int64_t)by * kColRows + wave * kMxBlock;
@@ -113,6 +154,7 @@ __device__ inline void quantize_columns(const MxQuantArgs& a, uint32_t bx, uint3
             else if (one) x[i] = p[i * a.ldx];
         }
     }
+    if (kBeside && a.rows.codes) quantize_beside<kBf16>(a, x, c0, r0, reinterpret_cast<uint8_t*>(row_scales));
     us2 m = mags(x[0]);
 #pragma unroll
     for (int i = 1; i < kMxBlock; ++i) m = __builtin_elementwise_max(m, mags(x[i]));
@@ -148,6 +190,9 @@ __device__ inline void quantize_columns(const MxQuantArgs& a, uint32_t bx, uint3
     }
     if (threadIdx.x < kColCols && c0 + threadIdx.x < a.q.rows)
         *reinterpret_cast<uint32_t*>(a.q.scales + (c0 + threadIdx.x) * a.q.lds + first) = scales[threadIdx.x];
+    const int64_t row = (int64_t)by * kColRows + threadIdx.x;
+    if (kBeside && a.rows.codes && threadIdx.x < kColRows && row < a.rows.rows)
+        *reinterpret_cast<uint32_t*>(a.rows.scales + row * a.rows.lds + c0 / kMxBlock) = row_scales[threadIdx.x];
 }
 
 // Workgroups go to the XCDs in turn; each XCD gets a run of neighbours, two along the rows of x at a time, so that
@@ -166,11 +211,12 @@ __device__ inline void column_place(uint32_t id, uint32_t blocks_x, uint32_t blo
     bx = __builtin_amdgcn_readfirstlane(two ? in >> 1 : in);
 }
 
-// Up to kMxJobs matrices in one launch: each has its run of workgroups.
-template <bool kBf16>
+// Up to kMxJobs matrices in one launch: each has its run of workgroups.  kBeside: one of them by rows and by columns at
+// once, which takes 88 registers in place of 47.
+template <bool kBf16, bool kBeside>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(MxQuantJobs jobs) {
     __shared__ __attribute__((aligned(16))) uint8_t codes[kColCols * kColPitch];
-    __shared__ uint32_t scales[kColCols];
+    __shared__ uint32_t scales[kColCols], row_scales[kColRows];
     int j = 0;
 #pragma unroll
     for (int i = 1; i < kMxJobs; ++i) j += i < jobs.count && blockIdx.x >= jobs.job[i].block0;
@@ -179,8 +225,8 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(MxQuantJobs jobs) {
     uint32_t by = id / a.blocks_x, bx = id - by * a.blocks_x;
     if (a.columns) {
         if (a.runs) column_place(id, a.blocks_x, a.blocks_y, bx, by);
-        if (a.aligned) quantize_columns<kBf16, true>(a, bx, by, codes, scales);
-        else quantize_columns<kBf16, false>(a, bx, by, codes, scales);
+        if (a.aligned) quantize_columns<kBf16, true, kBeside>(a, bx, by, codes, scales, row_scales);
+        else quantize_columns<kBf16, false, kBeside>(a, bx, by, codes, scales, row_scales);
     } else {
         if (a.few) quantize_rows<kBf16, 1>(a, bx, by);
         else quantize_rows<kBf16, kRowSteps>(a, bx, by);
@@ -313,10 +359,16 @@ int64_t set_blocks(MxQuantArgs& a) {
     return x * y;
 }
 
-hipError_t launch_jobs(const MxQuantJobs& jobs, int64_t blocks, bool bf16, hipStream_t stream) {
-    if (bf16) hipLaunchKernelGGL((quantize_kernel<true>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, jobs);
-    else hipLaunchKernelGGL((quantize_kernel<false>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, jobs);
+template <bool kBeside>
+hipError_t launch_kind(const MxQuantJobs& jobs, int64_t blocks, bool bf16, hipStream_t stream) {
+    if (bf16) hipLaunchKernelGGL((quantize_kernel<true, kBeside>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, jobs);
+    else hipLaunchKernelGGL((quantize_kernel<false, kBeside>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, jobs);
     return hipGetLastError();
+}
+hipError_t launch_jobs(const MxQuantJobs& jobs, int64_t blocks, bool bf16, hipStream_t stream) {
+    bool beside = false;
+    for (int i = 0; i < jobs.count; ++i) beside = beside || jobs.job[i].rows.codes;
+    return beside ? launch_kind<true>(jobs, blocks, bf16, stream) : launch_kind<false>(jobs, blocks, bf16, stream);
 }
 
 // One matrix of more workgroups than a launch takes: rows of it at a time.
@@ -334,6 +386,11 @@ hipError_t in_pieces(const MxQuantArgs& args, hipStream_t stream) {
         (args.columns ? a.q.k : a.q.rows) = all - r < most ? all - r : most;
         a.q.codes += args.columns ? r / 2 : r * a.q.ldc;
         a.q.scales += args.columns ? r / kMxBlock : r * a.q.lds;
+        if (a.rows.codes) {
+            a.rows.codes += r * a.rows.ldc;
+            a.rows.scales += r * a.rows.lds;
+            a.rows.rows = a.q.k;
+        }
         MxQuantJobs jobs{};
         jobs.job[0] = a;
         jobs.count = 1;
@@ -359,6 +416,11 @@ hipError_t dequantize(const MxDequantArgs& args, hipStream_t stream) {
 }
 
 }  // namespace
+
+// Rows and columns at once save a read of x, and a wave works longer on what it has read: us of a backward, at once /
+// apart: 7189 x 11008 x 1024 (4902 workgroups) 177 / 202, 5673 x 11008 x 5120 (3870) 424 / 447, 2048 x 4096 x 4096 (512)
+// 69.0 / 70.1, 512 x 4096 x 1024 (128) 21.1 / 19.8, 100 x 300 x 200 (3) 10.0 / 7.2.
+bool mx4_quantize_both(int64_t rows, int64_t cols) { return ceil_div(rows, kColRows) * ceil_div(cols, kColCols) >= 512; }
 
 hipError_t launch_mx4_quantize(const MxQuantArgs* args, int count, hipStream_t stream) {
     MxQuantJobs jobs{};

@@ -358,6 +358,29 @@ def test_linear_backward_at_size(case, kind):
         assert bool(((got.double() - want).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("m,n,pitch", [(3000, 2701, 2701), (2500, 4096, 4100), (8000, 1100, 1128)])
+def test_grad_out_by_rows_and_by_columns_at_once(m, n, pitch, kind):
+    """A large grad_out is quantized both ways in one pass: every code shows in products with rows that are one block each."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    g = torch.randn((m, pitch), generator=gen, device="cuda").mul_(torch.exp2(torch.randint(-3, 4, (m, 1), generator=gen, device="cuda")))
+    g = g.to(DTYPE[kind])[:, :n]
+    g[5, 64:96], g[64:96, 7] = 0.0, 0.0
+    g[m - 1, n - 1], g[9, 200] = float("nan"), float("inf")
+    say(f"mx4_linear_backward both ways {m} {n} {kind}")
+    x, w = (torch.randn((r, 24), generator=gen, device="cuda").to(DTYPE[kind]) for r in (m, n))
+    gx, gw = i8.mx4_linear_backward(g, x, w)
+    one = i8.mx4_linear_backward(g, None, w, need_grad_w=False)[0], i8.mx4_linear_backward(g, x, None, need_grad_x=False)[1]
+    back = lambda t, columns: i8.mx4_dequantize(i8.mx4_quantize(t, columns), torch.float32).double()
+    for got, a, b, same in ((gx, back(g, False), back(w, True), one[0]), (gw, back(g, True), back(x, True), one[1])):
+        bad = a.isnan().any(1)
+        assert int(bad.sum()) == 2 and bool(got[bad].isnan().all()) and bool(same[bad].isnan().all())
+        want, size = a[~bad] @ b.t(), a[~bad].abs() @ b.abs().t()
+        tol = (-(-a.shape[1] // 128) * 2 + 64) * 2.0 ** -23 * size + torch.finfo(DTYPE[kind]).eps / 2 * want.abs() + STEP[kind]
+        for t in (got, same):
+            assert bool(((t[~bad].double() - want).abs() <= tol).all())
+
+
 def test_gradients_are_differences_of_the_linear():
     """Where every operand is on the 4-bit grid, the linear is linear and its gradients are its differences."""
     rng = np.random.default_rng(88)
