@@ -224,6 +224,20 @@ def test_matmul_exact_sums_large(case):
     assert torch.equal(i8.mx4_matmul(qa, qb, bias.bfloat16(), torch.bfloat16), (want + bias).bfloat16())
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+def test_outputs_larger_than_the_last_level_cache(kind):
+    """Such results are stored another way; sums of whole quarters, exact in fp32."""
+    m, n, k = 8500, 16904, 90
+    gen = torch.Generator(device="cuda").manual_seed(96)
+    grid = torch.tensor(np.concatenate([mx4.GRID, -mx4.GRID]), dtype=torch.float32, device="cuda")
+    x, w = (grid[torch.randint(0, 16, (r, k), generator=gen, device="cuda")] for r in (m, n))
+    for t in (x, w):
+        t[:, ::32] = 6.0                                       # every block's scale is 1
+    say(f"mx4_matmul past the cache {kind}")
+    got = i8.mx4_matmul(i8.mx4_quantize(x.half()), i8.mx4_quantize(w.half()), dtype=DTYPE[kind])
+    assert torch.equal(got, (x @ w.t()).to(DTYPE[kind]))
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 60, 600), (4, 90, 1152), (16, 40, 128), (40, 300, 600), (200, 260, 384), (800, 900, 640)])
 def test_a_neighbours_scales_are_not_read_as_a_rows_own(m, n, k):
     """Rows that end in the middle of a stage of 256, beside rows that begin with a block that is no number."""
