@@ -895,9 +895,10 @@ i8mp_status i8mp_fp4_cache_append(const i8mp_fp4_cache* cache, const i8mp_fp4_ap
 }
 
 namespace {
-// the internal form of a quantized matrix, if its sizes are in range; `filled` also looks at the pointers
+// the internal form of a quantized matrix, if its sizes are in range (mx4_data looks at its pointers)
 bool mx4(const i8mp_mx4* p, Mx4* q) {
-    if (!p || p->rows < 0 || p->rows > I8MP_MX4_MAX_ROWS || p->k < 0 || p->ldc > I8MP_MAX_LD || p->lds > I8MP_MAX_LD) return false;
+    if (!p || p->rows < 0 || p->rows > I8MP_MX4_MAX_ROWS || p->ldc > I8MP_MAX_LD || p->lds > I8MP_MAX_LD) return false;
+    if (p->k < 0 || p->k > 2 * I8MP_MAX_LD) return false;   // else more than ldc holds, and near 2^63 kp would leave 64 bits
     *q = Mx4{p->codes, p->ldc, p->scales, p->lds, p->rows, p->k};
     return p->ldc % 16 == 0 && p->lds % 4 == 0 && p->ldc >= q->kp() / 2 && p->lds >= q->kp() / kMxBlock;
 }

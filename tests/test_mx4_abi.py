@@ -196,3 +196,18 @@ def test_few_rows_need_no_workspace(L):
     assert L.i8mp_mx4_linear_workspace_bytes(1, 7, 1 << 21) > 0          # more than LDS holds
     if NO_GPU:
         assert L.i8mp_mx4_linear(A16 + 2, 0, 4, 203, mx(rows=7), None, A16, 7, None, 0, None) == EDEVICE
+
+
+def test_rows_whose_padded_length_leaves_64_bits(L):
+    """k + 127 past 2^63 would be a small padded length, which any matrix holds."""
+    top = (1 << 63) - 1
+    for k in (top, top - 126, top - 127, (1 << 21) + 1):
+        a, wide = mx(k=k), dict(ldc=1 << 20, lds=1 << 20)
+        for m in (a, mx(k=k, **wide)):
+            assert L.i8mp_mx4_quantize(A16, 0, 5, k, k, 0, m, None) == EINVAL, k
+            assert L.i8mp_mx4_quantize(A16, 0, k, 5, 5, 1, m, None) == EINVAL, k
+            assert L.i8mp_mx4_dequantize(m, 0, A16, k, None) == EINVAL, k
+            assert L.i8mp_mx4_matmul(m, m, None, 0, A16, 5, A16, BIG, None) == EINVAL, k
+            assert L.i8mp_mx4_linear(A16, 0, 5, k, m, None, A16, 5, A16, BIG, None) == EINVAL, k
+    if NO_GPU:
+        assert L.i8mp_mx4_quantize(A16, 0, 5, 1 << 21, 1 << 21, 0, mx(k=1 << 21, **wide), None) == EDEVICE
