@@ -858,6 +858,7 @@ def fp4_cache_append(cache: Fp4Cache, q: Optional[torch.Tensor], k: torch.Tensor
         raise ValueError("cos and sin differ in shape")
     if rows == 0:
         raise ValueError("cos and sin have no rows")
+    _int32(rotary=2 * half)
     ldq = hsq = ldo = hso = heads = 0
     if q is not None:
         ldq, hsq = _heads(q, "q", cache.dtype, None, c.head_dim)

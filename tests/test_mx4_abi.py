@@ -211,3 +211,18 @@ def test_rows_whose_padded_length_leaves_64_bits(L):
             assert L.i8mp_mx4_linear(A16, 0, 5, k, m, None, A16, 5, A16, BIG, None) == EINVAL, k
     if NO_GPU:
         assert L.i8mp_mx4_quantize(A16, 0, 5, 1 << 21, 1 << 21, 0, mx(k=1 << 21, **wide), None) == EDEVICE
+
+
+def test_tables_wider_than_the_c_call_can_say(monkeypatch):
+    """ctypes keeps an int's low 32 bits: tables of 2^31 + 64 columns would turn 128 dims."""
+    def refuse(*a):
+        raise AssertionError("the call must not reach the library")
+
+    monkeypatch.setattr(i8, "_device_of", lambda *t: torch.device("cuda", 0))
+    monkeypatch.setattr(i8, "_run", refuse)
+    c = i8.Fp4Cache.create(2, 1, 128, 16, device="cpu")
+    h, i = torch.zeros((1, 1, 128), dtype=torch.float16), torch.zeros(1, dtype=torch.int64)
+    for half in ((1 << 31) + 64, 1 << 30):
+        t = torch.empty((1, half), device="meta")
+        with pytest.raises(ValueError, match="rotary is out of range"):
+            i8.fp4_cache_append(c, h, h, h, i, i, t, t)
