@@ -14,6 +14,8 @@
 
 using namespace i8mp;
 
+extern "C" int64_t i8mp_launch_blocks = (int64_t)1 << 22;
+
 namespace {
 
 constexpr size_t kAlign = 256;

@@ -517,13 +517,14 @@ int64_t move_blocks(const KvMoveArgs& a, int64_t tokens) {
     return per >= kThreads ? quads * ceil_div(per, kThreads) : ceil_div(quads, kThreads / per);
 }
 
-// Tokens in launches of at most 2^22 workgroups (a grid holds fewer than 2^32 lanes), and 2^22 more with `beside`
-// lanes a token.
+// Tokens in launches of at most i8mp_launch_blocks workgroups, and as many more with `beside` lanes a token: whole spans.
 template <typename F>
 hipError_t in_pieces(const KvMoveArgs& args, int elem, int64_t beside, F launch) {
     const int64_t per = ceil_div((int64_t)args.c.heads * 8 * args.c.blocks, kThreads);
-    int64_t most = ((int64_t)1 << 22) / per / (kSpan / kQuad + 1) * kSpan;
-    if (most * beside > (int64_t)1 << 30) most = ((int64_t)1 << 30) / beside / kSpan * kSpan;
+    const int64_t lanes = i8mp_launch_blocks * kThreads;
+    int64_t most = i8mp_launch_blocks / per / (kSpan / kQuad + 1) * kSpan;
+    if (most * beside > lanes) most = lanes / beside / kSpan * kSpan;
+    if (most < kSpan) most = kSpan;
     for (int64_t t = 0; t < args.tokens; t += most) {
         KvMoveArgs a = args;
         a.tokens = args.tokens - t < most ? args.tokens - t : most;

@@ -336,8 +336,6 @@ hipError_t by_rows(int64_t rows, int64_t chunks, F launch) {
     return hipSuccess;
 }
 
-constexpr int64_t kMaxBlocks = 1 << 22;   // of a launch: a grid holds fewer than 2^32 lanes
-
 // the workgroups of a matrix
 int64_t set_blocks(MxQuantArgs& a) {
     int64_t x, y;
@@ -376,7 +374,7 @@ hipError_t in_pieces(const MxQuantArgs& args, hipStream_t stream) {
     const int64_t all = args.columns ? args.q.k : args.q.rows;
     MxQuantArgs a = args;
     int64_t most = all;
-    while (set_blocks(a) > kMaxBlocks) {
+    while (set_blocks(a) > i8mp_launch_blocks && most > kMxPad) {
         most = round_up(most / 2, kMxPad);
         (args.columns ? a.q.k : a.q.rows) = most;
     }
@@ -430,7 +428,7 @@ hipError_t launch_mx4_quantize(const MxQuantArgs* args, int count, hipStream_t s
         MxQuantArgs& a = jobs.job[jobs.count];
         a = args[i];
         const int64_t more = set_blocks(a);
-        if (more > kMaxBlocks / kMxJobs) {
+        if (more > i8mp_launch_blocks / kMxJobs) {
             if (hipError_t e = in_pieces(args[i], stream); e != hipSuccess) return e;
             continue;
         }
