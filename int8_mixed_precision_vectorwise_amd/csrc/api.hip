@@ -10,6 +10,7 @@
 #include "backward.h"
 #include "fp4.h"
 #include "kvcache.h"
+#include "launch_limit.h"
 #include "mx4.h"
 
 using namespace i8mp;

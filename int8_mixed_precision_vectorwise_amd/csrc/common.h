@@ -28,11 +28,6 @@ constexpr int kMaxRowBlocks = 8;      // partial bitmaps written by the detect p
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
-// Workgroups of 256 that a launch of the cache's moves and of the microscaled quantization has at most, times two at
-// most where queries turn beside: 2^22 (api.hip), for a grid holds fewer than 2^32 lanes.  Larger calls are cut into
-// launches.  No part of the interface and not const only so that tests can cut small calls.
-extern "C" int64_t i8mp_launch_blocks;
-
 // Scratch of the quantizer: kMaxRowBlocks partial outlier bitmaps of
 // ceil(k/32) words each.
 inline size_t quant_scratch_bytes(int64_t k) {

@@ -14,6 +14,7 @@
 // in 62 us (5.5 TB/s) and read in 53 (6.4 TB/s); with a lane for 8 dims of one token and
 // V in 2-byte accesses both took 251 us.  A few tokens are a launch: 3.7 us.
 #include "kvcache.h"
+#include "launch_limit.h"
 #include "quant_util.h"
 
 namespace i8mp {

@@ -13,6 +13,7 @@
 // element in, 17/32 of a byte out, and memory bounds them.  4096 x 22016 bfloat16: by
 // rows 37 us (6.1 TB/s), by columns 37.5, back 34 (6.7 TB/s); one row of 5120 2.2 and 2.0.
 #include "common.h"
+#include "launch_limit.h"
 #include "mx4.h"
 #include "mx4_util.h"
 #include "quant_util.h"
