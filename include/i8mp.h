@@ -582,7 +582,7 @@ typedef struct i8mp_mx4 {
     uint8_t* codes;   /* device, 16-byte aligned                          */
     uint8_t* scales;  /* device, 4-byte aligned                           */
     int64_t rows;     /* >= 0, <= I8MP_MX4_MAX_ROWS                       */
-    int64_t k;        /* >= 0                                             */
+    int64_t k;        /* >= 0, <= 2 I8MP_MAX_LD                           */
     int64_t ldc;      /* bytes: >= kp / 2, a multiple of 16, <= I8MP_MAX_LD */
     int64_t lds;      /* bytes: >= kp / 32, a multiple of 4, <= I8MP_MAX_LD */
 } i8mp_mx4;

@@ -344,6 +344,7 @@ __device__ inline int64_t row_of(const KvAppendArgs& a, int64_t token) {
 
 // Heads of q that a lane turns by one token's angles.  Four, with their conversions to 64 bits, take 140 registers and
 // leave a SIMD three waves; with two, four fit: 16381 tokens of 32 / 32 heads of 128 appended in 141 us, with four in 150.
+// (bfloat16 heads of 256 keep 12 bytes a lane in scratch for it.)
 constexpr int kTurnHeads = 2;
 
 // q: a lane has two 8-dim pieces of kTurnHeads heads of a token, those that turn into each other, so that q may
@@ -428,7 +429,9 @@ __global__ __launch_bounds__(kThreads, 4) void kv_append_kernel(KvAppendArgs a) 
     if (turns) {
 #pragma unroll
         for (int i = 0; i < kQuad; ++i) {
-            __builtin_amdgcn_sched_barrier(0);   // one token's angles in registers at a time
+            // one token's angles in registers at a time; so a call of few tokens waits four times for a position and
+            // then its angles (64 tokens: 6.6 us, the write without rotation 4)
+            __builtin_amdgcn_sched_barrier(0);
             if (slot[i] < 0) continue;
             const int64_t row = row_of(a, l.tok0 + i);
             const float *cos = a.cos + row * a.ldcos, *sin = a.sin + row * a.ldsin;

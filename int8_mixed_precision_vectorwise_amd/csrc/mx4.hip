@@ -416,9 +416,15 @@ hipError_t dequantize(const MxDequantArgs& args, hipStream_t stream) {
 
 }  // namespace
 
-// Rows and columns at once save a read of x, and a wave works longer on what it has read: us of a backward, at once /
-// apart: 7189 x 11008 x 1024 (4902 workgroups) 177 / 202, 5673 x 11008 x 5120 (3870) 424 / 447, 2048 x 4096 x 4096 (512)
-// 69.0 / 70.1, 512 x 4096 x 1024 (128) 21.1 / 19.8, 100 x 300 x 200 (3) 10.0 / 7.2.
+// Rows and columns at once save a read of x, and a wave works longer on what it has read.  us of a captured backward, at
+// once / apart, fp16 (bfloat16 differs by 1 %), by the workgroups that x takes:
+//    128   512 x  4096 x 1024   20.0 /  17.7         512  2048 x  4096 x 4096   61.9 /  61.9
+//    256  1024 x  4096 x 1024   25.6 /  23.1         605  1333 x  7001 x  900   54.3 /  56.4
+//    320  1000 x  5000 x  600   27.2 /  24.1         688  1024 x 11008 x 4096   112  / 114
+//    384  1536 x  4096 x 4096   54.9 /  54.2        1024  4096 x  4096 x 4096   97.8 / 100.6
+//    430   640 x 11008 x 2048   61.4 /  59.6        4902  7189 x 11008 x 1024   177  / 202
+// They cross near 512.  Where x's rows begin at odd elements a second read costs more, and at once is faster by 1 to 7 %
+// from 128 workgroups on (2048 x 2560 x 2560, rows of 2563: 38.6 / 40.7); 512 holds for those too.
 bool mx4_quantize_both(int64_t rows, int64_t cols) { return ceil_div(rows, kColRows) * ceil_div(cols, kColCols) >= 512; }
 
 hipError_t launch_mx4_quantize(const MxQuantArgs* args, int count, hipStream_t stream) {

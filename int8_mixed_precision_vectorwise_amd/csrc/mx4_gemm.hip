@@ -34,6 +34,9 @@
 // overlap.  The 16x16x128 instruction reaches 7.2 PFLOP/s alone, but its 64 accumulators
 // of four registers left the compiler no room (100 registers spilled).
 //
+// Those tiles keep 103 to 134 scalar registers in lanes of vector registers (two tiles' descriptors and the products'
+// arguments are alive at once); the smaller ones keep none.
+//
 // A tile's results pass through LDS: the bias of its columns waits in registers (read from
 // LDS beside them it cost 2 us a tile), whole tiles leave by one address and fixed steps.
 //
